@@ -7,46 +7,12 @@
 
 #include <stdint.h>
 
-#include <initializer_list>
 #include <limits>
 
+#include "kda_check.h"
 #include "kda_launch.h"
 
-namespace {
-
-struct Span {
-    uintptr_t lo = 0, hi = 0;  // [lo, hi); empty spans overlap nothing
-};
-
-Span span(const void* p, uint64_t bytes) {
-    Span s;
-    if (p && bytes) {
-        s.lo = reinterpret_cast<uintptr_t>(p);
-        s.hi = s.lo + bytes;
-    }
-    return s;
-}
-
-bool overlaps(const Span& a, const Span& b) {
-    return a.lo < a.hi && b.lo < b.hi && a.lo < b.hi && b.lo < a.hi;
-}
-
-bool overlaps_any(const Span& a, std::initializer_list<Span> others) {
-    for (const Span& b : others)
-        if (overlaps(a, b)) return true;
-    return false;
-}
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-bool valid_dtype(kda_dtype dt) { return dt == KDA_F32 || dt == KDA_BF16; }
-
-uint64_t esize(kda_dtype dt) { return dt == KDA_F32 ? 4u : 2u; }
-
-// Largest element count a single tensor may have (keeps byte sizes in range).
-constexpr uint64_t kMaxElems = (uint64_t)1 << 56;
-
-}  // namespace
+using namespace kda::check;
 
 extern "C" {
 
