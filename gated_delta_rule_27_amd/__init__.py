@@ -26,6 +26,11 @@ Functions (same names as the C entry points):
   cannot allocate: the tables live in the library's static device scratch);
 * ``kda_prologue`` and ``kda_epilogue``  the elementwise work of a KDA layer
   around the core (short convolution, Swish, norms, gates);
+* ``kda_tree_prologue``, ``kda_tree_decode``, ``kda_tree_accept`` and
+  ``kda_tree_commit``  speculative decoding with a tree of drafted tokens:
+  the layer's prologue and the KDA outputs of all nodes with the cached state
+  untouched, the accepted path and next token, and state and convolution
+  history moved along that path;
 * ``kda_chunk_fwd_workspace_size``, ``kda_status_str``, ``kda_abi_version``.
 """
 import ctypes
@@ -100,6 +105,20 @@ def lib():
         L.kda_chunk_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, i32, i64, i32, i32,
                                             i32, ctypes.c_int, vp, vp, vp, vp, vp, vp, vp, vp,
                                             vp]
+        cf = ctypes.c_float
+        L.kda_tree_prologue.restype = ctypes.c_int
+        L.kda_tree_prologue.argtypes = [vp] * 9 + [i32, i32, i32, i32, ctypes.c_int, vp, cf] + \
+            [vp] * 6
+        L.kda_tree_decode.restype = ctypes.c_int
+        L.kda_tree_decode.argtypes = [vp] * 8 + [i32, i32, i32, i32, i32, ctypes.c_int, vp, vp]
+        L.kda_tree_accept_workspace_size.restype = sz
+        L.kda_tree_accept_workspace_size.argtypes = [i32, i32, i32, ctypes.c_int]
+        L.kda_tree_accept.restype = ctypes.c_int
+        L.kda_tree_accept.argtypes = [vp] * 6 + [i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, sz,
+                                                 vp]
+        L.kda_tree_commit.restype = ctypes.c_int
+        L.kda_tree_commit.argtypes = [vp] * 7 + [i32, i32, i32, i32, i32, i32, ctypes.c_int] + \
+            [vp] * 5
         _lib = L
     return _lib
 
@@ -605,9 +624,209 @@ def kda_decode_multi(q, k, v, log_alpha, beta, S, n_tok=None, *, update_state=Tr
     return o
 
 
+MAX_TREE = 64          # KDA_MAX_TREE of include/kda.h
+MAX_VOCAB = 1 << 22    # KDA_MAX_VOCAB
+MAX_PATH = 1 << 24     # KDA_MAX_PATH
+
+
+def _need(t, name, shape, dtype, device):
+    """A tensor argument of the tree calls: shape, dtype, device, contiguous;
+    its address, or None for one that is not given."""
+    if t is None:
+        return None
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device} like the first argument (got {t.device})")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _first(t, name, dim):
+    """The argument the others are measured by: its shape, dtype and device."""
+    if not isinstance(t, _torch().Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dim() != dim:
+        raise ValueError(f"{name} must have {dim} dimensions (got {tuple(t.shape)})")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be on a ROCm device (got {t.device})")
+    _dtype_code(t)
+    return t.shape, t.dtype, t.device
+
+
+def _required(**named):
+    for name, t in named.items():
+        if t is None:
+            raise TypeError(f"{name} is required")
+
+
+def _on_device(device, fn, *args):
+    """fn(*args, stream) with `device` current: the launch then goes to the
+    device of the stream, whichever device the caller has current."""
+    cuda = _torch().cuda
+    if device.index == cuda.current_device():
+        return fn(*args, cuda.current_stream(device).cuda_stream)
+    with cuda.device(device):
+        return fn(*args, cuda.current_stream(device).cuda_stream)
+
+
+def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_node=None,
+                      conv_state=None, *, l2_eps=1e-6, out=None):
+    """kda_prologue for the nodes of drafted trees: a node convolves over
+    itself and its three nearest ancestors, then the end of the history.
+
+    xq, xk, xv, a_raw: [B, N, H, 128]; b_raw: [B, N, H] (bf16 or fp32, one
+    dtype), N <= 64; conv_w: [3, H, 128, 4] fp32; a_bias: [H, 128] fp32;
+    parent: int32 [B, N] (the node that node i continues; outside [0, i): the
+    cached state) or None (a chain); n_node: int32 [B] or None (N each);
+    conv_state: [B, 3, 3, H, 128] in the input dtype, read only, or None (zero
+    history).  Returns (q, k, v, log_alpha, beta); rows at or past n_node[b]
+    are not written (`out` may supply the five tensors)."""
+    torch = _torch()
+    _required(xq=xq, xk=xk, xv=xv, a_raw=a_raw, b_raw=b_raw, conv_w=conv_w, a_bias=a_bias)
+    shape, dt, dev = _first(xq, "xq", 4)
+    B, N, H, D = shape
+    i32, f32 = torch.int32, torch.float32
+    ins = [_need(xq, "xq", shape, dt, dev),
+           _need(xk, "xk", shape, dt, dev), _need(xv, "xv", shape, dt, dev),
+           _need(a_raw, "a_raw", shape, dt, dev), _need(b_raw, "b_raw", (B, N, H), dt, dev),
+           _need(conv_w, "conv_w", (3, H, D, 4), f32, dev),
+           _need(a_bias, "a_bias", (H, D), f32, dev),
+           _need(parent, "parent", (B, N), i32, dev), _need(n_node, "n_node", (B,), i32, dev)]
+    hist = _need(conv_state, "conv_state", (B, 3, 3, H, D), dt, dev)
+    if out is None:
+        out = tuple(torch.empty_like(xq) for _ in range(4)) + (torch.empty_like(b_raw),)
+    elif len(out) != 5:
+        raise ValueError("out must be (q, k, v, log_alpha, beta)")
+    _required(**{f"out[{i}]": t for i, t in enumerate(out)})
+    outs = [_need(t, f"out[{i}]", shape if i < 4 else (B, N, H), dt, dev)
+            for i, t in enumerate(out)]
+    _check(_on_device(dev, lib().kda_tree_prologue, *ins, B, N, H, D, _dtype_code(xq), hist,
+                      float(l2_eps), *outs))
+    return tuple(out)
+
+
+def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=None):
+    """The KDA outputs of the nodes of drafted trees from one read of the
+    cached states, which are not written: o[b, i] is what node i's tokens
+    from the root on would read after their steps from S[b].
+
+    q, k, log_alpha, v: [B, N, H, 128]; beta: [B, N, H] (bf16 or fp32, one
+    dtype), N <= 64; S: [B, H, 128, 128] fp32; parent, n_node as for
+    kda_tree_prologue.  Returns o [B, N, H, 128] in the input dtype; rows at
+    or past n_node[b] are not written."""
+    torch = _torch()
+    _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, S=S)
+    shape, dt, dev = _first(q, "q", 4)
+    B, N, H, D = shape
+    ins = [_need(q, "q", shape, dt, dev), _need(k, "k", shape, dt, dev),
+           _need(v, "v", shape, dt, dev), _need(log_alpha, "log_alpha", shape, dt, dev),
+           _need(beta, "beta", (B, N, H), dt, dev),
+           _need(S, "S", (B, H, D, D), torch.float32, dev),
+           _need(parent, "parent", (B, N), torch.int32, dev),
+           _need(n_node, "n_node", (B,), torch.int32, dev)]
+    if o is None:
+        o = torch.empty_like(q)
+    _check(_on_device(dev, lib().kda_tree_decode, *ins, B, N, H, D, D, _dtype_code(q),
+                      _need(o, "o", shape, dt, dev)))
+    return o
+
+
+def kda_tree_accept_workspace_size(B, N, V, dtype=KDA_F32):
+    return lib().kda_tree_accept_workspace_size(int(B), int(N), int(V), int(dtype))
+
+
+def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_path=None,
+                    next_token=None, workspace=None):
+    """The accepted path and the next token of drafted trees (node 0 the
+    pending token, accepted by definition).
+
+    p: [B, N, V] the target's probabilities after each node; q: [B, N - 1, V]
+    the probabilities that each node's children were drawn with, or None
+    (drafts that were chosen, not drawn); both bf16 or both fp32.  tokens:
+    int32 [B, N] (tokens[:, 0] unused); u: fp32 [B, N] uniform random numbers
+    of [0, 1): u[:, i] tests node i, u[:, 0] draws the next token; parent,
+    n_node as for kda_tree_prologue.  Returns (path int32 [B, N]: accepted
+    nodes in order, then -1; n_path int32 [B]; next_token int32 [B]); the
+    emitted tokens are distributed as samples of the target.  n_path is the
+    n_tok of kda_decode_multi for a chain and the n_path of kda_tree_commit
+    for any tree."""
+    torch = _torch()
+    _required(p=p, tokens=tokens, u=u)
+    shape, dt, dev = _first(p, "p", 3)
+    B, N, V = shape
+    i32 = torch.int32
+    ins = [_need(p, "p", shape, dt, dev), _need(q, "q", (B, max(N - 1, 0), V), dt, dev),
+           _need(tokens, "tokens", (B, N), i32, dev), _need(parent, "parent", (B, N), i32, dev),
+           _need(n_node, "n_node", (B,), i32, dev), _need(u, "u", (B, N), torch.float32, dev)]
+    if path is None:
+        path = torch.empty((B, N), dtype=i32, device=dev)
+    if n_path is None:
+        n_path = torch.empty((B,), dtype=i32, device=dev)
+    if next_token is None:
+        next_token = torch.empty((B,), dtype=i32, device=dev)
+    code = _dtype_code(p)
+    if workspace is None:
+        size = lib().kda_tree_accept_workspace_size(B, N, V, code)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
+    else:
+        _dev(workspace, "workspace")
+        _same_device(dev, workspace=workspace)
+    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
+                                              workspace.numel() * workspace.element_size())
+    _check(_on_device(dev, lib().kda_tree_accept, *ins, B, N, V, code,
+                      _need(path, "path", (B, N), i32, dev),
+                      _need(n_path, "n_path", (B,), i32, dev),
+                      _need(next_token, "next_token", (B,), i32, dev), *ws))
+    return path, n_path, next_token
+
+
+def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
+    """Cached states S [B, H, 128, 128] fp32 moved in place along one path of
+    each tree: the tokens of nodes path[b, 0], path[b, 1], ... applied in
+    order, as that many kda_decode_step calls would.
+
+    k, log_alpha, v: [B, N, H, 128]; beta: [B, N, H] (bf16 or fp32, one
+    dtype); path: int32 [B, P] (a path ends before an entry outside [0, N));
+    n_path: int32 [B], entries to apply (clamped to [0, P]), or None (P each).
+    conv: None, or (xq, xk, xv, conv_state): conv_state [B, 3, 3, H, 128] is
+    moved in place to the last three of (history, inputs along the path).
+    Returns S."""
+    torch = _torch()
+    _required(k=k, v=v, log_alpha=log_alpha, beta=beta, S=S, path=path)
+    shape, dt, dev = _first(k, "k", 4)
+    B, N, H, D = shape
+    if not isinstance(path, torch.Tensor) or path.dim() != 2:
+        raise ValueError("path must be an int32 tensor [B, P]")
+    P = path.shape[1]
+    ins = [_need(k, "k", shape, dt, dev), _need(v, "v", shape, dt, dev),
+           _need(log_alpha, "log_alpha", shape, dt, dev), _need(beta, "beta", (B, N, H), dt, dev),
+           _need(S, "S", (B, H, D, D), torch.float32, dev),
+           _need(path, "path", (B, P), torch.int32, dev),
+           _need(n_path, "n_path", (B,), torch.int32, dev)]
+    if conv is None:
+        hist = [None] * 4
+    else:
+        if len(conv) != 4:
+            raise ValueError("conv must be (xq, xk, xv, conv_state)")
+        names = ("xq", "xk", "xv", "conv_state")
+        _required(**dict(zip(names, conv)))
+        hist = [_need(t, name, shape if i < 3 else (B, 3, 3, H, D), dt, dev)
+                for i, (name, t) in enumerate(zip(names, conv))]
+    _check(_on_device(dev, lib().kda_tree_commit, *ins, B, N, P, H, D, D, _dtype_code(k), *hist))
+    return S
+
+
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_step",
            "kda_decode_multi", "kda_segment_summary", "kda_segment_scan", "kda_prologue",
            "kda_epilogue", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size",
            "kda_chunk_bwd_noalloc", "BWD_NOALLOC_MAX_BYTES",
            "kda_chunk_fwd_workspace_size", "kda_status_str", "kda_abi_version", "KDAError",
-           "lib", "LIB_PATH"]
+           "kda_tree_prologue", "kda_tree_decode", "kda_tree_accept",
+           "kda_tree_accept_workspace_size", "kda_tree_commit", "MAX_TREE", "MAX_VOCAB",
+           "MAX_PATH", "lib", "LIB_PATH"]

@@ -19,7 +19,8 @@ BUILD_DIR = os.path.join(HERE, "_build")
 SOURCES = ["kda_api.cpp", "kda_chunk.hip", "kda_chunk_ws2.hip", "kda_chunk_ws2_s2.hip", "kda_chunk_ws3.hip",
            "kda_decode.hip", "kda_decode_multi.hip",
            "kda_segment.hip", "kda_layer.hip", "kda_bwd.hip",
-           "kda_bwd_ws.hip", "kda_noalloc.hip"]
+           "kda_bwd_ws.hip", "kda_noalloc.hip",
+           "kda_tree_api.cpp", "kda_tree_decode.hip", "kda_tree_accept.hip", "kda_tree_commit.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

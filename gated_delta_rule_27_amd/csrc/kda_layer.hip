@@ -27,8 +27,13 @@
 // block.  The L2 norm of a head is a DPP row sum plus a 16-lane swizzle.
 // Epilogue: persistent waves over batches of 16 (token, head) rows, one
 // 16-lane group per row, the next batch's loads in flight.
+//
+// The prologue over a tree of drafted tokens (tree_prologue_kernel) is a
+// kernel of its own: a node convolves over its ancestors, not over the rows
+// before it.
 #include "kda_device.h"
 #include "kda_launch.h"
+#include "kda_tree.h"
 
 namespace kda {
 
@@ -554,6 +559,138 @@ __global__ __launch_bounds__(256) void epilogue_kernel(EpilogueArgs a) {
     }
 }
 
+// ---- the prologue over a tree of drafted tokens ------------------------------
+// Waves as in prologue_kernel (gate waves: 4 heads; convolution waves: one
+// of q, k, v and 2 heads), each over kTreeNodes nodes of one sequence.  A
+// node's window is itself and its three nearest ancestors, then the end of
+// the cached history; its four rows are read where they lie, so a row is
+// read once from memory and up to three times more from the caches (its
+// descendants sit in the same or a neighbouring wave).  Lane i holds node
+// i's parent, so walking up is a lane read.  The arithmetic is token()'s of
+// prologue_conv, operation by operation: a chain gives its bits.
+constexpr int kTreeNodes = 8;
+
+template <typename TIn>
+__device__ __forceinline__ void tree_conv(const TreePrologueArgs& a, int64_t b, int i0, int n,
+                                          int task, int lane) {
+    const int HD = a.H * kHeadDim;
+    const int nslice = (a.H + 1) / 2;
+    const int tensor = task / nslice, slice = task % nslice;
+    const int h = 2 * slice + (lane >> 5), c4 = 4 * (lane & 31);
+    const bool live = h < a.H;
+    const int hc = live ? h * kHeadDim + c4 : c4;
+    const TIn* x = static_cast<const TIn*>(a.x[tensor]) + (size_t)b * a.N * HD;
+    TIn* out = static_cast<TIn*>(a.out[tensor]) + (size_t)b * a.N * HD;
+    const TIn* hist = a.state ? static_cast<const TIn*>(a.state) + ((size_t)b * 3 + tensor) * kHist * HD
+                              : nullptr;
+    const int par = lane < n ? tree_parent(a.parent, b, a.N, lane) : -1;
+
+    Raw4<TIn> row[kTreeNodes][kConvW];   // [..][j]: the input j steps up
+    bool zero[kTreeNodes][kConvW];       // (before the history: zero)
+#pragma unroll
+    for (int u = 0; u < kTreeNodes; ++u) {
+        int at = min(i0 + u, n - 1);
+#pragma unroll
+        for (int j = 0; j < kConvW; ++j) {
+            const TIn* src = at >= 0 ? x + (size_t)at * HD : (hist ? hist + (kHist + at) * HD : x);
+            zero[u][j] = at < 0 && !hist;
+            row[u][j].load(src + hc);
+            at = at >= 0 ? __builtin_amdgcn_readlane(par, at) : at - 1;
+        }
+    }
+    float w[kConvW][4];
+    {
+        const float* wp = a.conv_w + ((size_t)tensor * HD + hc) * kConvW;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const floatx4 t = *reinterpret_cast<const floatx4*>(wp + e * kConvW);
+#pragma unroll
+            for (int j = 0; j < kConvW; ++j) w[j][e] = t[j];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kTreeNodes; ++u) {
+        if (i0 + u >= n) break;
+        float y[4], ss = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            float in[kConvW];
+#pragma unroll
+            for (int j = 0; j < kConvW; ++j) in[j] = zero[u][j] ? 0.f : row[u][j][e];
+            const float c = __builtin_fmaf(
+                w[3][e], in[0],
+                __builtin_fmaf(w[2][e], in[1], __builtin_fmaf(w[1][e], in[2], w[0][e] * in[3])));
+            y[e] = c * sigmoid(c);
+            ss = __builtin_fmaf(y[e], y[e], ss);
+        }
+        if (tensor < 2) {
+            const float r = __builtin_amdgcn_rsqf(row32_sum(ss) + a.l2_eps);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] *= r;
+        }
+        if (live) store4(out + (size_t)(i0 + u) * HD + hc, y);
+    }
+}
+
+template <typename TIn>
+__device__ __forceinline__ void tree_gate(const TreePrologueArgs& a, int64_t b, int i0, int n,
+                                          int slice, int lane) {
+    const int HD = a.H * kHeadDim;
+    const int h = 4 * slice + (lane >> 4), c8 = 8 * (lane & 15);
+    const bool live = h < a.H;
+    const int hc = live ? h * kHeadDim + c8 : c8;
+    const size_t row0 = (size_t)b * a.N;
+    const TIn* x = static_cast<const TIn*>(a.x[3]) + row0 * HD;
+    TIn* out = static_cast<TIn*>(a.out[3]) + row0 * HD;
+    const TIn* braw = static_cast<const TIn*>(a.b_raw) + row0 * a.H;
+    TIn* beta = static_cast<TIn*>(a.beta) + row0 * a.H;
+    Raw8<TIn> xv[kTreeNodes];
+    TIn bv[kTreeNodes];
+#pragma unroll
+    for (int u = 0; u < kTreeNodes; ++u) {
+        const int i = min(i0 + u, n - 1);
+        xv[u].load(x + (size_t)i * HD + hc);
+        bv[u] = braw[(size_t)i * a.H + (live ? h : 0)];
+    }
+    float bias[8];
+    load8(a.a_bias + hc, bias);
+#pragma unroll
+    for (int u = 0; u < kTreeNodes; ++u) {
+        const int i = i0 + u;
+        if (i >= n) break;
+        float y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = -5.f * sigmoid(xv[u][e] + bias[e]);
+        if (live) {
+            store8(out + (size_t)i * HD + hc, y);
+            if (c8 == 0) beta[(size_t)i * a.H + h] = from_f32<TIn>(sigmoid(to_f32(bv[u])));
+        }
+    }
+}
+
+template <typename TIn>
+__global__ __launch_bounds__(256) void tree_prologue_kernel(TreePrologueArgs a, int64_t waves) {
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+    const int64_t wid = (int64_t)blockIdx.x * 4 + wave;
+    if (wid >= waves) return;
+    const int conv = 3 * ((a.H + 1) / 2), per = conv + (a.H + 3) / 4;
+    const int nb = (a.N + kTreeNodes - 1) / kTreeNodes;
+    const int task = (int)(wid % per);
+    const int64_t blk = wid / per, b = blk / nb;
+    const int i0 = (int)(blk % nb) * kTreeNodes;
+    const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
+    if (i0 >= n) return;
+    if (task < conv) tree_conv<TIn>(a, b, i0, n, task, lane);
+    else tree_gate<TIn>(a, b, i0, n, task - conv, lane);
+}
+
+template <typename TIn>
+hipError_t launch_tree_prologue_t(const TreePrologueArgs& a, hipStream_t stream) {
+    const int64_t waves = tree_prologue_waves(a.B, a.N, a.H);
+    tree_prologue_kernel<TIn><<<dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream>>>(a, waves);
+    return hipGetLastError();
+}
+
 template <typename TIn>
 hipError_t launch_prologue_t(const PrologueArgs& a, hipStream_t stream) {
     const int64_t gw = prologue_gate_waves(a.n_tblocks, a.H);
@@ -583,6 +720,11 @@ hipError_t launch_prologue(const PrologueArgs& a, int dtype, hipStream_t stream)
 
 hipError_t launch_epilogue(const EpilogueArgs& a, int dtype, hipStream_t stream) {
     return dtype == 0 ? launch_epilogue_t<float>(a, stream) : launch_epilogue_t<bf16>(a, stream);
+}
+
+hipError_t launch_tree_prologue(const TreePrologueArgs& a, int dtype, hipStream_t stream) {
+    return dtype == 0 ? launch_tree_prologue_t<float>(a, stream)
+                      : launch_tree_prologue_t<bf16>(a, stream);
 }
 
 }  // namespace kda

@@ -1,0 +1,92 @@
+// kda_tree.h -- internal interface between the C ABI of tree speculative
+// decoding (kda_tree_api.cpp) and its kernel launchers.  Arguments arrive
+// here already validated.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "kda_launch.h"
+
+namespace kda {
+
+constexpr int kMaxTree = 64;   // nodes of a tree: one lane, one mask bit each
+
+struct TreePrologueArgs {
+    const void* x[4];          // x_q, x_k, x_v, decay logits a: [B, N, H, 128]
+    const void* b_raw;         // [B, N, H]
+    const float* conv_w;       // [3, H, 128, 4]
+    const float* a_bias;       // [H, 128]
+    const int32_t* parent;     // [B, N] or null (chain)
+    const int32_t* n_node;     // [B] or null (N)
+    int32_t B, N, H;
+    const void* state;         // [B, 3, 3, H, 128] or null (zero history)
+    float l2_eps;
+    void* out[4];              // q, k, v, log_alpha
+    void* beta;
+};
+
+struct TreeDecodeArgs {
+    const void* q;             // [B, N, H, 128]
+    const void* k;
+    const void* v;
+    const void* log_alpha;
+    const void* beta;          // [B, N, H]
+    const float* S;            // [B, H, 128, 128]
+    const int32_t* parent;
+    const int32_t* n_node;
+    int32_t B, N, H;
+    void* o;
+};
+
+struct TreeAcceptArgs {
+    const void* p;             // [B, N, V]
+    const void* q;             // [B, N - 1, V] or null (certain drafts)
+    const int32_t* tokens;     // [B, N]
+    const int32_t* parent;
+    const int32_t* n_node;
+    const float* u;            // [B, N]
+    int32_t B, N, V;
+    int32_t* path;             // [B, N]
+    int32_t* n_path;           // [B]
+    int32_t* next_token;       // [B]
+    void* workspace;
+};
+
+struct TreeCommitArgs {
+    const void* k;             // [B, N, H, 128]
+    const void* v;
+    const void* log_alpha;
+    const void* beta;          // [B, N, H]
+    float* S;                  // [B, H, 128, 128]
+    const int32_t* path;       // [B, P]
+    const int32_t* n_path;     // [B] or null (P)
+    int32_t B, N, P, H;
+    const void* x[3];          // x_q, x_k, x_v
+    void* state;               // [B, 3, 3, H, 128] or null
+};
+
+// dtype: 0 = fp32, 1 = bf16 (kda_dtype values)
+hipError_t launch_tree_prologue(const TreePrologueArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_tree_decode(const TreeDecodeArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_tree_accept(const TreeAcceptArgs& a, int dtype, hipStream_t stream);
+hipError_t launch_tree_commit(const TreeCommitArgs& a, int dtype, hipStream_t stream);
+
+// Waves of the tree prologue: per sequence and 8 nodes, q, k, v x two-head
+// slices and the gates' four-head slices.
+inline int64_t tree_prologue_waves(int32_t B, int32_t N, int32_t H) {
+    return (int64_t)B * ((N + 7) / 8) * (3 * ((H + 1) / 2) + (H + 3) / 4);
+}
+
+// parent of node i of sequence b, -1 for the cached state
+__device__ __forceinline__ int tree_parent(const int32_t* parent, int64_t b, int N, int i) {
+    const int p = parent ? parent[b * N + i] : i - 1;
+    return p >= 0 && p < i ? p : -1;
+}
+// nodes of sequence b
+__device__ __forceinline__ int tree_count(const int32_t* n_node, int64_t b, int N) {
+    const int n = n_node ? n_node[b] : N;
+    return n < 0 ? 0 : (n > N ? N : n);
+}
+
+}  // namespace kda

@@ -1,0 +1,312 @@
+// kda_tree_accept.hip -- verification of a tree of drafted tokens: the
+// accepted path and the next token of every sequence, from the target's and
+// the drafts' probabilities and given random numbers.
+//
+// Node r's residual after some refused children is max(p - c q, 0): with
+// r_0 = p of mass Z_0 = 1 and r_{j+1} = max(r_j - Z_j q, 0) (a refusal takes
+// the draft distribution out of what is left, normalised), nested maxima
+// collapse as q >= 0, so c = Z_0 + ... + Z_j and one sum over the vocabulary
+// per refusal gives the next Z.  It is only formed when another child of r
+// is left to try; a chain never needs it.  Certain drafts (no q) need no sum
+// at all: a refusal takes p(t) out.
+//
+// The walk is a few dozen scalar decisions: lane i of every wavefront holds
+// node i's parent, token, random number and the two probabilities its test
+// reads (all fetched at once), and the wavefronts take the same decisions
+// side by side, so nothing is broadcast.  The bytes are in the last step:
+// the row that the next token is drawn from, read once for the sum of every
+// 1024-token tile (kept in LDS), and the one tile that holds the drawn
+// position again.  Sums are fp64: the drawn index is a whole number that a
+// rounding of the running sum must not move.
+#include "kda.h"
+#include "kda_device.h"
+#include "kda_tree.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kTile = 1024;          // tokens of a tile: 16 per lane of a wavefront
+constexpr int kPer = kTile / 64;
+constexpr int kMaxTiles = KDA_MAX_VOCAB / kTile;
+constexpr int kAcceptWaves = 16;
+
+__device__ __forceinline__ double lane_value(double x, int lane) {
+    union { double d; int w[2]; } v;
+    v.d = x;
+    v.w[0] = __builtin_amdgcn_readlane(v.w[0], lane);
+    v.w[1] = __builtin_amdgcn_readlane(v.w[1], lane);
+    return v.d;
+}
+__device__ __forceinline__ double wave_sum(double x) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+    return x;
+}
+// inclusive prefix sum over the lanes
+__device__ __forceinline__ double wave_scan(double x, int lane) {
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+        const double y = __shfl_up(x, off, 64);
+        if (lane >= off) x += y;
+    }
+    return x;
+}
+
+// 16 bytes of probabilities from an address that only its elements align
+// (rows of an odd vocabulary)
+template <typename T>
+__device__ __forceinline__ typename Vec16<T>::type load16(const T* p) {
+    typename Vec16<T>::type x;
+    __builtin_memcpy(&x, p, 16);
+    return x;
+}
+
+// What is left at a node: max(p - c q, 0), or p without the refused tokens
+// (lanes of `gone`).
+template <typename T, bool kQ>
+struct Residual {
+    const T* p;
+    const T* q;       // kQ; read only where c > 0
+    double c;
+    uint64_t gone;    // !kQ
+    int tok;          // this lane's token
+    int V;
+
+    __device__ __forceinline__ double weight(double pv, double qv) const {
+        const double w = kQ ? pv - c * qv : pv;
+        return w > 0.0 ? w : 0.0;   // (a NaN counts as 0)
+    }
+    // the weights of tokens v0 .. v0 + M - 1 (0 at and past V); M elements are 16 bytes
+    template <int M>
+    __device__ __forceinline__ void weights(int v0, bool with_q, double (&w)[M]) const {
+        if (v0 + M <= V) {
+            const typename Vec16<T>::type pv = load16(p + v0);
+            if (kQ && with_q) {
+                const typename Vec16<T>::type qv = load16(q + v0);
+#pragma unroll
+                for (int e = 0; e < M; ++e) w[e] = weight((double)to_f32((T)pv[e]), (double)to_f32((T)qv[e]));
+            } else {
+#pragma unroll
+                for (int e = 0; e < M; ++e) w[e] = weight((double)to_f32((T)pv[e]), 0.0);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                w[e] = 0.0;
+                if (v0 + e < V)
+                    w[e] = weight((double)to_f32(p[v0 + e]),
+                                  kQ && with_q ? (double)to_f32(q[v0 + e]) : 0.0);
+            }
+        }
+        if (!kQ) {
+            for (uint64_t g = gone; g; g &= g - 1) {
+                const int t = __builtin_amdgcn_readlane(tok, __builtin_ctzll(g));
+#pragma unroll
+                for (int e = 0; e < M; ++e)
+                    if (v0 + e == t) w[e] = 0.0;
+            }
+        }
+    }
+    // the sum of a tile's weights, in every lane
+    __device__ __forceinline__ double tile_sum(int tile, int lane) const {
+        constexpr int M = Vec16<T>::N;
+        const bool with_q = kQ && c > 0.0;
+        double s = 0.0;
+#pragma unroll
+        for (int j = 0; j < kPer / M; ++j) {
+            double w[M];
+            weights<M>(tile * kTile + j * 64 * M + lane * M, with_q, w);
+#pragma unroll
+            for (int e = 0; e < M; ++e) s += w[e];
+        }
+        return wave_sum(s);
+    }
+    // the first token of `tile` at which `base` plus the tile's running sum
+    // passes `target`; where rounding leaves none, its last one with weight
+    __device__ __forceinline__ int find(int tile, double base, double target, int lane) const {
+        constexpr int M = Vec16<T>::N;
+        const bool with_q = kQ && c > 0.0;
+        const int v0 = tile * kTile + lane * kPer;   // a lane's tokens are consecutive
+        double w[kPer], s = 0.0;
+#pragma unroll
+        for (int j = 0; j < kPer / M; ++j) {
+            double x[M];
+            weights<M>(v0 + j * M, with_q, x);
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                w[j * M + e] = x[e];
+                s += x[e];
+            }
+        }
+        const double incl = base + wave_scan(s, lane);
+        double run = __shfl_up(incl, 1, 64);
+        if (lane == 0) run = base;
+        int first = -1, last = -1;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) {
+            run += w[e];
+            if (w[e] > 0.0) {
+                last = v0 + e;
+                if (first < 0 && run > target) first = v0 + e;
+            }
+        }
+        const uint64_t hit = __ballot(first >= 0), any = __ballot(last >= 0);
+        if (hit) return __builtin_amdgcn_readlane(first, __builtin_ctzll(hit));
+        if (any) return __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(any));
+        return min(tile * kTile, V - 1);
+    }
+};
+
+template <typename T, bool kQ>
+__global__ __launch_bounds__(64 * kAcceptWaves) void tree_accept_kernel(TreeAcceptArgs a) {
+    __shared__ double tiles[kMaxTiles];
+    __shared__ double part[kAcceptWaves];
+    const int64_t b = blockIdx.x;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int N = a.N, V = a.V, ntile = (V + kTile - 1) / kTile;
+    const int n = tree_count(a.n_node, b, N);
+    int32_t* path = a.path + b * N;
+    if (n == 0) {
+        if (wave == 0) {
+            if (lane < N) path[lane] = -1;
+            if (lane == 0) {
+                a.n_path[b] = 0;
+                a.next_token[b] = -1;
+            }
+        }
+        return;
+    }
+
+    // node i in lane i
+    const bool node = lane >= 1 && lane < n;
+    const int par = node ? tree_parent(a.parent, b, N, lane) : -1;
+    const int tok = node ? a.tokens[b * N + lane] : -1;
+    const double u = lane < n ? (double)a.u[b * N + lane] : 0.0;
+    const bool sound = par >= 0 && tok >= 0 && tok < V;
+    const T* P = static_cast<const T*>(a.p) + (size_t)b * N * V;
+    const T* Q = kQ ? static_cast<const T*>(a.q) + (size_t)b * (N - 1) * V : nullptr;
+    const double pt = sound ? (double)to_f32(P[(size_t)par * V + tok]) : 0.0;
+    const double qt = kQ && sound ? (double)to_f32(Q[(size_t)par * V + tok]) : 0.0;
+    const uint64_t sound_mask = __ballot(sound);
+
+    Residual<T, kQ> res;
+    res.V = V;
+    res.tok = tok;
+    res.c = 0.0;
+    res.gone = 0;
+    auto at_node = [&](int r) {
+        res.p = P + (size_t)r * V;
+        res.q = kQ ? Q + (size_t)min(r, N - 2) * V : nullptr;
+    };
+    at_node(0);
+    int at = 0, m = 1, mine = lane == 0 ? 0 : -1;   // lane j: path[j]
+    double Z = 1.0;
+    uint64_t todo = __ballot(par == 0);
+    while (todo) {
+        const int i = __builtin_ctzll(todo);
+        todo &= todo - 1;
+        if (!((sound_mask >> i) & 1)) continue;
+        const double ui = lane_value(u, i), pi = lane_value(pt, i);
+        bool ok;
+        if (kQ) {
+            const double qi = lane_value(qt, i);
+            ok = ui * qi * Z < res.weight(pi, qi);
+            if (!ok) {
+                res.c += Z;
+                if (todo) {
+                    double s = 0.0;
+                    for (int t = wave; t < ntile; t += kAcceptWaves) s += res.tile_sum(t, lane);
+                    __syncthreads();   // (part of the sum before is read)
+                    if (lane == 0) part[wave] = s;
+                    __syncthreads();
+                    Z = 0.0;
+#pragma unroll
+                    for (int w = 0; w < kAcceptWaves; ++w) Z += part[w];
+                }
+            }
+        } else {
+            const int ti = __builtin_amdgcn_readlane(tok, i);
+            const bool again = (__ballot(tok == ti) & res.gone) != 0;
+            const double w = again ? 0.0 : res.weight(pi, 0.0);
+            ok = ui * Z < w;
+            if (!ok) {
+                res.gone |= (uint64_t)1 << i;
+                Z -= w;
+            }
+        }
+        if (ok) {
+            at = i;
+            if (lane == m) mine = i;
+            ++m;
+            at_node(at);
+            res.c = 0.0;
+            res.gone = 0;
+            Z = 1.0;
+            todo = __ballot(par == at);
+        }
+    }
+    if (wave == 0) {
+        if (lane < N) path[lane] = mine;
+        if (lane == 0) a.n_path[b] = m;
+    }
+
+    // the next token: from the residual, or from p where nothing is left
+    for (int again = 0; again < 2; ++again) {
+        for (int t = wave; t < ntile; t += kAcceptWaves) {
+            const double s = res.tile_sum(t, lane);
+            if (lane == 0) tiles[t] = s;
+        }
+        __syncthreads();
+        // every wavefront: the running sum over the tiles
+        double total = 0.0;
+        for (int t0 = 0; t0 < ntile; t0 += 64)
+            total += wave_sum(t0 + lane < ntile ? tiles[t0 + lane] : 0.0);
+        if (total > 0.0 || again) {
+            if (wave == 0) {
+                const double target = lane_value(u, 0) * total;
+                int tile = -1, filled = -1;   // the tile that passes the target; the last with weight
+                double base = 0.0, run = 0.0;
+                for (int t0 = 0; t0 < ntile && tile < 0; t0 += 64) {
+                    const double s = t0 + lane < ntile ? tiles[t0 + lane] : 0.0;
+                    const double incl = run + wave_scan(s, lane);
+                    const uint64_t hit = __ballot(s > 0.0 && incl > target), any = __ballot(s > 0.0);
+                    if (any) filled = t0 + 63 - __builtin_clzll(any);
+                    if (hit) {
+                        const int l = __builtin_ctzll(hit);
+                        tile = t0 + l;
+                        base = l ? lane_value(incl, l - 1) : run;
+                    }
+                    run = lane_value(incl, 63);
+                }
+                if (tile < 0) {   // (the target rounded past the end: the last token with weight)
+                    tile = max(filled, 0);
+                    base = -1e300;
+                }
+                const int next = res.find(tile, base, target, lane);
+                if (lane == 0) a.next_token[b] = next;
+            }
+            break;
+        }
+        __syncthreads();
+        res.c = 0.0;
+        res.gone = 0;
+    }
+}
+
+template <typename T>
+hipError_t launch_tree_accept_t(const TreeAcceptArgs& a, hipStream_t stream) {
+    const dim3 grid((unsigned)a.B), block(64 * kAcceptWaves);
+    if (a.q) tree_accept_kernel<T, true><<<grid, block, 0, stream>>>(a);
+    else tree_accept_kernel<T, false><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_tree_accept(const TreeAcceptArgs& a, int dtype, hipStream_t stream) {
+    return dtype == 0 ? launch_tree_accept_t<float>(a, stream) : launch_tree_accept_t<bf16>(a, stream);
+}
+
+}  // namespace kda

@@ -377,6 +377,157 @@ kda_status kda_decode_multi(const void* q, const void* k, const void* v,
                             int32_t Dk, int32_t Dv, kda_dtype dt,
                             int32_t update_state, void* o, hipStream_t stream);
 
+/*
+ * Speculative decoding with a tree of drafted tokens.  The tokens of one
+ * serving step are a tree of N nodes per sequence over its cached state:
+ * node 0 is the pending token (sampled, not yet in the state), every other
+ * node continues an earlier one.  A step of a layer is kda_tree_prologue ->
+ * kda_tree_decode -> kda_epilogue over all nodes at once, with state and
+ * convolution history left as they are; kda_tree_accept then chooses one
+ * path from the target's probabilities, and kda_tree_commit moves state and
+ * history of every layer along that path alone ("From GPT-2 to Kimi K3",
+ * "Speculative decoding cannot naively roll KDA back").  A chain of drafts
+ * is the tree with parent = NULL.
+ *
+ *   parent : [B, N] int32 device, parent[b][i] the node that node i
+ *            continues; any value outside [0, i) makes node i a
+ *            continuation of the cached state itself (-1 by custom).
+ *            NULL = a chain (node i continues node i - 1).
+ *   n_node : [B] int32 device, nodes of each sequence, clamped to [0, N] by
+ *            the kernels; NULL = N for every sequence.  Nodes at or past it
+ *            take no part and their output rows are not written.
+ *   1 <= N <= KDA_MAX_TREE.  B == 0 is allowed (nothing is launched).
+ */
+#define KDA_MAX_TREE 64
+
+/*
+ * The prologue of a KDA layer (kda_prologue) for the nodes of a tree: node i
+ * convolves over itself and its three nearest ancestors, and where it has
+ * fewer, over the end of the cached history.  For a chain the outputs are
+ * the bits of kda_prologue on the same tokens.
+ *
+ *   xq, xk, xv, a_raw, q, k, v, log_alpha : [B, N, H, D]  dt
+ *   b_raw, beta                           : [B, N, H]     dt
+ *   conv_w : [3, H, D, 4] fp32;  a_bias : [H, D] fp32
+ *   conv_state : [B, 3 (q, k, v), 3 (tokens), H, D] dt, read only; NULL =
+ *                zero history
+ * Errors, alignment and l2_eps as kda_prologue (parent, n_node: 4-byte
+ * aligned; N out of range is KDA_ERR_BAD_SHAPE).
+ */
+kda_status kda_tree_prologue(const void* xq, const void* xk, const void* xv,
+                             const void* a_raw, const void* b_raw,
+                             const float* conv_w, const float* a_bias,
+                             const int32_t* parent, const int32_t* n_node,
+                             int32_t B, int32_t N, int32_t H, int32_t D,
+                             kda_dtype dt, const void* conv_state, float l2_eps,
+                             void* q, void* k, void* v, void* log_alpha,
+                             void* beta, hipStream_t stream);
+
+/*
+ * The KDA outputs of every node of a tree from one read of the cached state,
+ * which is not written: with S_i = (I - beta_i k_i k_i^T) Diag(alpha_i)
+ * S_parent(i) + beta_i k_i v_i^T, o_i = S_i^T q_i.  Node i gives what
+ * kda_decode_multi would on the path from the root to i, to rounding.  A NaN
+ * or infinity among node i's inputs makes outputs NaN of i and of the nodes
+ * that descend from it, of no other node.
+ *
+ *   q, k, log_alpha : [B, N, H, Dk]  dt
+ *   v               : [B, N, H, Dv]  dt
+ *   beta            : [B, N, H]      dt
+ *   S               : [B, H, Dk, Dv] fp32, read only
+ *   o               : [B, N, H, Dv]  dt
+ * Alignment and errors as kda_decode_multi (o overlapping S, parent, n_node
+ * or an input is KDA_ERR_ALIAS).
+ */
+kda_status kda_tree_decode(const void* q, const void* k, const void* v,
+                           const void* log_alpha, const void* beta,
+                           const float* S, const int32_t* parent,
+                           const int32_t* n_node, int32_t B, int32_t N,
+                           int32_t H, int32_t Dk, int32_t Dv, kda_dtype dt,
+                           void* o, hipStream_t stream);
+
+/*
+ * Verification of the drafted tokens against the target's probabilities:
+ * the accepted path and the next token of every sequence.  The walk starts
+ * at node 0.  At node r, with p the target's distribution after r and q the
+ * draft distribution that r's children were drawn from, c = 0 and Z = 1 on
+ * arrival, r's children x (token t, random number u_x) are tried in
+ * ascending order:
+ *     w = max(p(t) - c q(t), 0);  x is accepted iff  u_x q(t) Z < w;
+ *     refused: c <- c + Z,  Z <- sum over v of max(p(v) - c q(v), 0).
+ * Without q the drafts are certain (chosen, not drawn): w = p(t), 0 for a
+ * token refused here before, x is accepted iff u_x Z < w, and a refusal
+ * takes p(t) out: Z <- Z - w.  An accepted child is the next r; where no
+ * child is accepted, the next token is drawn from what is left at r,
+ *     w(v) = max(p(v) - c q(v), 0)   (without q: p without refused tokens),
+ * as the smallest v with  sum of w over 0..v  >  u_0 * (sum of w)  (from p
+ * itself where w has no mass left).  The tokens so emitted are distributed
+ * as the target's own samples.  Sums and comparisons are in fp64.
+ *
+ *   p      : [B, N, V] dt, row i the target's distribution after node i
+ *   q      : [B, N - 1, V] dt, row i the draft distribution of node i's
+ *            children (the last node can have none); NULL = certain drafts
+ *   tokens : [B, N] int32, the drafted tokens (tokens[b][0] is not read); a
+ *            token outside [0, V) is refused and changes nothing else
+ *   u      : [B, N] fp32 in [0, 1): u[b][i] tests node i >= 1, u[b][0]
+ *            draws the next token
+ *   path   : [B, N] int32 output, the accepted nodes in order (path[b][0] =
+ *            0), then -1
+ *   n_path : [B] int32 output, accepted nodes (>= 1; 0 for a sequence
+ *            without nodes): n_tok of kda_decode_multi for a chain, n_path
+ *            of kda_tree_commit
+ *   next_token : [B] int32 output (-1 for a sequence without nodes)
+ * A node whose parent lies outside [0, i) is never reached.  p and q are
+ * probabilities: finite, >= 0, rows summing to 1 up to rounding (not
+ * checked; a NaN or negative weight counts as 0, nothing out of range is
+ * ever read or written, and the next token lies in [0, V)).
+ * 1 <= V <= KDA_MAX_VOCAB.  p and q 16-byte aligned, the int32 and fp32
+ * arrays 4-byte aligned.  The workspace (kda_tree_accept_workspace_size
+ * bytes, 16-byte aligned; may be NULL when that is 0) need not be cleared;
+ * calls that overlap in time need one each.  Any overlap of an output or
+ * the workspace with another buffer is KDA_ERR_ALIAS.
+ */
+#define KDA_MAX_VOCAB (1 << 22)
+
+size_t kda_tree_accept_workspace_size(int32_t B, int32_t N, int32_t V,
+                                      kda_dtype dt);
+
+kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
+                           const int32_t* parent, const int32_t* n_node,
+                           const float* u, int32_t B, int32_t N, int32_t V,
+                           kda_dtype dt, int32_t* path, int32_t* n_path,
+                           int32_t* next_token, void* workspace,
+                           size_t workspace_bytes, hipStream_t stream);
+
+/*
+ * Moves cached states, and convolution histories, along one path of each
+ * tree: the tokens of the nodes path[b][0], path[b][1], ... are applied in
+ * that order, as kda_decode_step would one after the other.
+ *
+ *   k, log_alpha : [B, N, H, Dk]  dt  (N >= 1 nodes, here without a limit)
+ *   v            : [B, N, H, Dv]  dt
+ *   beta         : [B, N, H]      dt
+ *   S            : [B, H, Dk, Dv] fp32, updated IN PLACE
+ *   path         : [B, P] int32; a path ends before an entry outside [0, N)
+ *   n_path       : [B] int32, entries to apply, clamped to [0, P]; NULL = P
+ *   xq, xk, xv   : [B, N, H, Dk]  dt, the inputs of the convolution
+ *   conv_state   : [B, 3 (q, k, v), 3 (tokens), H, Dk] dt, updated IN PLACE
+ *                  to the last three of (history, inputs along the path);
+ *                  NULL = not kept (xq, xk, xv are then not read)
+ * A sequence whose path is empty keeps its state and history untouched.
+ * 1 <= P <= KDA_MAX_PATH.  Alignment and errors as kda_decode_multi; S or conv_state
+ * overlapping another buffer is KDA_ERR_ALIAS.
+ */
+#define KDA_MAX_PATH (1 << 24)
+
+kda_status kda_tree_commit(const void* k, const void* v, const void* log_alpha,
+                           const void* beta, float* S, const int32_t* path,
+                           const int32_t* n_path, int32_t B, int32_t N,
+                           int32_t P, int32_t H, int32_t Dk, int32_t Dv,
+                           kda_dtype dt, const void* xq, const void* xk,
+                           const void* xv, void* conv_state,
+                           hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* kda_status_str(kda_status s);
 
