@@ -23,10 +23,14 @@
 // node) and v (per column) are therefore taken as 0 and remembered as bits,
 // and the outputs of the nodes that descend from them are set to NaN.
 //
-// Mapping.  One workgroup of four wavefronts per (sequence, head); wavefront
-// w owns value columns 32 w .. 32 w + 31 (lane: columns 2 (l % 16), +1) over
-// all 128 state rows, so everything after the Gram tiles (pseudo-values,
-// solve, outputs) stays in its own accumulators.
+// Mapping.  One workgroup of four wavefronts per (sequence, head).  Before
+// the product with the state wavefront w owns key channels 32 w .. 32 w + 31
+// of all nodes: G^T comes out of its MFMA with a lane holding 4 channels of
+// one node, the layout in which k and q are loaded and the scaled rows leave
+// for LDS, so none of it needs another wavefront.  From the state product on
+// it owns value columns 32 w .. 32 w + 31 (lane: columns 2 (l % 16), +1) over
+// all 128 state rows, and pseudo-values, solve and outputs stay in its own
+// accumulators.  All loads, the state's included, are issued at the start.
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_tree.h"
@@ -53,11 +57,13 @@ struct Rows<float> {
     static constexpr int kBytes = kFP * 4;   // of a row
     float* p;
     __device__ __forceinline__ Rows(unsigned char* base, int) : p(reinterpret_cast<float*>(base)) {}
-    __device__ __forceinline__ void put8(int row, int c, const float (&x)[8]) const {
-        float* d = p + row * kFP + c;
-        *reinterpret_cast<floatx4*>(d) = floatx4{x[0], x[1], x[2], x[3]};
-        *reinterpret_cast<floatx4*>(d + 4) = floatx4{x[4], x[5], x[6], x[7]};
+    __device__ __forceinline__ void put4(int row, int c, floatx4 x) const {
+        *reinterpret_cast<floatx4*>(p + row * kFP + c) = x;
     }
+    __device__ __forceinline__ float get(int row, int c) const { return p[row * kFP + c]; }
+    // fp32 values kept whole in the place of a row's elements
+    __device__ __forceinline__ void put4_f32(int row, int c, floatx4 x) const { put4(row, c, x); }
+    __device__ __forceinline__ float get_f32(int row, int c) const { return get(row, c); }
 };
 template <>
 struct Rows<bf16> {
@@ -66,33 +72,53 @@ struct Rows<bf16> {
     bf16* lo;
     __device__ __forceinline__ Rows(unsigned char* base, int rows)
         : hi(reinterpret_cast<bf16*>(base)), lo(hi + rows * kBP) {}
-    __device__ __forceinline__ void put8(int row, int c, const float (&x)[8]) const {
-        bf16x8 h, l;
+    __device__ __forceinline__ void put4(int row, int c, floatx4 x) const {
+        bf16x4 h, l;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 4; ++e) {
             h[e] = (bf16)x[e];
             l[e] = (bf16)(x[e] - (float)h[e]);
         }
-        *reinterpret_cast<bf16x8*>(hi + row * kBP + c) = h;
-        *reinterpret_cast<bf16x8*>(lo + row * kBP + c) = l;
+        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = h;
+        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = l;
+    }
+    __device__ __forceinline__ float get(int row, int c) const {
+        return (float)hi[row * kBP + c] + (float)lo[row * kBP + c];
+    }
+    // fp32 values kept whole in the place of a row's elements: upper half in hi, lower half in lo
+    __device__ __forceinline__ void put4_f32(int row, int c, floatx4 x) const {
+        shortx4 h, l;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t u = __builtin_bit_cast(uint32_t, (float)x[e]);
+            h[e] = (short)(u >> 16);
+            l[e] = (short)u;
+        }
+        *reinterpret_cast<shortx4*>(hi + row * kBP + c) = h;
+        *reinterpret_cast<shortx4*>(lo + row * kBP + c) = l;
+    }
+    __device__ __forceinline__ float get_f32(int row, int c) const {
+        const uint32_t h = *reinterpret_cast<const uint16_t*>(hi + row * kBP + c);
+        const uint32_t l = *reinterpret_cast<const uint16_t*>(lo + row * kBP + c);
+        return __builtin_bit_cast(float, h << 16 | l);
     }
 };
 
-// acc += (rows a0 .. a0 + 15 of A) (rows b0 .. b0 + 15 of B)^T over 128 channels
+// (rows a0 .. a0 + 15 of A) (rows b0 .. b0 + 15 of B)^T over channels c0 .. c1 - 1
 __device__ __forceinline__ floatx4 gram(const Rows<float>& A, int a0, const Rows<float>& B, int b0,
-                                        int l16, int g) {
+                                        int c0, int c1, int l16, int g) {
     floatx4 acc = zero4();
 #pragma unroll
-    for (int kb = 0; kb < kHeadDim; kb += 16)
+    for (int kb = c0; kb < c1; kb += 16)
         acc = mma_f32_k16(frag_k16(A.p + (a0 + l16) * kFP, kb, g), frag_k16(B.p + (b0 + l16) * kFP, kb, g),
                           acc);
     return acc;
 }
 __device__ __forceinline__ floatx4 gram(const Rows<bf16>& A, int a0, const Rows<bf16>& B, int b0,
-                                        int l16, int g) {
+                                        int c0, int c1, int l16, int g) {
     floatx4 acc = zero4();
 #pragma unroll
-    for (int kb = 0; kb < kHeadDim; kb += 32) {
+    for (int kb = c0; kb < c1; kb += 32) {
         const bf16x8 ah = frag_k32(A.hi + (a0 + l16) * kBP, kb, g), al = frag_k32(A.lo + (a0 + l16) * kBP, kb, g);
         const bf16x8 bh = frag_k32(B.hi + (b0 + l16) * kBP, kb, g), bl = frag_k32(B.lo + (b0 + l16) * kBP, kb, g);
         acc = mma_bf16_k32(al, bh, acc);
@@ -150,19 +176,6 @@ __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const
     }
 }
 
-__device__ __forceinline__ void row8(const bf16* p, float (&x)[8]) {
-    const bf16x8 a = *reinterpret_cast<const bf16x8*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = (float)a[e];
-}
-__device__ __forceinline__ void row8(const float* p, float (&x)[8]) {
-    const floatx4 a = *reinterpret_cast<const floatx4*>(p), b = *reinterpret_cast<const floatx4*>(p + 4);
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        x[e] = a[e];
-        x[4 + e] = b[e];
-    }
-}
 __device__ __forceinline__ floatx2 pair(const bf16* p) {
     const bf16x2 a = *reinterpret_cast<const bf16x2*>(p);
     return floatx2{(float)a[0], (float)a[1]};
@@ -175,20 +188,68 @@ __device__ __forceinline__ void put_pair(float* p, float x, float y) {
     *reinterpret_cast<floatx2*>(p) = floatx2{x, y};
 }
 
+// 4 consecutive channels as loaded
+__device__ __forceinline__ bf16x4 load4(const bf16* p) { return *reinterpret_cast<const bf16x4*>(p); }
+__device__ __forceinline__ floatx4 load4(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
+__device__ __forceinline__ floatx4 widen(bf16x4 x) {
+    return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
+}
+__device__ __forceinline__ floatx4 widen(floatx4 x) { return x; }
+template <typename T>
+struct Four;
+template <>
+struct Four<bf16> { typedef bf16x4 type; };
+template <>
+struct Four<float> { typedef floatx4 type; };
+
+// G^T of 16 nodes (columns) and 16 channels: log alpha^T (a: channel l16,
+// nodes 16 J + 4 g + 0..3) times the ancestor bits of node l16
+template <int NT>
+__device__ __forceinline__ floatx4 gather_decay(const floatx4 (&a)[NT], uint64_t m, int I, int g) {
+    floatx4 acc = zero4();
+#pragma unroll
+    for (int J = 0; J < NT; ++J) {
+        if (J > I) break;
+        const uint32_t bits = (uint32_t)(m >> (16 * J + 4 * g));
+        acc = mma_f32_k16(a[J], floatx4{(bits & 1) ? 1.f : 0.f, (bits & 2) ? 1.f : 0.f,
+                                        (bits & 4) ? 1.f : 0.f, (bits & 8) ? 1.f : 0.f}, acc);
+    }
+    return acc;
+}
+// (bf16 log alpha times 0 or 1 is exact)
+template <int NT>
+__device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], uint64_t m, int I, int g) {
+    floatx4 acc = zero4();
+#pragma unroll
+    for (int J = 0; J < NT; J += 2) {
+        if (J > I) break;
+        bf16x8 x, y;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int jj = J + (e >> 2);
+            x[e] = jj < NT ? a[jj < NT ? jj : 0][e & 3] : (bf16)0.f;
+            y[e] = jj < NT && ((m >> (16 * jj + 4 * g + (e & 3))) & 1) ? (bf16)1.f : (bf16)0.f;
+        }
+        acc = mma_bf16_k32(x, y, acc);
+    }
+    return acc;
+}
+
+// e^x: for bf16 results the hardware's 2^x (x log2 e rounds to |x| 2^-24, at
+// |x| <= 64 some 2^-18 of the result), for fp32 the library's
+template <typename T>
+__device__ __forceinline__ float exp_t(float x) { return __expf(x); }
+template <>
+__device__ __forceinline__ float exp_t<float>(float x) { return expf(x); }
+
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
-// non-finite elements become 0; whether there was one
-__device__ __forceinline__ bool drop_nonfinite(float (&x)[8]) {
+// whether one of four is not finite
+template <typename V>
+__device__ __forceinline__ bool unsound(V x) {
     float s = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(x[e], 0.f, s);   // 0, or NaN
-    if (s == 0.f) return false;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = finite_or_0(x[e]);
-    return true;
-}
-// whether any of this lane's row of 16 lanes says so
-__device__ __forceinline__ bool any_of_row(bool x, int lane) {
-    return ((__ballot(x) >> (lane & 48)) & 0xffff) != 0;
+    for (int e = 0; e < 4; ++e) s = __builtin_fmaf((float)x[e], 0.f, s);   // 0, or NaN
+    return s != 0.f;
 }
 
 // LDS of a workgroup for up to 16 NT nodes
@@ -197,22 +258,23 @@ struct TreeLds {
     static constexpr int kN = 16 * NT;
     static constexpr int kLP = kN + 4;                        // a row of a Gram matrix
     static constexpr int kRowsB = kN * Rows<T>::kBytes;       // an operand array
-    static constexpr int kGramB = 2 * kN * kLP * 4;           // both Gram matrices
-    static constexpr int kGB = kN * kFP * 4;                  // G
     static constexpr int kXk = 0, kXq = kRowsB;
-    static constexpr int kY = 2 * kRowsB;                     // log alpha, then Y or the Gram matrices
-    static constexpr int kG = kY + (kRowsB > kGramB ? kRowsB : kGramB);   // G, then the Gram matrices
-    static constexpr int kInv = kG + (kGramB > kGB ? kGramB : kGB);
-    static constexpr int kBeta = kInv + NT * 16 * 20 * 4;
+    static constexpr int kY = 2 * kRowsB;                     // Y; for channels out of range G itself
+    static constexpr int kGram = 3 * kRowsB;                  // both Gram matrices
+    static constexpr int kInv = kGram + 2 * kN * kLP * 4;     // inverse diagonal blocks
+    // NT = 1: the wavefronts' parts of both Gram tiles
+    static constexpr int kPart = kInv + NT * 16 * 20 * 4;
+    static constexpr int kBeta = kPart + (NT == 1 ? 4 * 2 * 16 * 20 * 4 : 0);
     static constexpr int kAnc = kBeta + kN * 4;
-    static constexpr int kBad = kAnc + kN * 8;                // non-finite log alpha, k, beta of a node
-    static constexpr int kFlag = kBad + 3 * kN * 4;
+    static constexpr int kBad = kAnc + kN * 8;                // per wavefront: nodes with non-finite inputs
+    static constexpr int kFlag = kBad + 4 * 8;                // per wavefront: channels out of range
     static constexpr int kBytes = kFlag + 16;
 };
 
 template <typename T, int NT>
-__global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
+__global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_decode_kernel(TreeDecodeArgs a) {
     using L = TreeLds<T, NT>;
+    typedef typename Four<T>::type four;
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -234,122 +296,160 @@ __global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
     const float* S = a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim) + (size_t)(4 * g) * kHeadDim + c0;
 
     const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN), Y(lds + L::kY, L::kN);
-    float* stage = reinterpret_cast<float*>(lds + L::kY);     // log alpha, then Y
-    float* G = reinterpret_cast<float*>(lds + L::kG);
+    float* gkk = reinterpret_cast<float*>(lds + L::kGram);
+    float* gqk = gkk + L::kN * L::kLP;
     float* inv = reinterpret_cast<float*>(lds + L::kInv);
+    float* part = reinterpret_cast<float*>(lds + L::kPart);
     float* sbeta = reinterpret_cast<float*>(lds + L::kBeta);
     uint64_t* anc = reinterpret_cast<uint64_t*>(lds + L::kAnc);
-    int* bad = reinterpret_cast<int*>(lds + L::kBad);
+    uint64_t* bad = reinterpret_cast<uint64_t*>(lds + L::kBad);
     int* flag = reinterpret_cast<int*>(lds + L::kFlag);
 
-    // ---- node rows: thread = (row, 8 channels), 16 rows a pass --------------
-    const int r16 = tid >> 4, c8 = 8 * (tid & 15);
+    // ---- everything this workgroup reads, in the order it is needed ---------
+    // (rows past the nodes repeat the last one and are replaced by 0 where they are used)
+    int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
+    four lar[2][NT], kr[NT][2], qr[NT][2];
 #pragma unroll
-    for (int I = 0; I < NT; ++I) {
-        if (I >= nt) break;
-        const int i = 16 * I + r16;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (i < n) row8(la + i * HD + c8, x);
-        const bool unsound = drop_nonfinite(x);
-        const bool any = any_of_row(unsound, lane);
-        if (l16 == 0) bad[i] = any;
-        float* d = stage + i * kFP + c8;
-        *reinterpret_cast<floatx4*>(d) = floatx4{x[0], x[1], x[2], x[3]};
-        *reinterpret_cast<floatx4*>(d + 4) = floatx4{x[4], x[5], x[6], x[7]};
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int J = 0; J < NT; ++J)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                lar[t][J][e] = la[min(16 * J + 4 * g + e, n - 1) * HD + 32 * w + 16 * t + l16];
+#pragma unroll
+    for (int I = 0; I < NT; ++I)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const size_t off = min(16 * I + l16, n - 1) * HD + 32 * w + 16 * t + 4 * g;
+            kr[I][t] = load4(k + off);
+            qr[I][t] = load4(q + off);
+        }
+    float bt = to_f32(beta[(size_t)min(lane, n - 1) * H]);
+    floatx2 vv[NT][4];
+#pragma unroll
+    for (int I = 0; I < NT; ++I)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vv[I][e] = pair(v + min(16 * I + 4 * g + e, n - 1) * HD + c0);
+    floatx2 st[4][8];
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            st[kb][e] = __builtin_nontemporal_load(
+                reinterpret_cast<const floatx2*>(S + (32 * kb + 16 * (e >> 2) + (e & 3)) * kHeadDim));
+    __builtin_amdgcn_sched_barrier(0);
+
+    // ---- ancestor masks, lane = node, by doubling: a lane joins the mask of the node it points at, then
+    // points where that node points
+    uint64_t mask = (uint64_t)1 << lane;
+    while (__ballot(par >= 0)) {
+        const uint64_t pm = __shfl(mask, par < 0 ? lane : par, 64);
+        const int pp = __shfl(par, par < 0 ? lane : par, 64);
+        if (par >= 0) {
+            mask |= pm;
+            par = pp;
+        }
     }
-    if (w == 0) {
-        // ancestor masks by doubling: a lane joins the mask of the node it points at, then points where
-        // that node points
-        int p = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
-        uint64_t m = (uint64_t)1 << lane;
-        while (__ballot(p >= 0)) {
-            const uint64_t pm = __shfl(m, p < 0 ? lane : p, 64);
-            const int pp = __shfl(p, p < 0 ? lane : p, 64);
-            if (p >= 0) {
-                m |= pm;
-                p = pp;
+
+    // ---- G^T, scaled rows: this wavefront's 32 channels ----------------------
+    uint64_t bad_node = __ballot(lane < n && !(bt - bt == 0.f));   // non-finite beta, log alpha, k
+    if (w == 0 && lane < L::kN) {
+        anc[lane] = mask;
+        sbeta[lane] = lane < n ? finite_or_0(bt) : 0.f;
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int J = 0; J < NT; ++J) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (16 * J + 4 * g + e >= n) lar[t][J][e] = (T)0.f;
+            if (__any(unsound(lar[t][J]))) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float x = (float)lar[t][J][e];
+                    const uint64_t off = __ballot(!(x - x == 0.f));   // group gg: node 16 J + 4 gg + e
+#pragma unroll
+                    for (int gg = 0; gg < 4; ++gg)
+                        if ((off >> (16 * gg)) & 0xffff) bad_node |= (uint64_t)1 << (16 * J + 4 * gg + e);
+                    if (!(x - x == 0.f)) lar[t][J][e] = (T)0.f;
+                }
             }
         }
-        if (lane < L::kN) {
-            const float bt = lane < n ? to_f32(beta[(size_t)lane * H]) : 0.f;
-            const bool sound = bt - bt == 0.f;
-            anc[lane] = m;
-            sbeta[lane] = sound ? bt : 0.f;
-            bad[2 * L::kN + lane] = !sound;
-        }
-    }
-    __syncthreads();
-
-    // ---- G = (ancestor matrix) (log alpha): this wavefront's 32 channels ----
+    floatx4 GT[NT][2];
     bool deep = false;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
-        const uint64_t m = anc[16 * I + l16];
-        floatx4 acc[2] = {zero4(), zero4()};
+        const uint64_t m = __shfl(mask, 16 * I + l16, 64);
 #pragma unroll
-        for (int J = 0; J <= I; ++J) {
-            const uint32_t bits = (uint32_t)(m >> (16 * J + 4 * g));
-            const floatx4 am = {(bits & 1) ? 1.f : 0.f, (bits & 2) ? 1.f : 0.f, (bits & 4) ? 1.f : 0.f,
-                                (bits & 8) ? 1.f : 0.f};
+        for (int t = 0; t < 2; ++t) {
+            GT[I][t] = gather_decay<NT>(lar[t], m, I, g);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const float* src = stage + (16 * J + 4 * g) * kFP + 32 * w + 16 * t + l16;
-                acc[t] = mma_f32_k16(am, floatx4{src[0], src[kFP], src[2 * kFP], src[3 * kFP]}, acc[t]);
-            }
+            for (int e = 0; e < 4; ++e) deep |= !(GT[I][t][e] >= -kMaxDecay);
         }
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                G[(16 * I + 4 * g + e) * kFP + 32 * w + 16 * t + l16] = acc[t][e];
-                deep |= !(acc[t][e] >= -kMaxDecay);
-            }
     }
-    const bool any_deep = __any(deep);
-    if (lane == 0) flag[w] = any_deep ? 1 : 0;
-    __syncthreads();
-    deep = (flag[0] | flag[1] | flag[2] | flag[3]) != 0;
-
-    // ---- scaled rows --------------------------------------------------------
+    deep = __any(deep);
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
-        const int i = 16 * I + r16;
-        float kx[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, qx[8], x[8];
+        const int i = 16 * I + l16;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) qx[e] = 0.f;
-        if (i < n) {
-            row8(k + i * HD + c8, kx);
-            row8(q + i * HD + c8, qx);
+        for (int t = 0; t < 2; ++t) {
+            const int c = 32 * w + 16 * t + 4 * g;
+            floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]), ex;
+            if (i >= n) kx = qx = zero4();
+            if (__any(unsound(kx))) {
+                uint64_t off = __ballot(unsound(kx));   // lane (l16, any g): node 16 I + l16
+                off |= off >> 32;
+                off |= off >> 16;
+                bad_node |= (off & 0xffff) << (16 * I);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) kx[e] = finite_or_0(kx[e]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
+            Xk.put4(i, c, kx * ex);
+            Xq.put4(i, c, qx * ex);
+            if (!deep) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[I][t][e]);
+                Y.put4(i, c, kx * ex);
+            } else {
+                Y.put4_f32(i, c, GT[I][t]);
+            }
         }
-        const bool unsound = drop_nonfinite(kx);
-        const bool any = any_of_row(unsound, lane);
-        if (l16 == 0) bad[L::kN + i] = any;
-        float gv[8];
-        row8(G + i * kFP + c8, gv);
-        float ex[8];
+    }
+    if (lane == 0) {
+        bad[w] = bad_node;
+        flag[w] = deep ? 1 : 0;
+    }
+    if (NT == 1) {
+        // both Gram tiles over this wavefront's channels, which it alone has written
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
 #pragma unroll
-        for (int e = 0; e < 8; ++e) ex[e] = expf(gv[e]);
+        for (int s = 0; s < 2; ++s) {
+            const floatx4 acc = gram(s ? Xq : Xk, 0, Y, 0, 32 * w, 32 * w + 32, l16, g);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = kx[e] * ex[e];
-        Xk.put8(i, c8, x);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = qx[e] * ex[e];
-        Xq.put8(i, c8, x);
-        if (!deep) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = kx[e] * expf(-gv[e]);
-            Y.put8(i, c8, x);
+            for (int e = 0; e < 4; ++e) part[((s * 4 + w) * 16 + 4 * g + e) * 20 + l16] = acc[e];
         }
     }
     __syncthreads();
 
     // ---- Gram matrices, masked by ancestry ----------------------------------
-    // (pair by pair they are written while G is read: to the unused Y)
-    float* gkk = reinterpret_cast<float*>(lds + (deep ? L::kY : L::kG));
-    float* gqk = gkk + L::kN * L::kLP;
-    if (!deep) {
+    const int deep_waves = flag[0] | flag[1] << 1 | flag[2] << 2 | flag[3] << 3;
+    if (deep_waves == 0 && NT == 1) {
+        const int i = tid >> 4, j = tid & 15, x = i * 20 + j;
+        const bool on = (anc[i] >> j) & 1;
+        float s[2];
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            const float* pm = part + m * 4 * 320 + x;
+            s[m] = (pm[0] + pm[320]) + (pm[640] + pm[960]);
+        }
+        gkk[i * L::kLP + j] = on && i != j ? sbeta[i] * s[0] : 0.f;
+        gqk[i * L::kLP + j] = on ? s[1] : 0.f;
+    } else if (deep_waves == 0) {
         int tile = 0;
 #pragma unroll
         for (int I = 0; I < NT; ++I) {
@@ -359,7 +459,7 @@ __global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
 #pragma unroll
                 for (int s = 0; s < 2; ++s, ++tile) {
                     if ((tile & 3) != w) continue;
-                    const floatx4 acc = gram(s ? Xq : Xk, 16 * I, Y, 16 * J, l16, g);
+                    const floatx4 acc = gram(s ? Xq : Xk, 16 * I, Y, 16 * J, 0, kHeadDim, l16, g);
                     const int j = 16 * J + l16;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -371,33 +471,25 @@ __global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
             }
         }
     } else {
+        // pair by pair: e^{G_i - G_j} for the channels out of range
         for (int pr = tid; pr < 256 * nt * nt; pr += 256) {
             const int i = pr / (16 * nt), j = pr % (16 * nt);
             float skk = 0.f, sqk = 0.f;
             if (i < n && ((anc[i] >> j) & 1)) {
                 for (int c = 0; c < kHeadDim; ++c) {
-                    const float kd = finite_or_0(to_f32(k[j * HD + c])) * expf(G[i * kFP + c] - G[j * kFP + c]);
-                    skk += finite_or_0(to_f32(k[i * HD + c])) * kd;
-                    sqk += to_f32(q[i * HD + c]) * kd;
+                    if ((deep_waves >> (c >> 5)) & 1) {
+                        const float kd = finite_or_0(to_f32(k[j * HD + c])) * exp_t<T>(Y.get_f32(i, c) - Y.get_f32(j, c));
+                        skk += finite_or_0(to_f32(k[i * HD + c])) * kd;
+                        sqk += to_f32(q[i * HD + c]) * kd;
+                    } else {
+                        const float y = Y.get(j, c);
+                        skk += Xk.get(i, c) * y;
+                        sqk += Xq.get(i, c) * y;
+                    }
                 }
             }
             gkk[i * L::kLP + j] = i == j ? 0.f : sbeta[i] * skk;
             gqk[i * L::kLP + j] = sqk;
-        }
-    }
-    __syncthreads();
-
-    // ---- inverses of the unit lower triangular diagonal blocks I + L --------
-    if (w == 0 && g < nt) {   // lane = (block g, column l16)
-        const float* Lg = gkk + 16 * g * L::kLP + 16 * g;
-        float x[16];
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            float s = r == l16 ? 1.f : 0.f;
-#pragma unroll
-            for (int j = 0; j < r; ++j) s -= Lg[r * L::kLP + j] * x[j];
-            x[r] = s;
-            inv[(16 * g + r) * 20 + l16] = s;
         }
     }
 
@@ -406,21 +498,31 @@ __global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
 #pragma unroll
     for (int r = 0; r < NT; ++r) held[r][0] = held[r][1] = read[r][0] = read[r][1] = zero4();
 #pragma unroll
-    for (int kb = 0; kb < kHeadDim; kb += 32) {
-        floatx2 s[8];
+    for (int kb = 0; kb < 4; ++kb) {
+        state_product<NT>(Xk, 32 * kb, st[kb], held, nt, l16, g);
+        state_product<NT>(Xq, 32 * kb, st[kb], read, nt, l16, g);
+    }
+    __syncthreads();
+
+    // ---- inverses of the unit lower triangular diagonal blocks I + L: wavefront w that of block w, lane =
+    // column, column by column (once x[j] is final it leaves all later rows)
+    if (w < nt && g == 0) {
+        const float* Lw = gkk + 16 * w * L::kLP + 16 * w;
+        float x[16];
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            s[e] = __builtin_nontemporal_load(
-                reinterpret_cast<const floatx2*>(S + (kb + 16 * (e >> 2) + (e & 3)) * kHeadDim));
-        state_product<NT>(Xk, kb, s, held, nt, l16, g);
-        state_product<NT>(Xq, kb, s, read, nt, l16, g);
+        for (int r = 0; r < 16; ++r) x[r] = r == l16 ? 1.f : 0.f;
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+            inv[(16 * w + j) * 20 + l16] = x[j];
+#pragma unroll
+            for (int r = j + 1; r < 16; ++r) x[r] -= Lw[r * L::kLP + j] * x[j];
+        }
     }
     __syncthreads();
 
     // ---- pseudo-values and outputs, block by block --------------------------
-    const uint64_t bad_node = __ballot(lane < n && (bad[lane] | bad[L::kN + lane] | bad[2 * L::kN + lane]));
+    bad_node = bad[0] | bad[1] | bad[2] | bad[3];
     uint64_t bad_col[2] = {bad_node, bad_node};   // bit j: node j taints this lane's column t
-    floatx2 vv[NT][4];
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
@@ -428,7 +530,7 @@ __global__ __launch_bounds__(256) void tree_decode_kernel(TreeDecodeArgs a) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int i = 16 * I + 4 * g + e;
-            vv[I][e] = i < n ? pair(v + i * HD + c0) : floatx2{0.f, 0.f};
+            if (i >= n) vv[I][e] = floatx2{0.f, 0.f};
             s = __builtin_fmaf(vv[I][e][0], 0.f, __builtin_fmaf(vv[I][e][1], 0.f, s));
         }
         if (__any(s != 0.f)) {
