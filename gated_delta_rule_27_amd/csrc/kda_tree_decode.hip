@@ -31,6 +31,8 @@
 // it owns value columns 32 w .. 32 w + 31 (lane: columns 2 (l % 16), +1) over
 // all 128 state rows, and pseudo-values, solve and outputs stay in its own
 // accumulators.  All loads, the state's included, are issued at the start.
+#include <type_traits>
+
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_tree.h"
@@ -44,6 +46,18 @@ constexpr int kFP = kHeadDim + 4;   // fp32 LDS row
 constexpr int kBP = kHeadDim + 8;   // bf16 LDS row
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+// x, y as bf16 (hi) and the bf16 of what that leaves out (lo)
+__device__ __forceinline__ void split2(float x, float y, bf16x2& hi, bf16x2& lo) {
+    hi = __builtin_convertvector((floatx2{x, y}), bf16x2);
+    const uint32_t u = __builtin_bit_cast(uint32_t, hi);
+    lo = __builtin_convertvector((floatx2{x - __builtin_bit_cast(float, u << 16),
+                                          y - __builtin_bit_cast(float, u & 0xffff0000u)}), bf16x2);
+}
+__device__ __forceinline__ bf16x4 join(bf16x2 a, bf16x2 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3); }
+__device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+}
 
 // Rows of 128 channels as MFMA operands in LDS.  fp32 rows as they are;
 // for bf16 inputs a scaled row is no longer a bf16 value, so it is held as
@@ -73,14 +87,11 @@ struct Rows<bf16> {
     __device__ __forceinline__ Rows(unsigned char* base, int rows)
         : hi(reinterpret_cast<bf16*>(base)), lo(hi + rows * kBP) {}
     __device__ __forceinline__ void put4(int row, int c, floatx4 x) const {
-        bf16x4 h, l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            h[e] = (bf16)x[e];
-            l[e] = (bf16)(x[e] - (float)h[e]);
-        }
-        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = h;
-        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = l;
+        bf16x2 h[2], l[2];
+        split2(x[0], x[1], h[0], l[0]);
+        split2(x[2], x[3], h[1], l[1]);
+        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = join(h[0], h[1]);
+        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = join(l[0], l[1]);
     }
     __device__ __forceinline__ float get(int row, int c) const {
         return (float)hi[row * kBP + c] + (float)lo[row * kBP + c];
@@ -155,11 +166,11 @@ __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const
     bf16x8 bh[2], bl[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
+        bf16x2 h[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            bh[t][e] = (bf16)s[e][t];
-            bl[t][e] = (bf16)(s[e][t] - (float)bh[t][e]);
-        }
+        for (int e = 0; e < 4; ++e) split2(s[2 * e][t], s[2 * e + 1][t], h[e], l[e]);
+        bh[t] = join(join(h[0], h[1]), join(h[2], h[3]));
+        bl[t] = join(join(l[0], l[1]), join(l[2], l[3]));
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -176,36 +187,71 @@ __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const
     }
 }
 
-__device__ __forceinline__ floatx2 pair(const bf16* p) {
-    const bf16x2 a = *reinterpret_cast<const bf16x2*>(p);
-    return floatx2{(float)a[0], (float)a[1]};
-}
-__device__ __forceinline__ floatx2 pair(const float* p) { return *reinterpret_cast<const floatx2*>(p); }
-__device__ __forceinline__ void put_pair(bf16* p, float x, float y) {
-    *reinterpret_cast<bf16x2*>(p) = bf16x2{(bf16)x, (bf16)y};   // RNE
-}
-__device__ __forceinline__ void put_pair(float* p, float x, float y) {
-    *reinterpret_cast<floatx2*>(p) = floatx2{x, y};
-}
-
-// 4 consecutive channels as loaded
-__device__ __forceinline__ bf16x4 load4(const bf16* p) { return *reinterpret_cast<const bf16x4*>(p); }
-__device__ __forceinline__ floatx4 load4(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
+// Elements through a buffer resource of the sequence's nodes: 32-bit
+// offsets, and rows past the nodes read 0 and drop their stores.
+template <typename T>
+struct Elems;
+template <>
+struct Elems<bf16> {
+    typedef bf16x2 two;    // as loaded
+    typedef bf16x4 four;
+    static __device__ __forceinline__ bf16 load1(rsrc_t r, uint32_t off) { return buf_load_bf16(r, off); }
+    static __device__ __forceinline__ two load2(rsrc_t r, uint32_t off) {
+        return __builtin_bit_cast(bf16x2, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+    }
+    static __device__ __forceinline__ four load4(rsrc_t r, uint32_t off) { return buf_load_bf16x4(r, off); }
+    static __device__ __forceinline__ void store2(rsrc_t r, uint32_t off, float x, float y) {   // RNE
+        __builtin_amdgcn_raw_buffer_store_b32(
+            __builtin_bit_cast(int, __builtin_convertvector((floatx2{x, y}), bf16x2)), r, (int)off, 0, 0);
+    }
+};
+typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
+template <>
+struct Elems<float> {
+    typedef floatx2 two;
+    typedef floatx4 four;
+    static __device__ __forceinline__ float load1(rsrc_t r, uint32_t off) {
+        return __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
+    }
+    static __device__ __forceinline__ two load2(rsrc_t r, uint32_t off) {
+        return __builtin_bit_cast(floatx2, __builtin_amdgcn_raw_buffer_load_b64(r, (int)off, 0, 0));
+    }
+    static __device__ __forceinline__ four load4(rsrc_t r, uint32_t off) {
+        return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+    }
+    static __device__ __forceinline__ void store2(rsrc_t r, uint32_t off, float x, float y) {
+        __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2_t, floatx2{x, y}), r, (int)off, 0, 0);
+    }
+};
 __device__ __forceinline__ floatx4 widen(bf16x4 x) {
     return floatx4{(float)x[0], (float)x[1], (float)x[2], (float)x[3]};
 }
 __device__ __forceinline__ floatx4 widen(floatx4 x) { return x; }
-template <typename T>
-struct Four;
-template <>
-struct Four<bf16> { typedef bf16x4 type; };
-template <>
-struct Four<float> { typedef floatx4 type; };
+
+// s, or NaN where an element is not finite
+__device__ __forceinline__ float probe(float s, floatx2 x) {
+    return __builtin_fmaf(x[0], 0.f, __builtin_fmaf(x[1], 0.f, s));
+}
+__device__ __forceinline__ float probe(float s, bf16x2 x) {
+    return probe(s, floatx2{(float)x[0], (float)x[1]});
+}
+template <typename V>
+__device__ __forceinline__ float probe4(float s, V x) {
+    return probe(probe(s, __builtin_shufflevector(x, x, 0, 1)), __builtin_shufflevector(x, x, 2, 3));
+}
+
+// bits 0..3 as four bf16, 1 or 0
+__device__ __forceinline__ bf16x4 bits4(uint32_t b) {
+    typedef uint32_t u2 __attribute__((ext_vector_type(2)));
+    // two bits to the low bits of two halves, times the bf16 one
+    const uint32_t lo = ((b & 3u) * 0x8001u) & 0x10001u, hi = (((b >> 2) & 3u) * 0x8001u) & 0x10001u;
+    return __builtin_bit_cast(bf16x4, u2{lo * 0x3f80u, hi * 0x3f80u});
+}
 
 // G^T of 16 nodes (columns) and 16 channels: log alpha^T (a: channel l16,
 // nodes 16 J + 4 g + 0..3) times the ancestor bits of node l16
-template <int NT>
-__device__ __forceinline__ floatx4 gather_decay(const floatx4 (&a)[NT], uint64_t m, int I, int g) {
+template <int NT, typename M>
+__device__ __forceinline__ floatx4 gather_decay(const floatx4 (&a)[NT], M m, int I, int g) {
     floatx4 acc = zero4();
 #pragma unroll
     for (int J = 0; J < NT; ++J) {
@@ -217,20 +263,19 @@ __device__ __forceinline__ floatx4 gather_decay(const floatx4 (&a)[NT], uint64_t
     return acc;
 }
 // (bf16 log alpha times 0 or 1 is exact)
-template <int NT>
-__device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], uint64_t m, int I, int g) {
+template <int NT, typename M>
+__device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], M m, int I, int g) {
     floatx4 acc = zero4();
 #pragma unroll
     for (int J = 0; J < NT; J += 2) {
         if (J > I) break;
-        bf16x8 x, y;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int jj = J + (e >> 2);
-            x[e] = jj < NT ? a[jj < NT ? jj : 0][e & 3] : (bf16)0.f;
-            y[e] = jj < NT && ((m >> (16 * jj + 4 * g + (e & 3))) & 1) ? (bf16)1.f : (bf16)0.f;
-        }
-        acc = mma_bf16_k32(x, y, acc);
+        const bf16 z = (bf16)0.f;
+        const bf16x4 zero = {z, z, z, z};
+        const bool two = J + 1 < NT;
+        acc = mma_bf16_k32(join(a[J], two ? a[two ? J + 1 : J] : zero),
+                           join(bits4((uint32_t)(m >> (16 * J + 4 * g))),
+                                two ? bits4((uint32_t)(m >> (two ? 16 * J + 16 + 4 * g : 0))) : zero),
+                           acc);
     }
     return acc;
 }
@@ -243,15 +288,6 @@ template <>
 __device__ __forceinline__ float exp_t<float>(float x) { return expf(x); }
 
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
-// whether one of four is not finite
-template <typename V>
-__device__ __forceinline__ bool unsound(V x) {
-    float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) s = __builtin_fmaf((float)x[e], 0.f, s);   // 0, or NaN
-    return s != 0.f;
-}
-
 // LDS of a workgroup for up to 16 NT nodes
 template <typename T, int NT>
 struct TreeLds {
@@ -261,11 +297,12 @@ struct TreeLds {
     static constexpr int kXk = 0, kXq = kRowsB;
     static constexpr int kY = 2 * kRowsB;                     // Y; for channels out of range G itself
     static constexpr int kGram = 3 * kRowsB;                  // both Gram matrices
-    static constexpr int kInv = kGram + 2 * kN * kLP * 4;     // inverse diagonal blocks
+    static constexpr int kDiag = kGram + 2 * kN * kLP * 4;    // diagonal blocks of the first, transposed
+    static constexpr int kInv = kDiag + NT * 16 * 20 * 4;     // their inverses (of I + block)
     // NT = 1: the wavefronts' parts of both Gram tiles
     static constexpr int kPart = kInv + NT * 16 * 20 * 4;
     static constexpr int kBeta = kPart + (NT == 1 ? 4 * 2 * 16 * 20 * 4 : 0);
-    static constexpr int kAnc = kBeta + kN * 4;
+    static constexpr int kAnc = kBeta + kN * 4;               // (8 bytes a node)
     static constexpr int kBad = kAnc + kN * 8;                // per wavefront: nodes with non-finite inputs
     static constexpr int kFlag = kBad + 4 * 8;                // per wavefront: channels out of range
     static constexpr int kBytes = kFlag + 16;
@@ -274,7 +311,8 @@ struct TreeLds {
 template <typename T, int NT>
 __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_decode_kernel(TreeDecodeArgs a) {
     using L = TreeLds<T, NT>;
-    typedef typename Four<T>::type four;
+    using E = Elems<T>;
+    using Mask = typename std::conditional<NT <= 2, uint32_t, uint64_t>::type;   // a bit per node
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -284,112 +322,127 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
     const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, N));
     if (n == 0) return;
     const int nt = (n + 15) / 16;
-    const size_t HD = (size_t)H * kHeadDim;
-    const size_t base = ((size_t)b * N * H + h) * kHeadDim;   // node 0's row; nodes are HD apart
-    const T* k = static_cast<const T*>(a.k) + base;
-    const T* q = static_cast<const T*>(a.q) + base;
-    const T* v = static_cast<const T*>(a.v) + base;
-    const T* la = static_cast<const T*>(a.log_alpha) + base;
-    const T* beta = static_cast<const T*>(a.beta) + (size_t)b * N * H + h;
-    T* o = static_cast<T*>(a.o) + base;
-    const int c0 = 32 * w + 2 * l16;                          // this lane's first column
-    const float* S = a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim) + (size_t)(4 * g) * kHeadDim + c0;
+    constexpr uint32_t es = sizeof(T);
+    const uint32_t row_b = (uint32_t)H * kHeadDim * es;       // from node to node (64 rows: < 2^32 bytes)
+    const size_t base = ((size_t)b * N * H + h) * kHeadDim;   // node 0's row
+    const uint32_t rows_b = (uint32_t)(n - 1) * row_b + kHeadDim * es;
+    auto rows = [&](const void* p) { return make_rsrc_u32(static_cast<const T*>(p) + base, rows_b); };
+    const rsrc_t kr_ = rows(a.k), qr_ = rows(a.q), vr_ = rows(a.v), lr_ = rows(a.log_alpha), or_ = rows(a.o);
+    const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
 
     const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN), Y(lds + L::kY, L::kN);
     float* gkk = reinterpret_cast<float*>(lds + L::kGram);
     float* gqk = gkk + L::kN * L::kLP;
+    float* diag = reinterpret_cast<float*>(lds + L::kDiag);
     float* inv = reinterpret_cast<float*>(lds + L::kInv);
     float* part = reinterpret_cast<float*>(lds + L::kPart);
     float* sbeta = reinterpret_cast<float*>(lds + L::kBeta);
-    uint64_t* anc = reinterpret_cast<uint64_t*>(lds + L::kAnc);
-    uint64_t* bad = reinterpret_cast<uint64_t*>(lds + L::kBad);
+    Mask* anc = reinterpret_cast<Mask*>(lds + L::kAnc);
+    Mask* bad = reinterpret_cast<Mask*>(lds + L::kBad);
     int* flag = reinterpret_cast<int*>(lds + L::kFlag);
 
     // ---- everything this workgroup reads, in the order it is needed ---------
-    // (rows past the nodes repeat the last one and are replaced by 0 where they are used)
     int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
-    four lar[2][NT], kr[NT][2], qr[NT][2];
+    typename E::four lar[2][NT], kr[NT][2], qr[NT][2];
+    const uint32_t at_g = 4 * g * row_b, at_l = l16 * row_b;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int J = 0; J < NT; ++J)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                lar[t][J][e] = la[min(16 * J + 4 * g + e, n - 1) * HD + 32 * w + 16 * t + l16];
+                lar[t][J][e] = E::load1(lr_, at_g + (32 * w + l16) * es + (16 * J + e) * row_b + 16 * t * es);
 #pragma unroll
     for (int I = 0; I < NT; ++I)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const size_t off = min(16 * I + l16, n - 1) * HD + 32 * w + 16 * t + 4 * g;
-            kr[I][t] = load4(k + off);
-            qr[I][t] = load4(q + off);
+            const uint32_t off = at_l + (32 * w + 4 * g) * es + 16 * I * row_b + 16 * t * es;
+            kr[I][t] = E::load4(kr_, off);
+            qr[I][t] = E::load4(qr_, off);
         }
-    float bt = to_f32(beta[(size_t)min(lane, n - 1) * H]);
-    floatx2 vv[NT][4];
+    float bt = to_f32(E::load1(make_rsrc_u32(static_cast<const T*>(a.beta) + (size_t)b * N * H + h,
+                                             ((uint32_t)(n - 1) * H + 1) * es),
+                               (uint32_t)lane * H * es));
+    typename E::two vv[NT][4];
 #pragma unroll
     for (int I = 0; I < NT; ++I)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vv[I][e] = pair(v + min(16 * I + 4 * g + e, n - 1) * HD + c0);
+        for (int e = 0; e < 4; ++e) vv[I][e] = E::load2(vr_, at_g + c0 * es + (16 * I + e) * row_b);
     floatx2 st[4][8];
+    {
+        const rsrc_t sr = make_rsrc_u32(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim),
+                                        kHeadDim * kHeadDim * 4);
+        const int at = (4 * g * kHeadDim + c0) * 4;
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb)
+        for (int kb = 0; kb < 4; ++kb)
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            st[kb][e] = __builtin_nontemporal_load(
-                reinterpret_cast<const floatx2*>(S + (32 * kb + 16 * (e >> 2) + (e & 3)) * kHeadDim));
+            for (int e = 0; e < 8; ++e)   // read once: streamed past the caches
+                st[kb][e] = __builtin_bit_cast(
+                    floatx2, __builtin_amdgcn_raw_buffer_load_b64(
+                                 sr, at + (e & 3) * kHeadDim * 4, (32 * kb + 16 * (e >> 2)) * kHeadDim * 4, 2));
+    }
     __builtin_amdgcn_sched_barrier(0);
 
     // ---- ancestor masks, lane = node, by doubling: a lane joins the mask of the node it points at, then
     // points where that node points
-    uint64_t mask = (uint64_t)1 << lane;
+    Mask mask = lane < L::kN ? (Mask)1 << (lane & (L::kN - 1)) : 0;
     while (__ballot(par >= 0)) {
-        const uint64_t pm = __shfl(mask, par < 0 ? lane : par, 64);
+        const Mask pm = __shfl(mask, par < 0 ? lane : par, 64);
         const int pp = __shfl(par, par < 0 ? lane : par, 64);
         if (par >= 0) {
             mask |= pm;
             par = pp;
         }
     }
-
-    // ---- G^T, scaled rows: this wavefront's 32 channels ----------------------
-    uint64_t bad_node = __ballot(lane < n && !(bt - bt == 0.f));   // non-finite beta, log alpha, k
     if (w == 0 && lane < L::kN) {
         anc[lane] = mask;
-        sbeta[lane] = lane < n ? finite_or_0(bt) : 0.f;
+        sbeta[lane] = finite_or_0(bt);
     }
+
+    // ---- G^T, scaled rows: this wavefront's 32 channels ----------------------
+    Mask bad_node = (Mask)__ballot(!(bt - bt == 0.f));   // non-finite beta, log alpha, k
+    {
+        float s = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+        for (int J = 0; J < NT; ++J)
 #pragma unroll
-        for (int J = 0; J < NT; ++J) {
+            for (int t = 0; t < 2; ++t) s = probe4(probe4(s, lar[t][J]), kr[J][t]);
+        if (__any(s != 0.f)) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (16 * J + 4 * g + e >= n) lar[t][J][e] = (T)0.f;
-            if (__any(unsound(lar[t][J]))) {
+            for (int J = 0; J < NT; ++J)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = (float)lar[t][J][e];
-                    const uint64_t off = __ballot(!(x - x == 0.f));   // group gg: node 16 J + 4 gg + e
+                for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int gg = 0; gg < 4; ++gg)
-                        if ((off >> (16 * gg)) & 0xffff) bad_node |= (uint64_t)1 << (16 * J + 4 * gg + e);
-                    if (!(x - x == 0.f)) lar[t][J][e] = (T)0.f;
-                }
-            }
+                    for (int e = 0; e < 4; ++e) {
+                        float x = (float)lar[t][J][e];   // node 16 J + 4 g + e
+                        uint64_t off = __ballot(!(x - x == 0.f));
+#pragma unroll
+                        for (int gg = 0; gg < 4; ++gg)
+                            if ((off >> (16 * gg)) & 0xffff) bad_node |= (Mask)1 << (16 * J + 4 * gg + e);
+                        lar[t][J][e] = (T)finite_or_0(x);
+                        x = (float)kr[J][t][e];          // node 16 J + l16
+                        off = __ballot(!(x - x == 0.f));
+                        off |= off >> 32;
+                        off |= off >> 16;
+                        bad_node |= (Mask)(off & 0xffff) << (16 * J);
+                        kr[J][t][e] = (T)finite_or_0(x);
+                    }
         }
+    }
     floatx4 GT[NT][2];
-    bool deep = false;
+    float least = 0.f;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
-        const uint64_t m = __shfl(mask, 16 * I + l16, 64);
+        const Mask m = __shfl(mask, 16 * I + l16, 64);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             GT[I][t] = gather_decay<NT>(lar[t], m, I, g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) deep |= !(GT[I][t][e] >= -kMaxDecay);
+            for (int e = 0; e < 4; ++e) least = fminf(least, GT[I][t][e]);
         }
     }
-    deep = __any(deep);
+    const bool deep = __any(least < -kMaxDecay);
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
@@ -397,16 +450,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int c = 32 * w + 16 * t + 4 * g;
-            floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]), ex;
-            if (i >= n) kx = qx = zero4();
-            if (__any(unsound(kx))) {
-                uint64_t off = __ballot(unsound(kx));   // lane (l16, any g): node 16 I + l16
-                off |= off >> 32;
-                off |= off >> 16;
-                bad_node |= (off & 0xffff) << (16 * I);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) kx[e] = finite_or_0(kx[e]);
-            }
+            const floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]);
+            floatx4 ex;
 #pragma unroll
             for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
             Xk.put4(i, c, kx * ex);
@@ -447,7 +492,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
             const float* pm = part + m * 4 * 320 + x;
             s[m] = (pm[0] + pm[320]) + (pm[640] + pm[960]);
         }
-        gkk[i * L::kLP + j] = on && i != j ? sbeta[i] * s[0] : 0.f;
+        diag[j * 20 + i] = on && i != j ? sbeta[i] * s[0] : 0.f;
         gqk[i * L::kLP + j] = on ? s[1] : 0.f;
     } else if (deep_waves == 0) {
         int tile = 0;
@@ -461,12 +506,15 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
                     if ((tile & 3) != w) continue;
                     const floatx4 acc = gram(s ? Xq : Xk, 16 * I, Y, 16 * J, 0, kHeadDim, l16, g);
                     const int j = 16 * J + l16;
+                    floatx4 x;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const int i = 16 * I + 4 * g + e;
                         const bool on = ((anc[i] >> j) & 1) && (s || j != i);
-                        (s ? gqk : gkk)[i * L::kLP + j] = on ? (s ? acc[e] : sbeta[i] * acc[e]) : 0.f;
+                        x[e] = on ? (s ? acc[e] : sbeta[i] * acc[e]) : 0.f;
+                        if (s || J < I) (s ? gqk : gkk)[i * L::kLP + j] = x[e];
                     }
+                    if (!s && J == I) *reinterpret_cast<floatx4*>(diag + j * 20 + 4 * g) = x;
                 }
             }
         }
@@ -478,9 +526,11 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
             if (i < n && ((anc[i] >> j) & 1)) {
                 for (int c = 0; c < kHeadDim; ++c) {
                     if ((deep_waves >> (c >> 5)) & 1) {
-                        const float kd = finite_or_0(to_f32(k[j * HD + c])) * exp_t<T>(Y.get_f32(i, c) - Y.get_f32(j, c));
-                        skk += finite_or_0(to_f32(k[i * HD + c])) * kd;
-                        sqk += to_f32(q[i * HD + c]) * kd;
+                        const uint32_t at_i = i * row_b + c * es, at_j = j * row_b + c * es;
+                        const float kd = finite_or_0(to_f32(E::load1(kr_, at_j))) *
+                                         exp_t<T>(Y.get_f32(i, c) - Y.get_f32(j, c));
+                        skk += finite_or_0(to_f32(E::load1(kr_, at_i))) * kd;
+                        sqk += to_f32(E::load1(qr_, at_i)) * kd;
                     } else {
                         const float y = Y.get(j, c);
                         skk += Xk.get(i, c) * y;
@@ -488,7 +538,9 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
                     }
                 }
             }
-            gkk[i * L::kLP + j] = i == j ? 0.f : sbeta[i] * skk;
+            skk = i == j ? 0.f : sbeta[i] * skk;
+            gkk[i * L::kLP + j] = skk;
+            if ((i ^ j) < 16) diag[j * 20 + (i & 15)] = skk;
             gqk[i * L::kLP + j] = sqk;
         }
     }
@@ -507,7 +559,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
     // ---- inverses of the unit lower triangular diagonal blocks I + L: wavefront w that of block w, lane =
     // column, column by column (once x[j] is final it leaves all later rows)
     if (w < nt && g == 0) {
-        const float* Lw = gkk + 16 * w * L::kLP + 16 * w;
+        const float* Lw = diag + 16 * w * 20;   // [column][row]
         float x[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) x[r] = r == l16 ? 1.f : 0.f;
@@ -515,56 +567,62 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
         for (int j = 0; j < 16; ++j) {
             inv[(16 * w + j) * 20 + l16] = x[j];
 #pragma unroll
-            for (int r = j + 1; r < 16; ++r) x[r] -= Lw[r * L::kLP + j] * x[j];
+            for (int r4 = (j + 1) / 4; r4 < 4; ++r4) {
+                const floatx4 c = *reinterpret_cast<const floatx4*>(Lw + j * 20 + 4 * r4);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (4 * r4 + e > j) x[4 * r4 + e] -= c[e] * x[j];
+            }
         }
     }
     __syncthreads();
 
     // ---- pseudo-values and outputs, block by block --------------------------
     bad_node = bad[0] | bad[1] | bad[2] | bad[3];
-    uint64_t bad_col[2] = {bad_node, bad_node};   // bit j: node j taints this lane's column t
-#pragma unroll
-    for (int I = 0; I < NT; ++I) {
-        if (I >= nt) break;
+    Mask bad_col[2] = {bad_node, bad_node};   // bit j: node j taints this lane's column t
+    {
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * I + 4 * g + e;
-            if (i >= n) vv[I][e] = floatx2{0.f, 0.f};
-            s = __builtin_fmaf(vv[I][e][0], 0.f, __builtin_fmaf(vv[I][e][1], 0.f, s));
-        }
+        for (int I = 0; I < NT; ++I)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s = probe(s, vv[I][e]);
         if (__any(s != 0.f)) {
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                uint32_t m = 0;
+            for (int I = 0; I < NT; ++I)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float x = vv[I][e][t];
-                    vv[I][e][t] = finite_or_0(x);
-                    m |= (x - x == 0.f ? 0u : 1u) << (4 * g + e);
+                for (int t = 0; t < 2; ++t) {
+                    uint32_t m = 0;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float x = (float)vv[I][e][t];
+                        vv[I][e][t] = (T)finite_or_0(x);
+                        m |= (x - x == 0.f ? 0u : 1u) << (4 * g + e);
+                    }
+                    m |= __shfl_xor(m, 16, 64);
+                    m |= __shfl_xor(m, 32, 64);
+                    bad_col[t] |= (Mask)m << (16 * I);
                 }
-                m |= __shfl_xor(m, 16, 64);
-                m |= __shfl_xor(m, 32, 64);
-                bad_col[t] |= (uint64_t)m << (16 * I);
-            }
         }
     }
     const bool tainted = __any((bad_col[0] | bad_col[1]) != 0);
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
-        const floatx4 bt = *reinterpret_cast<const floatx4*>(sbeta + 16 * I + 4 * g);
+        const floatx4 bt4 = *reinterpret_cast<const floatx4*>(sbeta + 16 * I + 4 * g);
+        const floatx4 ia = frag_k16(inv + (16 * I + l16) * 20, 0, g);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             floatx4 rhs;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rhs[e] = bt[e] * (vv[I][e][t] - held[I][t][e]);
-            floatx4 prev = zero4();
+            for (int e = 0; e < 4; ++e) rhs[e] = bt4[e] * ((float)vv[I][e][t] - held[I][t][e]);
+            if (I > 0) {
+                floatx4 prev = zero4();
 #pragma unroll
-            for (int J = 0; J < I; ++J)
-                prev = mma_f32_k16(frag_k16(gkk + (16 * I + l16) * L::kLP, 16 * J, g), held[J][t], prev);
-            rhs -= prev;
-            held[I][t] = mma_f32_k16(frag_k16(inv + (16 * I + l16) * 20, 0, g), rhs, zero4());
+                for (int J = 0; J < I; ++J)
+                    prev = mma_f32_k16(frag_k16(gkk + (16 * I + l16) * L::kLP, 16 * J, g), held[J][t], prev);
+                rhs -= prev;
+            }
+            held[I][t] = mma_f32_k16(ia, rhs, zero4());
         }
         floatx4 out[2] = {zero4(), zero4()};
 #pragma unroll
@@ -578,17 +636,15 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
         if (tainted) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const uint64_t m = anc[16 * I + 4 * g + e];
+                const Mask m = anc[16 * I + 4 * g + e];
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
                     if (m & bad_col[t]) out[t][e] = __builtin_nanf("");
             }
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int i = 16 * I + 4 * g + e;
-            if (i < n) put_pair(o + i * HD + c0, out[0][e], out[1][e]);
-        }
+        for (int e = 0; e < 4; ++e)
+            E::store2(or_, at_g + c0 * es + (16 * I + e) * row_b, out[0][e], out[1][e]);
     }
 }
 
