@@ -23,15 +23,23 @@
 // node) and v (per column) are therefore taken as 0 and remembered as bits,
 // and the outputs of the nodes that descend from them are set to NaN.
 //
-// Mapping.  One workgroup of four wavefronts per (sequence, head).  Before
-// the product with the state wavefront w owns key channels 32 w .. 32 w + 31
-// of all nodes: G^T comes out of its MFMA with a lane holding 4 channels of
-// one node, the layout in which k and q are loaded and the scaled rows leave
-// for LDS, so none of it needs another wavefront.  From the state product on
-// it owns value columns 32 w .. 32 w + 31 (lane: columns 2 (l % 16), +1) over
-// all 128 state rows, and pseudo-values, solve and outputs stay in its own
-// accumulators.  All loads, the state's included, are issued at the start.
+// Mapping.  One workgroup of four wavefronts per (sequence, head); all loads,
+// the state's included, are issued at the start.
+// Before the product with the state wavefront w owns key channels 32 w ..
+// 32 w + 31 of all nodes.  G^T comes out of its MFMA with a lane holding 4
+// channels of one node: the layout k and q are loaded in, and at once the
+// operand layout of the Gram tiles, so these take their operands from
+// registers, each wavefront over its own channels, and only the partial
+// tiles are summed over the wavefronts through LDS.  The tiles are formed
+// transposed (ancestor x node): a lane then holds what it has to hold of the
+// tile as an operand of the solve, and keeps and reads it as 16 bytes.
+// From the state product on wavefront w owns value columns 32 w .. 32 w + 31
+// (lane: columns 2 (l % 16), +1) over all 128 state rows, and pseudo-values,
+// solve and outputs stay in its own accumulators.  The scaled rows are all
+// that every wavefront needs of the others' work; beyond 32 nodes k's and
+// q's rows take turns in LDS, so that two workgroups share a compute unit.
 #include <type_traits>
+#include <utility>
 
 #include "kda.h"
 #include "kda_device.h"
@@ -59,11 +67,53 @@ __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Rows of 128 channels as MFMA operands in LDS.  fp32 rows as they are;
-// for bf16 inputs a scaled row is no longer a bf16 value, so it is held as
-// the sum of two bf16 (hi and the rounding's remainder lo): the products
-// hi hi + hi lo + lo hi leave a relative error of 2^-17, so that the one
-// rounding that counts is the output's.
+// Four consecutive k of a row or column of an MFMA operand.  fp32 values as
+// they are; for bf16 inputs a scaled value is no longer a bf16, so it is held
+// as the sum of two (hi and what its rounding leaves, lo): the products
+// hi hi + hi lo + lo hi leave a relative error of 2^-17, and the one rounding
+// that counts is the output's.
+template <typename T>
+struct Op;
+template <>
+struct __attribute__((aligned(16))) Op<float> {
+    floatx4 x;
+    static __device__ __forceinline__ Op of(floatx4 v) { return Op{v}; }
+    static __device__ __forceinline__ Op f32(floatx4 v) { return Op{v}; }   // kept whole
+    __device__ __forceinline__ floatx4 as_f32() const { return x; }
+};
+template <>
+struct __attribute__((aligned(16))) Op<bf16> {
+    bf16x4 hi, lo;
+    static __device__ __forceinline__ Op of(floatx4 v) {
+        bf16x2 h[2], l[2];
+        split2(v[0], v[1], h[0], l[0]);
+        split2(v[2], v[3], h[1], l[1]);
+        return Op{join(h[0], h[1]), join(l[0], l[1])};
+    }
+    // fp32 values kept whole in its place
+    static __device__ __forceinline__ Op f32(floatx4 v) { return __builtin_bit_cast(Op, v); }
+    __device__ __forceinline__ floatx4 as_f32() const { return __builtin_bit_cast(floatx4, *this); }
+};
+// acc += a b over 16 (a0, b0) or 32 k
+__device__ __forceinline__ floatx4 mma(Op<float> a0, Op<float> b0, floatx4 acc) {
+    return mma_f32_k16(a0.x, b0.x, acc);
+}
+__device__ __forceinline__ floatx4 mma(Op<float> a0, Op<float> a1, Op<float> b0, Op<float> b1, floatx4 acc) {
+    return mma_f32_k16(a1.x, b1.x, mma_f32_k16(a0.x, b0.x, acc));
+}
+__device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> a1, Op<bf16> b0, Op<bf16> b1, floatx4 acc) {
+    const bf16x8 ah = join(a0.hi, a1.hi), bh = join(b0.hi, b1.hi);
+    acc = mma_bf16_k32(join(a0.lo, a1.lo), bh, acc);
+    acc = mma_bf16_k32(ah, join(b0.lo, b1.lo), acc);
+    return mma_bf16_k32(ah, bh, acc);
+}
+__device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> b0, floatx4 acc) {
+    const bf16 z = (bf16)0.f;
+    const Op<bf16> zero{{z, z, z, z}, {z, z, z, z}};
+    return mma(a0, zero, b0, zero, acc);
+}
+
+// Rows of 128 channels in LDS, as A operands of the state product
 template <typename T>
 struct Rows;
 template <>
@@ -71,13 +121,9 @@ struct Rows<float> {
     static constexpr int kBytes = kFP * 4;   // of a row
     float* p;
     __device__ __forceinline__ Rows(unsigned char* base, int) : p(reinterpret_cast<float*>(base)) {}
-    __device__ __forceinline__ void put4(int row, int c, floatx4 x) const {
-        *reinterpret_cast<floatx4*>(p + row * kFP + c) = x;
+    __device__ __forceinline__ void put(int row, int c, Op<float> x) const {
+        *reinterpret_cast<floatx4*>(p + row * kFP + c) = x.x;
     }
-    __device__ __forceinline__ float get(int row, int c) const { return p[row * kFP + c]; }
-    // fp32 values kept whole in the place of a row's elements
-    __device__ __forceinline__ void put4_f32(int row, int c, floatx4 x) const { put4(row, c, x); }
-    __device__ __forceinline__ float get_f32(int row, int c) const { return get(row, c); }
 };
 template <>
 struct Rows<bf16> {
@@ -86,103 +132,50 @@ struct Rows<bf16> {
     bf16* lo;
     __device__ __forceinline__ Rows(unsigned char* base, int rows)
         : hi(reinterpret_cast<bf16*>(base)), lo(hi + rows * kBP) {}
-    __device__ __forceinline__ void put4(int row, int c, floatx4 x) const {
-        bf16x2 h[2], l[2];
-        split2(x[0], x[1], h[0], l[0]);
-        split2(x[2], x[3], h[1], l[1]);
-        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = join(h[0], h[1]);
-        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = join(l[0], l[1]);
-    }
-    __device__ __forceinline__ float get(int row, int c) const {
-        return (float)hi[row * kBP + c] + (float)lo[row * kBP + c];
-    }
-    // fp32 values kept whole in the place of a row's elements: upper half in hi, lower half in lo
-    __device__ __forceinline__ void put4_f32(int row, int c, floatx4 x) const {
-        shortx4 h, l;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t u = __builtin_bit_cast(uint32_t, (float)x[e]);
-            h[e] = (short)(u >> 16);
-            l[e] = (short)u;
-        }
-        *reinterpret_cast<shortx4*>(hi + row * kBP + c) = h;
-        *reinterpret_cast<shortx4*>(lo + row * kBP + c) = l;
-    }
-    __device__ __forceinline__ float get_f32(int row, int c) const {
-        const uint32_t h = *reinterpret_cast<const uint16_t*>(hi + row * kBP + c);
-        const uint32_t l = *reinterpret_cast<const uint16_t*>(lo + row * kBP + c);
-        return __builtin_bit_cast(float, h << 16 | l);
+    __device__ __forceinline__ void put(int row, int c, Op<bf16> x) const {
+        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = x.hi;
+        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = x.lo;
     }
 };
 
-// (rows a0 .. a0 + 15 of A) (rows b0 .. b0 + 15 of B)^T over channels c0 .. c1 - 1
-__device__ __forceinline__ floatx4 gram(const Rows<float>& A, int a0, const Rows<float>& B, int b0,
-                                        int c0, int c1, int l16, int g) {
-    floatx4 acc = zero4();
-#pragma unroll
-    for (int kb = c0; kb < c1; kb += 16)
-        acc = mma_f32_k16(frag_k16(A.p + (a0 + l16) * kFP, kb, g), frag_k16(B.p + (b0 + l16) * kFP, kb, g),
-                          acc);
-    return acc;
-}
-__device__ __forceinline__ floatx4 gram(const Rows<bf16>& A, int a0, const Rows<bf16>& B, int b0,
-                                        int c0, int c1, int l16, int g) {
-    floatx4 acc = zero4();
-#pragma unroll
-    for (int kb = c0; kb < c1; kb += 32) {
-        const bf16x8 ah = frag_k32(A.hi + (a0 + l16) * kBP, kb, g), al = frag_k32(A.lo + (a0 + l16) * kBP, kb, g);
-        const bf16x8 bh = frag_k32(B.hi + (b0 + l16) * kBP, kb, g), bl = frag_k32(B.lo + (b0 + l16) * kBP, kb, g);
-        acc = mma_bf16_k32(al, bh, acc);
-        acc = mma_bf16_k32(ah, bl, acc);
-        acc = mma_bf16_k32(ah, bh, acc);
+// 32 rows kb .. kb + 31 of one state column as the other operand: rows
+// kb + 4 g + 0..3 and kb + 16 + 4 g + 0..3, in the place of the fp32 values
+template <typename T>
+struct StateOp {
+    Op<T> half[2];
+    static __device__ __forceinline__ StateOp of(const floatx2 (&s)[8], int t) {
+        return StateOp{{Op<T>::of(floatx4{s[0][t], s[1][t], s[2][t], s[3][t]}),
+                        Op<T>::of(floatx4{s[4][t], s[5][t], s[6][t], s[7][t]})}};
     }
-    return acc;
-}
-
-// Row tiles of X times 32 rows kb .. kb + 31 of this wavefront's state
-// columns (s[8 rows][2 columns]: rows kb + 4 g + 0..3 and kb + 16 + 4 g + 0..3)
+};
+// acc += row tiles of X times them
 template <int RT>
-__device__ __forceinline__ void state_product(const Rows<float>& X, int kb, const floatx2 (&s)[8],
+__device__ __forceinline__ void state_product(const Rows<float>& X, int kb, const StateOp<float> (&s)[2],
                                               floatx4 (&acc)[RT][2], int nrt, int l16, int g) {
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        floatx4 b[2];
+    for (int r = 0; r < RT; ++r) {
+        if (r < nrt) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
-            b[t] = floatx4{s[4 * half][t], s[4 * half + 1][t], s[4 * half + 2][t], s[4 * half + 3][t]};
+            for (int half = 0; half < 2; ++half) {
+                const Op<float> a{frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g)};
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-            if (r < nrt) {
-                const floatx4 a = frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g);
-#pragma unroll
-                for (int t = 0; t < 2; ++t) acc[r][t] = mma_f32_k16(a, b[t], acc[r][t]);
+                for (int t = 0; t < 2; ++t) acc[r][t] = mma(a, s[t].half[half], acc[r][t]);
             }
         }
     }
 }
 template <int RT>
-__device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const floatx2 (&s)[8],
+__device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const StateOp<bf16> (&s)[2],
                                               floatx4 (&acc)[RT][2], int nrt, int l16, int g) {
-    bf16x8 bh[2], bl[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        bf16x2 h[4], l[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) split2(s[2 * e][t], s[2 * e + 1][t], h[e], l[e]);
-        bh[t] = join(join(h[0], h[1]), join(h[2], h[3]));
-        bl[t] = join(join(l[0], l[1]), join(l[2], l[3]));
-    }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
         if (r < nrt) {
-            const bf16x8 ah = frag_k32(X.hi + (16 * r + l16) * kBP, kb, g);
-            const bf16x8 al = frag_k32(X.lo + (16 * r + l16) * kBP, kb, g);
+            const bf16* hi = X.hi + (16 * r + l16) * kBP;
+            const bf16* lo = X.lo + (16 * r + l16) * kBP;
+            const Op<bf16> a0{frag_k16(hi, kb, g), frag_k16(lo, kb, g)};
+            const Op<bf16> a1{frag_k16(hi, kb + 16, g), frag_k16(lo, kb + 16, g)};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                acc[r][t] = mma_bf16_k32(al, bh[t], acc[r][t]);
-                acc[r][t] = mma_bf16_k32(ah, bl[t], acc[r][t]);
-                acc[r][t] = mma_bf16_k32(ah, bh[t], acc[r][t]);
-            }
+            for (int t = 0; t < 2; ++t) acc[r][t] = mma(a0, a1, s[t].half[0], s[t].half[1], acc[r][t]);
         }
     }
 }
@@ -288,30 +281,93 @@ template <>
 __device__ __forceinline__ float exp_t<float>(float x) { return expf(x); }
 
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
+// (I + L)^{-1} of a strictly lower triangular tile in place; element (i, j)
+// lies at lane 16 (j / 4) + i, j % 4.  One lane per column, row by row.
+__device__ __forceinline__ void invert(float* tile, int l16, int g) {
+    if (g != 0) return;
+    float x[16];
+    x[0] = l16 == 0 ? 1.f : 0.f;
+#pragma unroll
+    for (int r = 1; r < 16; ++r) {
+        float s = r == l16 ? 1.f : 0.f;
+#pragma unroll
+        for (int jq = 0; jq < (r + 3) / 4; ++jq) {
+            const floatx4 c = *reinterpret_cast<const floatx4*>(tile + (16 * jq + r) * 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (4 * jq + e < r) s -= c[e] * x[4 * jq + e];
+        }
+        x[r] = s;
+    }
+#pragma unroll
+    for (int r = 0; r < 16; ++r) tile[(16 * (l16 >> 2) + r) * 4 + (l16 & 3)] = x[r];
+}
+
+// f(0), ..., f(N - 1) with the index a constant expression
+template <typename F, int... I>
+__device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+    each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// The Gram tiles (I, J <= I) of both matrices, in the order in which they
+// are formed: diagonal tiles of k k first (wavefront I sums and inverts that
+// of block I), then k k, then q k.
+template <int NT>
+struct Tiles {
+    static constexpr int kHalf = NT * (NT + 1) / 2, kAll = 2 * kHalf;
+    static constexpr int kRound = kAll < 8 ? kAll : 8;   // summed at a time
+    static constexpr bool q(int t) { return t >= kHalf; }
+    static constexpr int row(int t) {
+        if (t < NT) return t;
+        int i = q(t) ? 0 : 1, left = q(t) ? t - kHalf : t - NT;
+        for (; left >= (q(t) ? i + 1 : i); ++i) left -= q(t) ? i + 1 : i;
+        return i;
+    }
+    static constexpr int col(int t) {
+        if (t < NT) return t;
+        int i = q(t) ? 0 : 1, left = q(t) ? t - kHalf : t - NT;
+        for (; left >= (q(t) ? i + 1 : i); ++i) left -= q(t) ? i + 1 : i;
+        return left;
+    }
+    // place of a finished tile
+    static constexpr int place(bool q, int I, int J) { return (q ? kHalf : 0) + I * (I + 1) / 2 + J; }
+};
+
 // LDS of a workgroup for up to 16 NT nodes
 template <typename T, int NT>
 struct TreeLds {
     static constexpr int kN = 16 * NT;
-    static constexpr int kLP = kN + 4;                        // a row of a Gram matrix
     static constexpr int kRowsB = kN * Rows<T>::kBytes;       // an operand array
-    static constexpr int kXk = 0, kXq = kRowsB;
-    static constexpr int kY = 2 * kRowsB;                     // Y; for channels out of range G itself
-    static constexpr int kGram = 3 * kRowsB;                  // both Gram matrices
-    static constexpr int kDiag = kGram + 2 * kN * kLP * 4;    // diagonal blocks of the first, transposed
-    static constexpr int kInv = kDiag + NT * 16 * 20 * 4;     // their inverses (of I + block)
-    // NT = 1: the wavefronts' parts of both Gram tiles
-    static constexpr int kPart = kInv + NT * 16 * 20 * 4;
-    static constexpr int kBeta = kPart + (NT == 1 ? 4 * 2 * 16 * 20 * 4 : 0);
+    static constexpr bool kTurns = NT > 2;                    // k's and q's rows in the same place
+    static constexpr bool kOver = NT > 1;                     // partial tiles in the place of the rows
+    static constexpr int kPartB = Tiles<NT>::kRound * 4 * 1024;
+    static constexpr int kXk = 0, kXq = kTurns ? 0 : kRowsB;
+    static constexpr int kRowsEnd = (kTurns ? 1 : 2) * kRowsB;
+    static constexpr int kPart = kOver ? 0 : kRowsEnd;
+    static constexpr int kGram = kOver ? (kRowsEnd > kPartB ? kRowsEnd : kPartB) : kRowsEnd + kPartB;
+    static constexpr int kBeta = kGram + Tiles<NT>::kAll * 1024;
     static constexpr int kAnc = kBeta + kN * 4;               // (8 bytes a node)
     static constexpr int kBad = kAnc + kN * 8;                // per wavefront: nodes with non-finite inputs
-    static constexpr int kFlag = kBad + 4 * 8;                // per wavefront: channels out of range
-    static constexpr int kBytes = kFlag + 16;
+    static constexpr int kBytes = kBad + 4 * 8;
 };
 
+// Wavefronts per SIMD that the registers are cut for: what the LDS allows,
+// fp32 operands one less
 template <typename T, int NT>
-__global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_decode_kernel(TreeDecodeArgs a) {
+constexpr int tree_waves() {
+    return (NT == 1 ? 4 : (NT == 2 ? 3 : 2)) - (sizeof(T) == 4 ? 1 : 0);
+}
+
+template <typename T, int NT>
+__global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel(TreeDecodeArgs a) {
     using L = TreeLds<T, NT>;
     using E = Elems<T>;
+    using O = Op<T>;
+    using TT = Tiles<NT>;
     using Mask = typename std::conditional<NT <= 2, uint32_t, uint64_t>::type;   // a bit per node
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
@@ -330,21 +386,18 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
     const rsrc_t kr_ = rows(a.k), qr_ = rows(a.q), vr_ = rows(a.v), lr_ = rows(a.log_alpha), or_ = rows(a.o);
     const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
 
-    const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN), Y(lds + L::kY, L::kN);
-    float* gkk = reinterpret_cast<float*>(lds + L::kGram);
-    float* gqk = gkk + L::kN * L::kLP;
-    float* diag = reinterpret_cast<float*>(lds + L::kDiag);
-    float* inv = reinterpret_cast<float*>(lds + L::kInv);
-    float* part = reinterpret_cast<float*>(lds + L::kPart);
+    const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN);
+    floatx4* part = reinterpret_cast<floatx4*>(lds + L::kPart);   // [tile of the round][wavefront][lane]
+    O* gram = reinterpret_cast<O*>(lds + L::kGram);               // [tile][lane]
     float* sbeta = reinterpret_cast<float*>(lds + L::kBeta);
     Mask* anc = reinterpret_cast<Mask*>(lds + L::kAnc);
     Mask* bad = reinterpret_cast<Mask*>(lds + L::kBad);
-    int* flag = reinterpret_cast<int*>(lds + L::kFlag);
 
     // ---- everything this workgroup reads, in the order it is needed ---------
     int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
     typename E::four lar[2][NT], kr[NT][2], qr[NT][2];
     const uint32_t at_g = 4 * g * row_b, at_l = l16 * row_b;
+    const uint32_t at_kq = at_l + (32 * w + 4 * g) * es;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -356,18 +409,20 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
     for (int I = 0; I < NT; ++I)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const uint32_t off = at_l + (32 * w + 4 * g) * es + 16 * I * row_b + 16 * t * es;
-            kr[I][t] = E::load4(kr_, off);
-            qr[I][t] = E::load4(qr_, off);
+            kr[I][t] = E::load4(kr_, at_kq + 16 * I * row_b + 16 * t * es);
+            qr[I][t] = E::load4(qr_, at_kq + 16 * I * row_b + 16 * t * es);
         }
     float bt = to_f32(E::load1(make_rsrc_u32(static_cast<const T*>(a.beta) + (size_t)b * N * H + h,
                                              ((uint32_t)(n - 1) * H + 1) * es),
                                (uint32_t)lane * H * es));
     typename E::two vv[NT][4];
+    auto load_v = [&]() {
 #pragma unroll
-    for (int I = 0; I < NT; ++I)
+        for (int I = 0; I < NT; ++I)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vv[I][e] = E::load2(vr_, at_g + c0 * es + (16 * I + e) * row_b);
+            for (int e = 0; e < 4; ++e) vv[I][e] = E::load2(vr_, at_g + c0 * es + (16 * I + e) * row_b);
+    };
+    if (!L::kOver) load_v();
     floatx2 st[4][8];
     {
         const rsrc_t sr = make_rsrc_u32(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim),
@@ -394,13 +449,14 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
             par = pp;
         }
     }
-    if (w == 0 && lane < L::kN) {
-        anc[lane] = mask;
-        sbeta[lane] = finite_or_0(bt);
-    }
 
     // ---- G^T, scaled rows: this wavefront's 32 channels ----------------------
     Mask bad_node = (Mask)__ballot(!(bt - bt == 0.f));   // non-finite beta, log alpha, k
+    bt = finite_or_0(bt);
+    if (w == 0 && lane < L::kN) {
+        anc[lane] = mask;
+        sbeta[lane] = bt;
+    }
     {
         float s = 0.f;
 #pragma unroll
@@ -429,11 +485,11 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
                     }
         }
     }
+    if (lane == 0) bad[w] = bad_node;
     floatx4 GT[NT][2];
     float least = 0.f;
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-        if (I >= nt) break;
         const Mask m = __shfl(mask, 16 * I + l16, 64);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -442,140 +498,136 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
             for (int e = 0; e < 4; ++e) least = fminf(least, GT[I][t][e]);
         }
     }
-    const bool deep = __any(least < -kMaxDecay);
+    const bool deep = __any(least < -kMaxDecay);   // (of this wavefront's channels)
+    O xk[NT][2], xq[NT][2], y[NT][2];
 #pragma unroll
-    for (int I = 0; I < NT; ++I) {
-        if (I >= nt) break;
-        const int i = 16 * I + l16;
+    for (int I = 0; I < NT; ++I)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int c = 32 * w + 16 * t + 4 * g;
             const floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]);
             floatx4 ex;
 #pragma unroll
             for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
-            Xk.put4(i, c, kx * ex);
-            Xq.put4(i, c, qx * ex);
+            xk[I][t] = O::of(kx * ex);
+            xq[I][t] = O::of(qx * ex);
             if (!deep) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[I][t][e]);
-                Y.put4(i, c, kx * ex);
+                y[I][t] = O::of(kx * ex);
             } else {
-                Y.put4_f32(i, c, GT[I][t]);
+                y[I][t] = O::f32(GT[I][t]);
             }
         }
-    }
-    if (lane == 0) {
-        bad[w] = bad_node;
-        flag[w] = deep ? 1 : 0;
-    }
-    if (NT == 1) {
-        // both Gram tiles over this wavefront's channels, which it alone has written
-        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+    auto put_rows = [&](const Rows<T>& X, const O (&x)[NT][2]) {
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
-            const floatx4 acc = gram(s ? Xq : Xk, 0, Y, 0, 32 * w, 32 * w + 32, l16, g);
+        for (int I = 0; I < NT; ++I)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) part[((s * 4 + w) * 16 + 4 * g + e) * 20 + l16] = acc[e];
-        }
+            for (int t = 0; t < 2; ++t) X.put(16 * I + l16, 32 * w + 16 * t + 4 * g, x[I][t]);
+    };
+    if (!L::kOver) {
+        put_rows(Xk, xk);
+        put_rows(Xq, xq);
     }
-    __syncthreads();
 
-    // ---- Gram matrices, masked by ancestry ----------------------------------
-    const int deep_waves = flag[0] | flag[1] << 1 | flag[2] << 2 | flag[3] << 3;
-    if (deep_waves == 0 && NT == 1) {
-        const int i = tid >> 4, j = tid & 15, x = i * 20 + j;
-        const bool on = (anc[i] >> j) & 1;
-        float s[2];
+    // ---- Gram tiles, transposed: ancestors x nodes --------------------------
+    each<(TT::kAll + TT::kRound - 1) / TT::kRound>([&](auto round) {
+        constexpr int t0 = round() * TT::kRound;
+        constexpr int count = TT::kAll - t0 < TT::kRound ? TT::kAll - t0 : TT::kRound;
+        if (t0 > 0) __syncthreads();   // (the round before has been summed)
+        each<count>([&](auto u) {
+            constexpr int t = t0 + u();
+            constexpr int I = TT::row(t), J = TT::col(t);
+            if (I >= nt) return;
+            const O(&x)[2] = TT::q(t) ? xq[I] : xk[I];
+            floatx4 acc = zero4();
+            if (!deep) {
+                acc = mma(y[J][0], y[J][1], x[0], x[1], acc);
+            } else {
+                // pair by pair with e^{G_i - G_j}, node j's values from lane j of the row of 16
+                const rsrc_t xr = TT::q(t) ? qr_ : kr_;
+                floatx4 xi[2], kj[2];
 #pragma unroll
-        for (int m = 0; m < 2; ++m) {
-            const float* pm = part + m * 4 * 320 + x;
-            s[m] = (pm[0] + pm[320]) + (pm[640] + pm[960]);
-        }
-        diag[j * 20 + i] = on && i != j ? sbeta[i] * s[0] : 0.f;
-        gqk[i * L::kLP + j] = on ? s[1] : 0.f;
-    } else if (deep_waves == 0) {
-        int tile = 0;
-#pragma unroll
-        for (int I = 0; I < NT; ++I) {
-            if (I >= nt) break;
-#pragma unroll
-            for (int J = 0; J <= I; ++J) {
-#pragma unroll
-                for (int s = 0; s < 2; ++s, ++tile) {
-                    if ((tile & 3) != w) continue;
-                    const floatx4 acc = gram(s ? Xq : Xk, 16 * I, Y, 16 * J, 0, kHeadDim, l16, g);
-                    const int j = 16 * J + l16;
-                    floatx4 x;
+                for (int c = 0; c < 2; ++c) {
+                    xi[c] = widen(E::load4(xr, at_kq + 16 * I * row_b + 16 * c * es));
+                    kj[c] = widen(E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es));
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        const int i = 16 * I + 4 * g + e;
-                        const bool on = ((anc[i] >> j) & 1) && (s || j != i);
-                        x[e] = on ? (s ? acc[e] : sbeta[i] * acc[e]) : 0.f;
-                        if (s || J < I) (s ? gqk : gkk)[i * L::kLP + j] = x[e];
-                    }
-                    if (!s && J == I) *reinterpret_cast<floatx4*>(diag + j * 20 + 4 * g) = x;
-                }
-            }
-        }
-    } else {
-        // pair by pair: e^{G_i - G_j} for the channels out of range
-        for (int pr = tid; pr < 256 * nt * nt; pr += 256) {
-            const int i = pr / (16 * nt), j = pr % (16 * nt);
-            float skk = 0.f, sqk = 0.f;
-            if (i < n && ((anc[i] >> j) & 1)) {
-                for (int c = 0; c < kHeadDim; ++c) {
-                    if ((deep_waves >> (c >> 5)) & 1) {
-                        const uint32_t at_i = i * row_b + c * es, at_j = j * row_b + c * es;
-                        const float kd = finite_or_0(to_f32(E::load1(kr_, at_j))) *
-                                         exp_t<T>(Y.get_f32(i, c) - Y.get_f32(j, c));
-                        skk += finite_or_0(to_f32(E::load1(kr_, at_i))) * kd;
-                        sqk += to_f32(E::load1(qr_, at_i)) * kd;
-                    } else {
-                        const float y = Y.get(j, c);
-                        skk += Xk.get(i, c) * y;
-                        sqk += Xq.get(i, c) * y;
+                        if (!TT::q(t)) xi[c][e] = finite_or_0(xi[c][e]);
+                        kj[c][e] = finite_or_0(kj[c][e]);
                     }
                 }
+                for (int j = 0; j < 16; ++j) {
+                    const int src = (lane & 48) | j;
+                    float s = 0.f;
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const floatx4 gi = y[I][c].as_f32(), gj = y[J][c].as_f32();
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            s += xi[c][e] * (__shfl(kj[c][e], src, 64) * exp_t<T>(gi[e] - __shfl(gj[e], src, 64)));
+                    }
+                    s += __shfl_xor(s, 16, 64);
+                    s += __shfl_xor(s, 32, 64);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (4 * g + e == j) acc[e] = s;
+                }
             }
-            skk = i == j ? 0.f : sbeta[i] * skk;
-            gkk[i * L::kLP + j] = skk;
-            if ((i ^ j) < 16) diag[j * 20 + (i & 15)] = skk;
-            gqk[i * L::kLP + j] = sqk;
-        }
-    }
+            part[(u() * 4 + w) * 64 + lane] = acc;
+        });
+        __syncthreads();
+        // summed by wavefront t % 4; masked by ancestry, rows of k k scaled by beta
+        each<count>([&](auto u) {
+            constexpr int t = t0 + u();
+            constexpr int I = TT::row(t), J = TT::col(t);
+            if ((t & 3) != w || I >= nt) return;
+            const floatx4* p = part + u() * 256 + lane;
+            floatx4 x = (p[0] + p[64]) + (p[128] + p[192]);
+            const Mask m = __shfl(mask, 16 * I + l16, 64) >> (16 * J + 4 * g);   // node i = 16 I + l16
+            const float scale = TT::q(t) ? 1.f : __shfl(bt, 16 * I + l16, 64);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool on = ((m >> e) & 1) && (TT::q(t) || I != J || 4 * g + e != l16);
+                x[e] = on ? scale * x[e] : 0.f;
+            }
+            O* to = gram + TT::place(TT::q(t), I, J) * 64;
+            to[lane] = t < NT ? O::f32(x) : O::of(x);
+            if (t < NT && !L::kOver) {
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+                invert(reinterpret_cast<float*>(to), l16, g);
+            }
+        });
+    });
 
     // ---- held and read: X S, this wavefront's columns -----------------------
     floatx4 held[NT][2], read[NT][2];
 #pragma unroll
     for (int r = 0; r < NT; ++r) held[r][0] = held[r][1] = read[r][0] = read[r][1] = zero4();
+    if (L::kOver) {
+        __syncthreads();   // the last round has been summed
+        put_rows(Xk, xk);
+        if (!L::kTurns) put_rows(Xq, xq);
+        if (w < nt) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
+        __syncthreads();
+    }
+    if (L::kOver) load_v();   // (registers are free only now)
+    StateOp<T> so[4][2];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
-        state_product<NT>(Xk, 32 * kb, st[kb], held, nt, l16, g);
-        state_product<NT>(Xq, 32 * kb, st[kb], read, nt, l16, g);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) so[kb][t] = StateOp<T>::of(st[kb], t);
+        state_product<NT>(Xk, 32 * kb, so[kb], held, nt, l16, g);
+        if (!L::kTurns) state_product<NT>(Xq, 32 * kb, so[kb], read, nt, l16, g);
     }
-    __syncthreads();
-
-    // ---- inverses of the unit lower triangular diagonal blocks I + L: wavefront w that of block w, lane =
-    // column, column by column (once x[j] is final it leaves all later rows)
-    if (w < nt && g == 0) {
-        const float* Lw = diag + 16 * w * 20;   // [column][row]
-        float x[16];
+    if (L::kTurns) {
+        __syncthreads();
+        put_rows(Xq, xq);
+        __syncthreads();
 #pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] = r == l16 ? 1.f : 0.f;
-#pragma unroll
-        for (int j = 0; j < 16; ++j) {
-            inv[(16 * w + j) * 20 + l16] = x[j];
-#pragma unroll
-            for (int r4 = (j + 1) / 4; r4 < 4; ++r4) {
-                const floatx4 c = *reinterpret_cast<const floatx4*>(Lw + j * 20 + 4 * r4);
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (4 * r4 + e > j) x[4 * r4 + e] -= c[e] * x[j];
-            }
-        }
+        for (int kb = 0; kb < 4; ++kb) state_product<NT>(Xq, 32 * kb, so[kb], read, nt, l16, g);
+    } else if (!L::kOver) {
+        __syncthreads();   // (the Gram tiles are there)
     }
-    __syncthreads();
 
     // ---- pseudo-values and outputs, block by block --------------------------
     bad_node = bad[0] | bad[1] | bad[2] | bad[3];
@@ -605,31 +657,44 @@ __global__ __launch_bounds__(256, NT == 1 ? 3 : (NT == 2 ? 2 : 1)) void tree_dec
         }
     }
     const bool tainted = __any((bad_col[0] | bad_col[1]) != 0);
+    O uo[NT][2];   // pseudo-values as operands
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         if (I >= nt) break;
         const floatx4 bt4 = *reinterpret_cast<const floatx4*>(sbeta + 16 * I + 4 * g);
-        const floatx4 ia = frag_k16(inv + (16 * I + l16) * 20, 0, g);
+        const floatx4 ia = gram[TT::place(false, I, I) * 64 + lane].as_f32();
+        floatx4 prev[2] = {zero4(), zero4()};
+        auto tile = [&](bool q, int J) { return gram[TT::place(q, I, J) * 64 + lane]; };
+#pragma unroll
+        for (int J = 0; J + 1 < I; J += 2) {
+            const O a0 = tile(false, J), a1 = tile(false, J + 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) prev[t] = mma(a0, a1, uo[J][t], uo[J + 1][t], prev[t]);
+        }
+        if (I & 1) {
+            const O a0 = tile(false, I - 1);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) prev[t] = mma(a0, uo[I - 1][t], prev[t]);
+        }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             floatx4 rhs;
 #pragma unroll
             for (int e = 0; e < 4; ++e) rhs[e] = bt4[e] * ((float)vv[I][e][t] - held[I][t][e]);
-            if (I > 0) {
-                floatx4 prev = zero4();
-#pragma unroll
-                for (int J = 0; J < I; ++J)
-                    prev = mma_f32_k16(frag_k16(gkk + (16 * I + l16) * L::kLP, 16 * J, g), held[J][t], prev);
-                rhs -= prev;
-            }
-            held[I][t] = mma_f32_k16(ia, rhs, zero4());
+            if (I > 0) rhs -= prev[t];
+            uo[I][t] = O::of(mma_f32_k16(ia, rhs, zero4()));
         }
         floatx4 out[2] = {zero4(), zero4()};
 #pragma unroll
-        for (int J = 0; J <= I; ++J) {
-            const floatx4 am = frag_k16(gqk + (16 * I + l16) * L::kLP, 16 * J, g);
+        for (int J = 0; J < I; J += 2) {
+            const O a0 = tile(true, J), a1 = tile(true, J + 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) out[t] = mma_f32_k16(am, held[J][t], out[t]);
+            for (int t = 0; t < 2; ++t) out[t] = mma(a0, a1, uo[J][t], uo[J + 1][t], out[t]);
+        }
+        if (!(I & 1)) {
+            const O a0 = tile(true, I);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) out[t] = mma(a0, uo[I][t], out[t]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) out[t] += read[I][t];
