@@ -33,7 +33,7 @@
 // before it.
 #include "kda_device.h"
 #include "kda_launch.h"
-#include "kda_tree.h"
+#include "kda_tree_device.h"
 
 namespace kda {
 

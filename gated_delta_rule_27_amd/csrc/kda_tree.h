@@ -78,15 +78,4 @@ inline int64_t tree_prologue_waves(int32_t B, int32_t N, int32_t H) {
     return (int64_t)B * ((N + 7) / 8) * (3 * ((H + 1) / 2) + (H + 3) / 4);
 }
 
-// parent of node i of sequence b, -1 for the cached state
-__device__ __forceinline__ int tree_parent(const int32_t* parent, int64_t b, int N, int i) {
-    const int p = parent ? parent[b * N + i] : i - 1;
-    return p >= 0 && p < i ? p : -1;
-}
-// nodes of sequence b
-__device__ __forceinline__ int tree_count(const int32_t* n_node, int64_t b, int N) {
-    const int n = n_node ? n_node[b] : N;
-    return n < 0 ? 0 : (n > N ? N : n);
-}
-
 }  // namespace kda

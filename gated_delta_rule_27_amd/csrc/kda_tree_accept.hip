@@ -20,7 +20,7 @@
 // rounding of the running sum must not move.
 #include "kda.h"
 #include "kda_device.h"
-#include "kda_tree.h"
+#include "kda_tree_device.h"
 
 namespace kda {
 

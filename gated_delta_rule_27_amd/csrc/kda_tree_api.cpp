@@ -17,11 +17,11 @@ namespace {
 
 constexpr uint64_t kMaxUnits = (uint64_t)std::numeric_limits<int32_t>::max();
 
-// B sequences of N nodes with H heads, one workgroup per (sequence, head) at
-// the most
+// B sequences of N nodes with H heads; twice as many workgroups as (sequence,
+// head) pairs at the most
 bool tree_shape(int32_t B, int32_t N, int32_t H, int32_t most) {
     if (B < 0 || N < 1 || N > most || H < 1 || H > KDA_MAX_HEADS) return false;
-    if ((uint64_t)B * (uint64_t)H > kMaxUnits) return false;
+    if ((uint64_t)B * (uint64_t)H > kMaxUnits / 2) return false;
     return (uint64_t)B * (uint64_t)N * (uint64_t)H <= kMaxElems / kda::kHeadDim;
 }
 

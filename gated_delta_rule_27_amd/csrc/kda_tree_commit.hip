@@ -11,14 +11,19 @@
 // Everything is fp32 on fp32 MFMA: the state is fp32 and carries every
 // rounding on to the tokens after it.
 //
-// Mapping.  One workgroup of four wavefronts per (sequence, head); wavefront
-// w owns value columns 32 w .. 32 w + 31 over all 128 rows.  The state stays
-// in its registers from the one read to the one write; a lane's rows
-// 16 kb + 4 g + 0..3 of two columns are at once the B operand of X S and the
-// accumulator of the update.
+// Mapping.  One workgroup of four wavefronts per (sequence, head) (two heads
+// of eight wavefronts stream whole 128 KB blocks but wait for each other:
+// 543 us against 490 for 256 x 96 states).  Before the state is touched
+// wavefront w owns key channels 32 w .. 32 w + 31 of the tokens, a lane 4
+// channels of one token at a time: the running sums are DPP scans along the
+// 16 lanes of a row, and the rows are at once the operands of X Y^T, whose
+// parts are summed through LDS.  Then it owns value columns 32 w .. 32 w + 31
+// over all 128 rows: the state stays in its registers from the one read to
+// the one write, and a lane's rows 16 kb + 4 g + 0..3 of two columns are both
+// the operand of X S and the accumulator of the update.
 #include "kda.h"
 #include "kda_device.h"
-#include "kda_tree.h"
+#include "kda_tree_device.h"
 
 namespace kda {
 
@@ -26,7 +31,8 @@ namespace {
 
 constexpr int kTok = 16;              // path tokens of a block
 constexpr int kXP = kHeadDim + 4;     // a token row in LDS
-constexpr int kTP = kTok + 4;         // a channel row of tokens in LDS
+constexpr int kStream = 2;            // states pass the caches by (the non-temporal policy)
+typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 __device__ __forceinline__ floatx2 pair(const bf16* p) {
@@ -34,21 +40,53 @@ __device__ __forceinline__ floatx2 pair(const bf16* p) {
     return floatx2{(float)a[0], (float)a[1]};
 }
 __device__ __forceinline__ floatx2 pair(const float* p) { return *reinterpret_cast<const floatx2*>(p); }
+__device__ __forceinline__ floatx4 four(const bf16* p) {
+    const bf16x4 a = *reinterpret_cast<const bf16x4*>(p);
+    return floatx4{(float)a[0], (float)a[1], (float)a[2], (float)a[3]};
+}
+__device__ __forceinline__ floatx4 four(const float* p) { return *reinterpret_cast<const floatx4*>(p); }
 
-// The last three inputs of (history, path inputs) for this head: a thread
-// holds 16 bytes of channels of one of q, k, v.  Each reads all it needs
-// before it writes.
+// Entries of the path that are applied: to the first one that is no node.
+__device__ __forceinline__ int path_length(const TreeCommitArgs& a, int64_t b, int lane) {
+    const int32_t* path = a.path + (size_t)b * a.P;
+    const int most = tree_count(a.n_path, b, a.P);
+    int m = 0;
+    while (m < most) {
+        const bool ok = m + lane < most && (unsigned)path[m + lane] < (unsigned)a.N;
+        const uint64_t bad = ~__ballot(ok);
+        if (bad) {
+            m += __builtin_ctzll(bad);
+            break;
+        }
+        m += 64;
+    }
+    return __builtin_amdgcn_readfirstlane(m);
+}
+
+// The last three inputs of (history, path inputs): a workgroup of its own
+// per kHistHeads heads of a sequence, a thread 16 bytes of channels of one of
+// q, k, v.  Each reads all it needs before it writes.
 template <typename T>
-__device__ __forceinline__ void commit_history(const TreeCommitArgs& a, int64_t b, int h,
-                                               const int32_t* path, int m, int tid) {
-    constexpr int M = Vec16<T>::N, kV = kHeadDim / M;
+struct History {
+    static constexpr int M = Vec16<T>::N, kV = kHeadDim / M;      // threads per head and tensor
+    static constexpr int kHeads = 256 / (3 * kV);
+};
+template <typename T>
+__device__ __forceinline__ void commit_history(const TreeCommitArgs& a, int64_t wg) {
     typedef typename Vec16<T>::type vec;
-    if (tid >= 3 * kV) return;
-    const int tensor = tid / kV, c = (tid % kV) * M;
+    constexpr int kV = History<T>::kV, kHeads = History<T>::kHeads;
+    const int groups = (a.H + kHeads - 1) / kHeads;
+    const int64_t b = wg / groups;
+    const int m = path_length(a, b, threadIdx.x & 63);
+    const int hh = threadIdx.x / (3 * kV), rest = threadIdx.x % (3 * kV);
+    const int h = (int)(wg % groups) * kHeads + hh;
+    if (m == 0 || hh >= kHeads || h >= a.H) return;
+    const int tensor = rest / kV, c = (rest % kV) * History<T>::M;
     const size_t HD = (size_t)a.H * kHeadDim, at = (size_t)h * kHeadDim + c;
     const T* x = static_cast<const T*>(tensor == 0 ? a.x[0] : (tensor == 1 ? a.x[1] : a.x[2])) +
                  (size_t)b * a.N * HD + at;
     T* hist = static_cast<T*>(a.state) + ((size_t)b * 3 + tensor) * 3 * HD + at;
+    const int32_t* path = a.path + (size_t)b * a.P;
     vec row[3];
 #pragma unroll
     for (int p = 0; p < 3; ++p) {
@@ -59,173 +97,189 @@ __device__ __forceinline__ void commit_history(const TreeCommitArgs& a, int64_t 
     for (int p = 0; p < 3; ++p) *reinterpret_cast<vec*>(hist + p * HD) = row[p];
 }
 
-template <typename T>
-__global__ __launch_bounds__(256) void tree_commit_kernel(TreeCommitArgs a) {
-    __shared__ __attribute__((aligned(16))) float X[kTok * kXP];
-    __shared__ __attribute__((aligned(16))) float Y[kTok * kXP];
-    __shared__ __attribute__((aligned(16))) float KT[kHeadDim * kTP];    // (k o e^{G_e - G})^T
-    __shared__ __attribute__((aligned(16))) float gam[kHeadDim];         // e^{G_e}
-    __shared__ __attribute__((aligned(16))) float part[4][kTok * kTP];   // X Y^T by channel quarter
-    __shared__ __attribute__((aligned(16))) float Ls[kTok * kTP];
-    __shared__ __attribute__((aligned(16))) float inv[4][kTok * kTP];    // a copy per wavefront
-    __shared__ __attribute__((aligned(16))) float sbeta[kTok];
-    __shared__ int32_t node[kTok];
+// LDS of one state
+struct __attribute__((aligned(16))) CommitLds {
+    float X[kTok * kXP];        // k o e^G
+    float K[kTok * kXP];        // k o e^{G_e - G}
+    float gam[kHeadDim];        // e^{G_e}
+    floatx4 part[4][64];        // transposed X Y^T over a wavefront's channels
+    float inv[4][kTok * kTok];  // (I + L)^{-1}, a copy per wavefront
+};
 
+// kLong: paths of more than one block.  (Where a path is one block at most
+// there is no loop for the state's registers to be copied around.)
+template <typename T, bool kLong>
+__global__ __launch_bounds__(256, kLong ? 2 : 4) void tree_commit_kernel(TreeCommitArgs a, int32_t units) {
+    __shared__ CommitLds lds;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = a.H, N = a.N;
+    if ((int)blockIdx.x >= units) {
+        commit_history<T>(a, (int)blockIdx.x - units);
+        return;
+    }
     const int64_t b = blockIdx.x / (unsigned)H;
     const int h = blockIdx.x % (unsigned)H;
     const int32_t* path = a.path + (size_t)b * a.P;
-
-    // the path's length: to the first entry that is no node
-    const int most = tree_count(a.n_path, b, a.P);
-    int m = 0;
-    while (m < most) {
-        const bool ok = m + lane < most && (unsigned)path[m + lane] < (unsigned)N;
-        const uint64_t bad = ~__ballot(ok);
-        if (bad) {
-            m += __builtin_ctzll(bad);
-            break;
-        }
-        m += 64;
-    }
-    m = __builtin_amdgcn_readfirstlane(m);
+    const int m = path_length(a, b, lane);
     if (m == 0) return;
-    if (a.state) commit_history<T>(a, b, h, path, m, tid);
 
     const size_t HD = (size_t)H * kHeadDim;
     const size_t base = ((size_t)b * N * H + h) * kHeadDim;   // node 0's row; nodes are HD apart
-    const T* k = static_cast<const T*>(a.k) + base;
-    const T* v = static_cast<const T*>(a.v) + base;
-    const T* la = static_cast<const T*>(a.log_alpha) + base;
+    const T* k = static_cast<const T*>(a.k) + base + 32 * w + 4 * g;
+    const T* la = static_cast<const T*>(a.log_alpha) + base + 32 * w + 4 * g;
     const T* beta = static_cast<const T*>(a.beta) + (size_t)b * N * H + h;
     const int c0 = 32 * w + 2 * l16;
-    float* S = a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim) + (size_t)(4 * g) * kHeadDim + c0;
+    const T* v = static_cast<const T*>(a.v) + base + c0;
+    const rsrc_t S = make_rsrc_u32(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim), kHeadDim * kHeadDim * 4);
+    const int at_s = (4 * g * kHeadDim + c0) * 4;
 
-    floatx2 st[8][4];   // rows 16 kb + 4 g + e, columns c0, c0 + 1
+    // a block's inputs; tokens past the path are zeros (and change nothing)
+    floatx4 kr[2], lr[2];
+    floatx2 vr[4];
+    float bt[4];
+    auto load_block = [&](int t0) {
+        const int left = m - t0;
+        const int node = path[t0 + min(l16, left - 1)];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            kr[t] = four(k + node * HD + 16 * t);
+            lr[t] = four(la + node * HD + 16 * t);
+            if (l16 >= left) kr[t] = lr[t] = zero4();
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int t = 4 * g + e;
+            const int nd = __shfl(node, t, 64);   // (lanes 0..15 hold the block's nodes)
+            vr[e] = pair(v + nd * HD);
+            bt[e] = to_f32(beta[(size_t)nd * H]);
+            if (t >= left) {
+                vr[e] = floatx2{0.f, 0.f};
+                bt[e] = 0.f;
+            }
+        }
+    };
+    load_block(0);
+    floatx2 st[8][4];   // rows 16 kb + 4 g + e of columns c0, c0 + 1
 #pragma unroll
     for (int kb = 0; kb < 8; ++kb)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            st[kb][e] = __builtin_nontemporal_load(
-                reinterpret_cast<const floatx2*>(S + (16 * kb + e) * kHeadDim));
+            st[kb][e] = __builtin_bit_cast(
+                floatx2, __builtin_amdgcn_raw_buffer_load_b64(S, at_s + e * kHeadDim * 4, kb * 16 * kHeadDim * 4,
+                                                              kStream));
+    __builtin_amdgcn_sched_barrier(0);
+    auto store_rows = [&](int kb) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2_t, st[kb][e]), S,
+                                                  at_s + e * kHeadDim * 4, kb * 16 * kHeadDim * 4, kStream);
+    };
 
-    for (int t0 = 0; t0 < m; t0 += kTok) {
-        const int cnt = min(kTok, m - t0);
-        __syncthreads();   // the block before is no longer read
-        // ---- scaled rows: two threads per channel ---------------------------
-        {
-            const int c = tid & (kHeadDim - 1);
-            float gs[kTok], kx[kTok];
-#pragma unroll
-            for (int t = 0; t < kTok; ++t) {
-                const size_t row = t < cnt ? (size_t)path[t0 + t] * HD : 0;
-                gs[t] = t < cnt ? to_f32(la[row + c]) : 0.f;
-                kx[t] = t < cnt ? to_f32(k[row + c]) : 0.f;
-            }
-#pragma unroll
-            for (int t = 1; t < kTok; ++t) gs[t] += gs[t - 1];
-            if (tid < kHeadDim) {
-#pragma unroll
-                for (int t = 0; t < kTok; ++t) X[t * kXP + c] = kx[t] * expf(gs[t]);
-                gam[c] = expf(gs[kTok - 1]);
-            } else {
-#pragma unroll
-                for (int t = 0; t < kTok; ++t) {
-                    Y[t * kXP + c] = kx[t] * expf(-gs[t]);
-                    KT[c * kTP + t] = kx[t] * expf(gs[kTok - 1] - gs[t]);
-                }
-            }
-            if (tid < kTok) {
-                const int i = path[t0 + min(tid, cnt - 1)];
-                node[tid] = i;
-                sbeta[tid] = tid < cnt ? to_f32(beta[(size_t)i * H]) : 0.f;
-            }
+    for (int t0 = 0; t0 < (kLong ? m : 1); t0 += kTok) {
+        if (t0 > 0) {
+            load_block(t0);
+            __syncthreads();   // the block before is no longer read
         }
+        // ---- scaled rows; lane = token l16, channels 32 w + 16 t + 4 g + e ---
+        floatx4 xt = zero4();
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int c = 32 * w + 16 * t + 4 * g;
+            floatx4 x, y, kk, gm;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float G = row_prefix_sum(lr[t][e]), ex = exp_f32(G);
+                x[e] = kr[t][e] * ex;
+                y[e] = kr[t][e] * exp_f32(-G);
+                kk[e] = kr[t][e] * exp_f32(row_bcast<15>(G) - G);
+                gm[e] = row_bcast<15>(ex);
+            }
+            *reinterpret_cast<floatx4*>(lds.X + l16 * kXP + c) = x;
+            *reinterpret_cast<floatx4*>(lds.K + l16 * kXP + c) = kk;
+            if (l16 == 0) *reinterpret_cast<floatx4*>(lds.gam + c) = gm;
+            xt = mma_f32_k16(y, x, xt);   // rows: token j = 4 g + e, column: token i = l16
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        lds.part[w][lane] = xt;
         __syncthreads();
-        // ---- X Y^T, a quarter of the channels per wavefront -----------------
+        // ---- (I + L)^{-1}: every wavefront its own copy ----------------------
         {
-            floatx4 acc = zero4();
+            const floatx4* p = &lds.part[0][lane];
+            floatx4 x = (p[0] + p[64]) + (p[128] + p[192]);
+            // row i's beta: beta of token l16, held by group l16 / 4
+            float bi = 0.f;
 #pragma unroll
-            for (int kb = 0; kb < 32; kb += 16)
-                acc = mma_f32_k16(frag_k16(X + l16 * kXP, 32 * w + kb, g),
-                                  frag_k16(Y + l16 * kXP, 32 * w + kb, g), acc);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[w][(4 * g + e) * kTP + l16] = acc[e];
-        }
-        __syncthreads();
-        {
-            const int i = tid >> 4, j = tid & 15, x = i * kTP + j;
-            Ls[x] = j < i ? sbeta[i] * ((part[0][x] + part[1][x]) + (part[2][x] + part[3][x])) : 0.f;
-        }
-        __syncthreads();
-        // ---- (I + L)^{-1}: lane = column, the four groups of 16 alike -------
-        {
-            float x[kTok];
-#pragma unroll
-            for (int r = 0; r < kTok; ++r) {
-                float s = r == l16 ? 1.f : 0.f;
-#pragma unroll
-                for (int j = 0; j < r; ++j) s -= Ls[r * kTP + j] * x[j];
-                x[r] = s;
+            for (int e = 0; e < 4; ++e) {
+                const float be = __shfl(bt[e], 16 * (l16 >> 2), 64);
+                if ((l16 & 3) == e) bi = be;
             }
-            // (the four groups write the same values)
 #pragma unroll
-            for (int r = 0; r < kTok; ++r) inv[w][r * kTP + l16] = x[r];
+            for (int e = 0; e < 4; ++e) x[e] = 4 * g + e < l16 ? bi * x[e] : 0.f;
+            float* tile = lds.inv[w];   // element (i, j): lane 16 (j / 4) + i, j % 4
+            *reinterpret_cast<floatx4*>(tile + lane * 4) = x;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            invert(tile, l16, g);
         }
-        // ---- held = X S and the pseudo-values -------------------------------
-        floatx2 vv[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) vv[e] = pair(v + node[4 * g + e] * HD + c0);
+        __builtin_amdgcn_sched_barrier(0);
+        // ---- held = X S and the pseudo-values ---------------------------
         floatx4 u[2] = {zero4(), zero4()};
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb) {
-            const floatx4 xa = frag_k16(X + l16 * kXP, 16 * kb, g);
+            const floatx4 xa = frag_k16(lds.X + l16 * kXP, 16 * kb, g);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
                 u[t] = mma_f32_k16(xa, floatx4{st[kb][0][t], st[kb][1][t], st[kb][2][t], st[kb][3][t]}, u[t]);
         }
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-        const floatx4 bt = *reinterpret_cast<const floatx4*>(sbeta + 4 * g);
-        const floatx4 ia = frag_k16(inv[w] + l16 * kTP, 0, g);
+        const floatx4 ia = *reinterpret_cast<const floatx4*>(lds.inv[w] + lane * 4);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             floatx4 rhs;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) rhs[e] = bt[e] * (vv[e][t] - u[t][e]);
+            for (int e = 0; e < 4; ++e) rhs[e] = bt[e] * (vr[e][t] - u[t][e]);
             u[t] = mma_f32_k16(ia, rhs, zero4());
         }
-        // ---- S <- Diag(e^{G_e}) S + (k o e^{G_e - G})^T u --------------------
+        // ---- S <- Diag(e^{G_e}) S + (k o e^{G_e - G})^T u ----------------
 #pragma unroll
         for (int kb = 0; kb < 8; ++kb) {
-            const floatx4 gm = *reinterpret_cast<const floatx4*>(gam + 16 * kb + 4 * g);
-            const floatx4 ka = frag_k16(KT + (16 * kb + l16) * kTP, 0, g);
+            const floatx4 gm = *reinterpret_cast<const floatx4*>(lds.gam + 16 * kb + 4 * g);
+            floatx4 ka;   // channel 16 kb + l16 of tokens 4 g + e
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ka[e] = lds.K[(4 * g + e) * kXP + 16 * kb + l16];
+            floatx4 acc[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                floatx4 acc;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[e] = gm[e] * st[kb][e][t];
-                acc = mma_f32_k16(ka, u[t], acc);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) st[kb][e][t] = acc[e];
+                for (int e = 0; e < 4; ++e) acc[t][e] = gm[e] * st[kb][e][t];
+                acc[t] = mma_f32_k16(ka, u[t], acc[t]);
             }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) st[kb][e] = floatx2{acc[0][e], acc[1][e]};
+            if (!kLong) store_rows(kb);
+            __builtin_amdgcn_sched_barrier(0);   // (few rows in flight between the two layouts)
         }
     }
+    if (kLong) {
 #pragma unroll
-    for (int kb = 0; kb < 8; ++kb)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-            __builtin_nontemporal_store(st[kb][e], reinterpret_cast<floatx2*>(S + (16 * kb + e) * kHeadDim));
+        for (int kb = 0; kb < 8; ++kb) store_rows(kb);
+    }
+}
+
+template <typename T>
+hipError_t launch_t(const TreeCommitArgs& a, hipStream_t stream) {
+    const int64_t units = (int64_t)a.B * a.H;
+    const int64_t hist = a.state ? (int64_t)a.B * ((a.H + History<T>::kHeads - 1) / History<T>::kHeads) : 0;
+    const dim3 grid((unsigned)(units + hist)), block(256);
+    if (a.P > kTok) tree_commit_kernel<T, true><<<grid, block, 0, stream>>>(a, (int32_t)units);
+    else tree_commit_kernel<T, false><<<grid, block, 0, stream>>>(a, (int32_t)units);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_tree_commit(const TreeCommitArgs& a, int dtype, hipStream_t stream) {
-    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
-    if (dtype == 0) tree_commit_kernel<float><<<grid, block, 0, stream>>>(a);
-    else tree_commit_kernel<bf16><<<grid, block, 0, stream>>>(a);
-    return hipGetLastError();
+    return dtype == 0 ? launch_t<float>(a, stream) : launch_t<bf16>(a, stream);
 }
 
 }  // namespace kda

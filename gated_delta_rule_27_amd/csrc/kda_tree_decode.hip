@@ -43,7 +43,7 @@
 
 #include "kda.h"
 #include "kda_device.h"
-#include "kda_tree.h"
+#include "kda_tree_device.h"
 
 namespace kda {
 
@@ -274,35 +274,13 @@ __device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], M m, int 
 }
 
 // e^x: for bf16 results the hardware's 2^x (x log2 e rounds to |x| 2^-24, at
-// |x| <= 64 some 2^-18 of the result), for fp32 the library's
+// |x| <= 64 some 2^-18 of the result), for fp32 with the remainder put back
 template <typename T>
 __device__ __forceinline__ float exp_t(float x) { return __expf(x); }
 template <>
-__device__ __forceinline__ float exp_t<float>(float x) { return expf(x); }
+__device__ __forceinline__ float exp_t<float>(float x) { return exp_f32(x); }
 
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
-// (I + L)^{-1} of a strictly lower triangular tile in place; element (i, j)
-// lies at lane 16 (j / 4) + i, j % 4.  One lane per column, row by row.
-__device__ __forceinline__ void invert(float* tile, int l16, int g) {
-    if (g != 0) return;
-    float x[16];
-    x[0] = l16 == 0 ? 1.f : 0.f;
-#pragma unroll
-    for (int r = 1; r < 16; ++r) {
-        float s = r == l16 ? 1.f : 0.f;
-#pragma unroll
-        for (int jq = 0; jq < (r + 3) / 4; ++jq) {
-            const floatx4 c = *reinterpret_cast<const floatx4*>(tile + (16 * jq + r) * 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (4 * jq + e < r) s -= c[e] * x[4 * jq + e];
-        }
-        x[r] = s;
-    }
-#pragma unroll
-    for (int r = 0; r < 16; ++r) tile[(16 * (l16 >> 2) + r) * 4 + (l16 & 3)] = x[r];
-}
-
 // f(0), ..., f(N - 1) with the index a constant expression
 template <typename F, int... I>
 __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
