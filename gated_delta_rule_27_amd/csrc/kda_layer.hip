@@ -96,12 +96,18 @@ template <>
 struct Raw4<bf16> {
     bf16x4 v;
     __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const bf16x4*>(p); }
+    __device__ __forceinline__ void stream(const bf16* p) {   // read once: past the caches
+        v = __builtin_nontemporal_load(reinterpret_cast<const bf16x4*>(p));
+    }
     __device__ __forceinline__ float operator[](int e) const { return (float)v[e]; }
 };
 template <>
 struct Raw4<float> {
     floatx4 v;
     __device__ __forceinline__ void load(const float* p) { v = *reinterpret_cast<const floatx4*>(p); }
+    __device__ __forceinline__ void stream(const float* p) {
+        v = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(p));
+    }
     __device__ __forceinline__ float operator[](int e) const { return v[e]; }
 };
 // tokens of loads in flight per lane of the convolution kernel
@@ -116,6 +122,9 @@ template <>
 struct Raw8<bf16> {
     bf16x8 v;
     __device__ __forceinline__ void load(const bf16* p) { v = *reinterpret_cast<const bf16x8*>(p); }
+    __device__ __forceinline__ void stream(const bf16* p) {
+        v = __builtin_nontemporal_load(reinterpret_cast<const bf16x8*>(p));
+    }
     __device__ __forceinline__ float operator[](int e) const { return (float)v[e]; }
 };
 template <>
@@ -124,6 +133,10 @@ struct Raw8<float> {
     __device__ __forceinline__ void load(const float* p) {
         a = *reinterpret_cast<const floatx4*>(p);
         b = *reinterpret_cast<const floatx4*>(p + 4);
+    }
+    __device__ __forceinline__ void stream(const float* p) {
+        a = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(p));
+        b = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(p + 4));
     }
     __device__ __forceinline__ float operator[](int e) const { return e < 4 ? a[e] : b[e - 4]; }
 };
@@ -560,44 +573,67 @@ __global__ __launch_bounds__(256) void epilogue_kernel(EpilogueArgs a) {
 }
 
 // ---- the prologue over a tree of drafted tokens ------------------------------
-// Waves as in prologue_kernel (gate waves: 4 heads; convolution waves: one
-// of q, k, v and 2 heads), each over kTreeNodes nodes of one sequence.  A
-// node's window is itself and its three nearest ancestors, then the end of
-// the cached history; its four rows are read where they lie, so a row is
-// read once from memory and up to three times more from the caches (its
-// descendants sit in the same or a neighbouring wave).  Lane i holds node
-// i's parent, so walking up is a lane read.  The arithmetic is token()'s of
-// prologue_conv, operation by operation: a chain gives its bits.
-constexpr int kTreeNodes = 8;
+// One workgroup per slice (2 heads of q, k or v for the convolution, 4 heads
+// for the gates) and group of sequences.  A node's window is itself and its
+// three nearest ancestors, then the end of the cached history: the four
+// wavefronts bring a sequence's rows (history, then nodes) into LDS, each row
+// read once from memory, and share out the nodes, whose windows are four LDS
+// reads; lane i holds node i's parent, so walking up is a lane read.  The
+// next sequence's rows are in flight meanwhile, and the convolution taps stay
+// in registers over the group (they are as many bytes as eight rows).  The
+// arithmetic is token()'s of prologue_conv, operation by operation: a chain
+// gives its bits.
+__device__ __forceinline__ void stream4(float* p, const float (&x)[4]) {
+    __builtin_nontemporal_store(floatx4{x[0], x[1], x[2], x[3]}, reinterpret_cast<floatx4*>(p));
+}
+__device__ __forceinline__ void stream4(bf16* p, const float (&x)[4]) {
+    const bf16x4 a = {(bf16)x[0], (bf16)x[1], (bf16)x[2], (bf16)x[3]};   // RNE
+    __builtin_nontemporal_store(__builtin_bit_cast(uintx2_t, a), reinterpret_cast<uintx2_t*>(p));
+}
 
-template <typename TIn>
-__device__ __forceinline__ void tree_conv(const TreePrologueArgs& a, int64_t b, int i0, int n,
-                                          int task, int lane) {
+__device__ __forceinline__ void stream8(float* p, const float (&x)[8]) {
+    __builtin_nontemporal_store(floatx4{x[0], x[1], x[2], x[3]}, reinterpret_cast<floatx4*>(p));
+    __builtin_nontemporal_store(floatx4{x[4], x[5], x[6], x[7]}, reinterpret_cast<floatx4*>(p + 4));
+}
+__device__ __forceinline__ void stream8(bf16* p, const float (&x)[8]) {
+    bf16x8 a;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = (bf16)x[e];   // RNE
+    __builtin_nontemporal_store(__builtin_bit_cast(uintx4_t, a), reinterpret_cast<uintx4_t*>(p));
+}
+
+// NR: rows of a wavefront, 4 NR >= N + 3
+template <typename TIn, int NR>
+__device__ __forceinline__ void tree_conv(const TreePrologueArgs& a, int b0, int b1, int task,
+                                          unsigned char* lds, int wave, int lane) {
     const int HD = a.H * kHeadDim;
     const int nslice = (a.H + 1) / 2;
     const int tensor = task / nslice, slice = task % nslice;
     const int h = 2 * slice + (lane >> 5), c4 = 4 * (lane & 31);
     const bool live = h < a.H;
     const int hc = live ? h * kHeadDim + c4 : c4;
-    const TIn* x = static_cast<const TIn*>(a.x[tensor]) + (size_t)b * a.N * HD;
-    TIn* out = static_cast<TIn*>(a.out[tensor]) + (size_t)b * a.N * HD;
-    const TIn* hist = a.state ? static_cast<const TIn*>(a.state) + ((size_t)b * 3 + tensor) * kHist * HD
-                              : nullptr;
-    const int par = lane < n ? tree_parent(a.parent, b, a.N, lane) : -1;
+    // (rows of 64 pieces of 4 channels; row 3 + i is node i, rows 0..2 the history)
+    Raw4<TIn>* rows = reinterpret_cast<Raw4<TIn>*>(lds) + lane;
 
-    Raw4<TIn> row[kTreeNodes][kConvW];   // [..][j]: the input j steps up
-    bool zero[kTreeNodes][kConvW];       // (before the history: zero)
+    Raw4<TIn> cur[NR];
+    int n = 0, par = -1;
+    auto load = [&](int b) {
+        n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
+        par = lane < n ? tree_parent(a.parent, b, a.N, lane) : -1;
+        const TIn* x = static_cast<const TIn*>(a.x[tensor]) + (size_t)b * a.N * HD + hc;
+        const TIn* hist = static_cast<const TIn*>(a.state) + ((size_t)b * 3 + tensor) * kHist * HD + hc;
 #pragma unroll
-    for (int u = 0; u < kTreeNodes; ++u) {
-        int at = min(i0 + u, n - 1);
-#pragma unroll
-        for (int j = 0; j < kConvW; ++j) {
-            const TIn* src = at >= 0 ? x + (size_t)at * HD : (hist ? hist + (kHist + at) * HD : x);
-            zero[u][j] = at < 0 && !hist;
-            row[u][j].load(src + hc);
-            at = at >= 0 ? __builtin_amdgcn_readlane(par, at) : at - 1;
+        for (int j = 0; j < NR; ++j) {
+            const int r = wave + 4 * j;
+            if (r < kHist) {
+                if (a.state) cur[j].load(hist + (size_t)r * HD);
+                else cur[j] = Raw4<TIn>{};   // zero history
+            } else if (r - kHist < n) {
+                cur[j].stream(x + (size_t)(r - kHist) * HD);
+            }
         }
-    }
+    };
+    load(b0);
     float w[kConvW][4];
     {
         const float* wp = a.conv_w + ((size_t)tensor * HD + hc) * kConvW;
@@ -608,87 +644,119 @@ __device__ __forceinline__ void tree_conv(const TreePrologueArgs& a, int64_t b, 
             for (int j = 0; j < kConvW; ++j) w[j][e] = t[j];
         }
     }
+    for (int b = b0; b < b1; ++b) {
+        if (b > b0) __syncthreads();   // the rows before are no longer read
 #pragma unroll
-    for (int u = 0; u < kTreeNodes; ++u) {
-        if (i0 + u >= n) break;
-        float y[4], ss = 0.f;
+        for (int j = 0; j < NR; ++j)
+            if (wave + 4 * j < n + kHist) rows[(wave + 4 * j) * 64] = cur[j];
+        __syncthreads();
+        const int nn = n, pp = par;
+        if (b + 1 < b1) load(b + 1);
+        TIn* out = static_cast<TIn*>(a.out[tensor]) + (size_t)b * a.N * HD + hc;
+        for (int i = wave; i < nn; i += 4) {
+            Raw4<TIn> in[kConvW];   // [j]: the input j steps up
+            int at = i;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            float in[kConvW];
+            for (int j = 0; j < kConvW; ++j) {
+                in[j] = rows[(kHist + at) * 64];
+                at = at >= 0 ? __builtin_amdgcn_readlane(pp, at) : at - 1;
+            }
+            float y[4], ss = 0.f;
 #pragma unroll
-            for (int j = 0; j < kConvW; ++j) in[j] = zero[u][j] ? 0.f : row[u][j][e];
-            const float c = __builtin_fmaf(
-                w[3][e], in[0],
-                __builtin_fmaf(w[2][e], in[1], __builtin_fmaf(w[1][e], in[2], w[0][e] * in[3])));
-            y[e] = c * sigmoid(c);
-            ss = __builtin_fmaf(y[e], y[e], ss);
+            for (int e = 0; e < 4; ++e) {
+                const float c = __builtin_fmaf(
+                    w[3][e], in[0][e],
+                    __builtin_fmaf(w[2][e], in[1][e],
+                                   __builtin_fmaf(w[1][e], in[2][e], w[0][e] * in[3][e])));
+                y[e] = c * sigmoid(c);
+                ss = __builtin_fmaf(y[e], y[e], ss);
+            }
+            if (tensor < 2) {
+                const float r = __builtin_amdgcn_rsqf(row32_sum(ss) + a.l2_eps);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= r;
+            }
+            if (live) stream4(out + (size_t)i * HD, y);
         }
-        if (tensor < 2) {
-            const float r = __builtin_amdgcn_rsqf(row32_sum(ss) + a.l2_eps);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] *= r;
-        }
-        if (live) store4(out + (size_t)(i0 + u) * HD + hc, y);
     }
 }
 
 template <typename TIn>
-__device__ __forceinline__ void tree_gate(const TreePrologueArgs& a, int64_t b, int i0, int n,
-                                          int slice, int lane) {
+__device__ __forceinline__ void tree_gate(const TreePrologueArgs& a, int b0, int b1, int slice,
+                                          int wave, int lane) {
+    constexpr int kU = 4;   // nodes of a wavefront in flight
     const int HD = a.H * kHeadDim;
     const int h = 4 * slice + (lane >> 4), c8 = 8 * (lane & 15);
     const bool live = h < a.H;
     const int hc = live ? h * kHeadDim + c8 : c8;
-    const size_t row0 = (size_t)b * a.N;
-    const TIn* x = static_cast<const TIn*>(a.x[3]) + row0 * HD;
-    TIn* out = static_cast<TIn*>(a.out[3]) + row0 * HD;
-    const TIn* braw = static_cast<const TIn*>(a.b_raw) + row0 * a.H;
-    TIn* beta = static_cast<TIn*>(a.beta) + row0 * a.H;
-    Raw8<TIn> xv[kTreeNodes];
-    TIn bv[kTreeNodes];
-#pragma unroll
-    for (int u = 0; u < kTreeNodes; ++u) {
-        const int i = min(i0 + u, n - 1);
-        xv[u].load(x + (size_t)i * HD + hc);
-        bv[u] = braw[(size_t)i * a.H + (live ? h : 0)];
-    }
     float bias[8];
     load8(a.a_bias + hc, bias);
+    for (int b = b0; b < b1; ++b) {
+        const size_t row0 = (size_t)b * a.N;
+        const TIn* x = static_cast<const TIn*>(a.x[3]) + row0 * HD + hc;
+        TIn* out = static_cast<TIn*>(a.out[3]) + row0 * HD + hc;
+        const TIn* braw = static_cast<const TIn*>(a.b_raw) + row0 * a.H + (live ? h : 0);
+        TIn* beta = static_cast<TIn*>(a.beta) + row0 * a.H + (live ? h : 0);
+        const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
+        for (int i0 = wave; i0 < n; i0 += 4 * kU) {
+            Raw8<TIn> xv[kU];
+            TIn bv[kU];
 #pragma unroll
-    for (int u = 0; u < kTreeNodes; ++u) {
-        const int i = i0 + u;
-        if (i >= n) break;
-        float y[8];
+            for (int u = 0; u < kU; ++u) {
+                const int i = min(i0 + 4 * u, n - 1);
+                xv[u].stream(x + (size_t)i * HD);
+                bv[u] = braw[(size_t)i * a.H];
+            }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = -5.f * sigmoid(xv[u][e] + bias[e]);
-        if (live) {
-            store8(out + (size_t)i * HD + hc, y);
-            if (c8 == 0) beta[(size_t)i * a.H + h] = from_f32<TIn>(sigmoid(to_f32(bv[u])));
+            for (int u = 0; u < kU; ++u) {
+                const int i = i0 + 4 * u;
+                if (i >= n) break;
+                float y[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) y[e] = -5.f * sigmoid(xv[u][e] + bias[e]);
+                if (live) {
+                    stream8(out + (size_t)i * HD, y);
+                    if (c8 == 0) beta[(size_t)i * a.H] = from_f32<TIn>(sigmoid(to_f32(bv[u])));
+                }
+            }
         }
     }
 }
 
-template <typename TIn>
-__global__ __launch_bounds__(256) void tree_prologue_kernel(TreePrologueArgs a, int64_t waves) {
+template <typename TIn, int NR>
+__global__ __launch_bounds__(256) void tree_prologue_kernel(TreePrologueArgs a, int per) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int64_t wid = (int64_t)blockIdx.x * 4 + wave;
-    if (wid >= waves) return;
-    const int conv = 3 * ((a.H + 1) / 2), per = conv + (a.H + 3) / 4;
-    const int nb = (a.N + kTreeNodes - 1) / kTreeNodes;
-    const int task = (int)(wid % per);
-    const int64_t blk = wid / per, b = blk / nb;
-    const int i0 = (int)(blk % nb) * kTreeNodes;
-    const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
-    if (i0 >= n) return;
-    if (task < conv) tree_conv<TIn>(a, b, i0, n, task, lane);
-    else tree_gate<TIn>(a, b, i0, n, task - conv, lane);
+    const int conv = 3 * ((a.H + 1) / 2), tasks = conv + (a.H + 3) / 4;
+    const int task = blockIdx.x % (unsigned)tasks;
+    const int b0 = (int)(blockIdx.x / (unsigned)tasks) * per;
+    const int b1 = min(b0 + per, a.B);
+    if (task < conv) tree_conv<TIn, NR>(a, b0, b1, task, lds, wave, lane);
+    else tree_gate<TIn>(a, b0, b1, task - conv, wave, lane);
+}
+
+template <typename TIn, int NR>
+hipError_t launch_tree_prologue_n(const TreePrologueArgs& a, hipStream_t stream) {
+    const int per = tree_prologue_sequences(a.B, a.H);
+    const int64_t tasks = tree_prologue_tasks(a.H);
+    const int bytes = (a.N + kHist) * 64 * (int)sizeof(Raw4<TIn>);
+    const auto kern = tree_prologue_kernel<TIn, NR>;
+    if (bytes > 64 * 1024) {
+        static std::atomic<uint64_t> done{0};
+        const hipError_t e = raise_lds_limit_once(reinterpret_cast<const void*>(kern),
+                                                  (kMaxTree + kHist) * 64 * (int)sizeof(Raw4<TIn>), done);
+        if (e != hipSuccess) return e;
+    }
+    kern<<<dim3((unsigned)(tasks * ((a.B + per - 1) / per))), dim3(256), bytes, stream>>>(a, per);
+    return hipGetLastError();
 }
 
 template <typename TIn>
 hipError_t launch_tree_prologue_t(const TreePrologueArgs& a, hipStream_t stream) {
-    const int64_t waves = tree_prologue_waves(a.B, a.N, a.H);
-    tree_prologue_kernel<TIn><<<dim3((unsigned)((waves + 3) / 4)), dim3(256), 0, stream>>>(a, waves);
-    return hipGetLastError();
+    if (a.N + kHist <= 12) return launch_tree_prologue_n<TIn, 3>(a, stream);
+    if (a.N + kHist <= 20) return launch_tree_prologue_n<TIn, 5>(a, stream);
+    if (a.N + kHist <= 36) return launch_tree_prologue_n<TIn, 9>(a, stream);
+    return launch_tree_prologue_n<TIn, 17>(a, stream);
 }
 
 template <typename TIn>

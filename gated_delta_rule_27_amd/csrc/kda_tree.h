@@ -72,10 +72,14 @@ hipError_t launch_tree_decode(const TreeDecodeArgs& a, int dtype, hipStream_t st
 hipError_t launch_tree_accept(const TreeAcceptArgs& a, int dtype, hipStream_t stream);
 hipError_t launch_tree_commit(const TreeCommitArgs& a, int dtype, hipStream_t stream);
 
-// Waves of the tree prologue: per sequence and 8 nodes, q, k, v x two-head
-// slices and the gates' four-head slices.
-inline int64_t tree_prologue_waves(int32_t B, int32_t N, int32_t H) {
-    return (int64_t)B * ((N + 7) / 8) * (3 * ((H + 1) / 2) + (H + 3) / 4);
+// Workgroups of the tree prologue per group of sequences: q, k, v x two-head
+// slices, then the gates' four-head slices.
+inline int64_t tree_prologue_tasks(int32_t H) { return 3 * (((int64_t)H + 1) / 2) + ((int64_t)H + 3) / 4; }
+// Sequences of a group: more than one once there are workgroups enough (256
+// sequences of 16 nodes x 96 heads: 200, 181, 180, 185 us at 1, 2, 4, 8).
+inline int32_t tree_prologue_sequences(int32_t B, int32_t H) {
+    const int64_t n = (int64_t)B * tree_prologue_tasks(H) / 2048;
+    return n < 1 ? 1 : (n > 4 ? 4 : (int32_t)n);
 }
 
 }  // namespace kda

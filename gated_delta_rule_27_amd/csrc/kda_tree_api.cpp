@@ -45,7 +45,6 @@ kda_status kda_tree_prologue(const void* xq, const void* xk, const void* xv, con
                              void* beta, hipStream_t stream) {
     if (!valid_dtype(dt)) return KDA_ERR_BAD_DTYPE;
     if (!tree_shape(B, N, H, KDA_MAX_TREE) || D != kda::kHeadDim) return KDA_ERR_BAD_SHAPE;
-    if ((uint64_t)kda::tree_prologue_waves(B, N, H) > kMaxUnits * 4u) return KDA_ERR_BAD_SHAPE;
     if (!(l2_eps >= 0.f) || l2_eps > std::numeric_limits<float>::max()) return KDA_ERR_BAD_SHAPE;
     if (B > 0 && (!xq || !xk || !xv || !a_raw || !b_raw || !conv_w || !a_bias || !q || !k || !v ||
                   !log_alpha || !beta))
