@@ -141,9 +141,15 @@ def _check(code):
         raise KDAError(code, kda_status_str(code))
 
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _dtype_code(t):
@@ -631,9 +637,15 @@ MAX_PATH = 1 << 24     # KDA_MAX_PATH
 
 def _need(t, name, shape, dtype, device):
     """A tensor argument of the tree calls: shape, dtype, device, contiguous;
-    its address, or None for one that is not given."""
+    its address, or None for one that is not given.  (One test when all is
+    well: these calls are a few microseconds of GPU work at batch 1.)"""
     if t is None:
         return None
+    try:
+        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -642,21 +654,20 @@ def _need(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} like the first argument (got {t.device})")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name, dim):
-    """The argument the others are measured by: its shape, dtype and device."""
+    """The argument the others are measured by: its shape, dtype, device and
+    dtype code."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dim() != dim:
         raise ValueError(f"{name} must have {dim} dimensions (got {tuple(t.shape)})")
-    if t.device.type != "cuda":
-        raise ValueError(f"{name} must be on a ROCm device (got {t.device})")
-    _dtype_code(t)
-    return t.shape, t.dtype, t.device
+    device = t.device
+    if device.type != "cuda":
+        raise ValueError(f"{name} must be on a ROCm device (got {device})")
+    return t.shape, t.dtype, device, _dtype_code(t)
 
 
 def _required(**named):
@@ -668,11 +679,13 @@ def _required(**named):
 def _on_device(device, fn, *args):
     """fn(*args, stream) with `device` current: the launch then goes to the
     device of the stream, whichever device the caller has current."""
-    cuda = _torch().cuda
-    if device.index == cuda.current_device():
-        return fn(*args, cuda.current_stream(device).cuda_stream)
-    with cuda.device(device):
-        return fn(*args, cuda.current_stream(device).cuda_stream)
+    torch = _torch()
+    index = device.index
+    if index == torch.cuda.current_device():
+        # (the address that torch.cuda.current_stream(index).cuda_stream holds, without the object)
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
+    with torch.cuda.device(device):
+        return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
 def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_node=None,
@@ -689,7 +702,7 @@ def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_n
     are not written (`out` may supply the five tensors)."""
     torch = _torch()
     _required(xq=xq, xk=xk, xv=xv, a_raw=a_raw, b_raw=b_raw, conv_w=conv_w, a_bias=a_bias)
-    shape, dt, dev = _first(xq, "xq", 4)
+    shape, dt, dev, code = _first(xq, "xq", 4)
     B, N, H, D = shape
     i32, f32 = torch.int32, torch.float32
     ins = [_need(xq, "xq", shape, dt, dev),
@@ -701,13 +714,11 @@ def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_n
     hist = _need(conv_state, "conv_state", (B, 3, 3, H, D), dt, dev)
     if out is None:
         out = tuple(torch.empty_like(xq) for _ in range(4)) + (torch.empty_like(b_raw),)
-    elif len(out) != 5:
+    elif len(out) != 5 or any(t is None for t in out):
         raise ValueError("out must be (q, k, v, log_alpha, beta)")
-    _required(**{f"out[{i}]": t for i, t in enumerate(out)})
-    outs = [_need(t, f"out[{i}]", shape if i < 4 else (B, N, H), dt, dev)
-            for i, t in enumerate(out)]
-    _check(_on_device(dev, lib().kda_tree_prologue, *ins, B, N, H, D, _dtype_code(xq), hist,
-                      float(l2_eps), *outs))
+    outs = [_need(t, "out", shape, dt, dev) for t in out[:4]]
+    _check(_on_device(dev, lib().kda_tree_prologue, *ins, B, N, H, D, code, hist, float(l2_eps),
+                      *outs, _need(out[4], "out[4]", (B, N, H), dt, dev)))
     return tuple(out)
 
 
@@ -722,7 +733,7 @@ def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=
     or past n_node[b] are not written."""
     torch = _torch()
     _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, S=S)
-    shape, dt, dev = _first(q, "q", 4)
+    shape, dt, dev, code = _first(q, "q", 4)
     B, N, H, D = shape
     ins = [_need(q, "q", shape, dt, dev), _need(k, "k", shape, dt, dev),
            _need(v, "v", shape, dt, dev), _need(log_alpha, "log_alpha", shape, dt, dev),
@@ -732,7 +743,7 @@ def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=
            _need(n_node, "n_node", (B,), torch.int32, dev)]
     if o is None:
         o = torch.empty_like(q)
-    _check(_on_device(dev, lib().kda_tree_decode, *ins, B, N, H, D, D, _dtype_code(q),
+    _check(_on_device(dev, lib().kda_tree_decode, *ins, B, N, H, D, D, code,
                       _need(o, "o", shape, dt, dev)))
     return o
 
@@ -758,19 +769,18 @@ def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_p
     for any tree."""
     torch = _torch()
     _required(p=p, tokens=tokens, u=u)
-    shape, dt, dev = _first(p, "p", 3)
+    shape, dt, dev, code = _first(p, "p", 3)
     B, N, V = shape
     i32 = torch.int32
     ins = [_need(p, "p", shape, dt, dev), _need(q, "q", (B, max(N - 1, 0), V), dt, dev),
            _need(tokens, "tokens", (B, N), i32, dev), _need(parent, "parent", (B, N), i32, dev),
            _need(n_node, "n_node", (B,), i32, dev), _need(u, "u", (B, N), torch.float32, dev)]
     if path is None:
-        path = torch.empty((B, N), dtype=i32, device=dev)
+        path = torch.empty_like(tokens)
     if n_path is None:
-        n_path = torch.empty((B,), dtype=i32, device=dev)
+        n_path = tokens.new_empty(B)
     if next_token is None:
-        next_token = torch.empty((B,), dtype=i32, device=dev)
-    code = _dtype_code(p)
+        next_token = tokens.new_empty(B)
     if workspace is None:
         size = lib().kda_tree_accept_workspace_size(B, N, V, code)
         workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
@@ -799,7 +809,7 @@ def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
     Returns S."""
     torch = _torch()
     _required(k=k, v=v, log_alpha=log_alpha, beta=beta, S=S, path=path)
-    shape, dt, dev = _first(k, "k", 4)
+    shape, dt, dev, code = _first(k, "k", 4)
     B, N, H, D = shape
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
         raise ValueError("path must be an int32 tensor [B, P]")
@@ -818,7 +828,7 @@ def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
         _required(**dict(zip(names, conv)))
         hist = [_need(t, name, shape if i < 3 else (B, 3, 3, H, D), dt, dev)
                 for i, (name, t) in enumerate(zip(names, conv))]
-    _check(_on_device(dev, lib().kda_tree_commit, *ins, B, N, P, H, D, D, _dtype_code(k), *hist))
+    _check(_on_device(dev, lib().kda_tree_commit, *ins, B, N, P, H, D, D, code, *hist))
     return S
 
 
