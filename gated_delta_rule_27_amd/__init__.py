@@ -111,11 +111,8 @@ def lib():
             [vp] * 6
         L.kda_tree_decode.restype = ctypes.c_int
         L.kda_tree_decode.argtypes = [vp] * 8 + [i32, i32, i32, i32, i32, ctypes.c_int, vp, vp]
-        L.kda_tree_accept_workspace_size.restype = sz
-        L.kda_tree_accept_workspace_size.argtypes = [i32, i32, i32, ctypes.c_int]
         L.kda_tree_accept.restype = ctypes.c_int
-        L.kda_tree_accept.argtypes = [vp] * 6 + [i32, i32, i32, ctypes.c_int, vp, vp, vp, vp, sz,
-                                                 vp]
+        L.kda_tree_accept.argtypes = [vp] * 6 + [i32, i32, i32, ctypes.c_int, vp, vp, vp, vp]
         L.kda_tree_commit.restype = ctypes.c_int
         L.kda_tree_commit.argtypes = [vp] * 7 + [i32, i32, i32, i32, i32, i32, ctypes.c_int] + \
             [vp] * 5
@@ -748,12 +745,8 @@ def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=
     return o
 
 
-def kda_tree_accept_workspace_size(B, N, V, dtype=KDA_F32):
-    return lib().kda_tree_accept_workspace_size(int(B), int(N), int(V), int(dtype))
-
-
 def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_path=None,
-                    next_token=None, workspace=None):
+                    next_token=None):
     """The accepted path and the next token of drafted trees (node 0 the
     pending token, accepted by definition).
 
@@ -781,18 +774,10 @@ def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_p
         n_path = tokens.new_empty(B)
     if next_token is None:
         next_token = tokens.new_empty(B)
-    if workspace is None:
-        size = lib().kda_tree_accept_workspace_size(B, N, V, code)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev) if size else None
-    else:
-        _dev(workspace, "workspace")
-        _same_device(dev, workspace=workspace)
-    ws = (None, 0) if workspace is None else (workspace.data_ptr(),
-                                              workspace.numel() * workspace.element_size())
     _check(_on_device(dev, lib().kda_tree_accept, *ins, B, N, V, code,
                       _need(path, "path", (B, N), i32, dev),
                       _need(n_path, "n_path", (B,), i32, dev),
-                      _need(next_token, "next_token", (B,), i32, dev), *ws))
+                      _need(next_token, "next_token", (B,), i32, dev)))
     return path, n_path, next_token
 
 
@@ -838,5 +823,5 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_
            "kda_chunk_bwd_noalloc", "BWD_NOALLOC_MAX_BYTES",
            "kda_chunk_fwd_workspace_size", "kda_status_str", "kda_abi_version", "KDAError",
            "kda_tree_prologue", "kda_tree_decode", "kda_tree_accept",
-           "kda_tree_accept_workspace_size", "kda_tree_commit", "MAX_TREE", "MAX_VOCAB",
+           "kda_tree_commit", "MAX_TREE", "MAX_VOCAB",
            "MAX_PATH", "lib", "LIB_PATH"]

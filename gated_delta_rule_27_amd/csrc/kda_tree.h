@@ -50,7 +50,6 @@ struct TreeAcceptArgs {
     int32_t* path;             // [B, N]
     int32_t* n_path;           // [B]
     int32_t* next_token;       // [B]
-    void* workspace;
 };
 
 struct TreeCommitArgs {

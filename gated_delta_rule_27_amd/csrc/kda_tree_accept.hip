@@ -38,20 +38,28 @@ __device__ __forceinline__ double lane_value(double x, int lane) {
     v.w[1] = __builtin_amdgcn_readlane(v.w[1], lane);
     return v.d;
 }
-__device__ __forceinline__ double wave_sum(double x) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) x += __shfl_xor(x, off, 64);
+// x of the lane that the data-parallel move `kCtrl` names, 0 where it names
+// none or the lane's row of 16 is not in kRows
+template <int kCtrl, int kRows>
+__device__ __forceinline__ double moved(double x) {
+    union { double d; int w[2]; } v;
+    v.d = x;
+    v.w[0] = __builtin_amdgcn_update_dpp(0, v.w[0], kCtrl, kRows, 0xf, false);
+    v.w[1] = __builtin_amdgcn_update_dpp(0, v.w[1], kCtrl, kRows, 0xf, false);
+    return v.d;
+}
+// inclusive prefix sum over the lanes: along the rows of 16 (shifts by 1, 2,
+// 4, 8), then lane 15 of rows 0 and 2 to the row after, lane 31 to the upper half
+__device__ __forceinline__ double wave_scan(double x) {
+    x += moved<0x111, 0xf>(x);
+    x += moved<0x112, 0xf>(x);
+    x += moved<0x114, 0xf>(x);
+    x += moved<0x118, 0xf>(x);
+    x += moved<0x142, 0xa>(x);
+    x += moved<0x143, 0xc>(x);
     return x;
 }
-// inclusive prefix sum over the lanes
-__device__ __forceinline__ double wave_scan(double x, int lane) {
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off, 64);
-        if (lane >= off) x += y;
-    }
-    return x;
-}
+__device__ __forceinline__ double wave_sum(double x) { return lane_value(wave_scan(x), 63); }
 
 // 16 bytes of probabilities from an address that only its elements align
 // (rows of an odd vocabulary)
@@ -108,8 +116,8 @@ struct Residual {
             }
         }
     }
-    // the sum of a tile's weights, in every lane
-    __device__ __forceinline__ double tile_sum(int tile, int lane) const {
+    // this lane's part of a tile's sum
+    __device__ __forceinline__ double tile_part(int tile, int lane) const {
         constexpr int M = Vec16<T>::N;
         const bool with_q = kQ && c > 0.0;
         double s = 0.0;
@@ -120,7 +128,21 @@ struct Residual {
 #pragma unroll
             for (int e = 0; e < M; ++e) s += w[e];
         }
-        return wave_sum(s);
+        return s;
+    }
+    // f(tile, sum) for this wavefront's tiles, several in flight
+    template <typename F>
+    __device__ __forceinline__ void tile_sums(int wave, int lane, F&& f) const {
+        constexpr int kU = 2;
+        const int ntile = (V + kTile - 1) / kTile;
+        for (int t0 = wave; t0 < ntile; t0 += kU * kAcceptWaves) {
+            double s[kU];
+#pragma unroll
+            for (int u = 0; u < kU; ++u) s[u] = tile_part(t0 + u * kAcceptWaves, lane);
+#pragma unroll
+            for (int u = 0; u < kU; ++u)
+                if (t0 + u * kAcceptWaves < ntile) f(t0 + u * kAcceptWaves, wave_sum(s[u]));
+        }
     }
     // the first token of `tile` at which `base` plus the tile's running sum
     // passes `target`; where rounding leaves none, its last one with weight
@@ -139,7 +161,7 @@ struct Residual {
                 s += x[e];
             }
         }
-        const double incl = base + wave_scan(s, lane);
+        const double incl = base + wave_scan(s);
         double run = __shfl_up(incl, 1, 64);
         if (lane == 0) run = base;
         int first = -1, last = -1;
@@ -217,7 +239,7 @@ __global__ __launch_bounds__(64 * kAcceptWaves) void tree_accept_kernel(TreeAcce
                 res.c += Z;
                 if (todo) {
                     double s = 0.0;
-                    for (int t = wave; t < ntile; t += kAcceptWaves) s += res.tile_sum(t, lane);
+                    res.tile_sums(wave, lane, [&](int, double x) { s += x; });
                     __syncthreads();   // (part of the sum before is read)
                     if (lane == 0) part[wave] = s;
                     __syncthreads();
@@ -254,10 +276,9 @@ __global__ __launch_bounds__(64 * kAcceptWaves) void tree_accept_kernel(TreeAcce
 
     // the next token: from the residual, or from p where nothing is left
     for (int again = 0; again < 2; ++again) {
-        for (int t = wave; t < ntile; t += kAcceptWaves) {
-            const double s = res.tile_sum(t, lane);
-            if (lane == 0) tiles[t] = s;
-        }
+        res.tile_sums(wave, lane, [&](int t, double x) {
+            if (lane == 0) tiles[t] = x;
+        });
         __syncthreads();
         // every wavefront: the running sum over the tiles
         double total = 0.0;
@@ -270,7 +291,7 @@ __global__ __launch_bounds__(64 * kAcceptWaves) void tree_accept_kernel(TreeAcce
                 double base = 0.0, run = 0.0;
                 for (int t0 = 0; t0 < ntile && tile < 0; t0 += 64) {
                     const double s = t0 + lane < ntile ? tiles[t0 + lane] : 0.0;
-                    const double incl = run + wave_scan(s, lane);
+                    const double incl = run + wave_scan(s);
                     const uint64_t hit = __ballot(s > 0.0 && incl > target), any = __ballot(s > 0.0);
                     if (any) filled = t0 + 63 - __builtin_clzll(any);
                     if (hit) {

@@ -131,39 +131,27 @@ kda_status kda_tree_decode(const void* q, const void* k, const void* v, const vo
     return KDA_OK;
 }
 
-size_t kda_tree_accept_workspace_size(int32_t B, int32_t N, int32_t V, kda_dtype dt) {
-    (void)B;
-    (void)N;
-    (void)V;
-    (void)dt;
-    return 0;
-}
-
 kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
                            const int32_t* parent, const int32_t* n_node, const float* u,
                            int32_t B, int32_t N, int32_t V, kda_dtype dt, int32_t* path,
-                           int32_t* n_path, int32_t* next_token, void* workspace,
-                           size_t workspace_bytes, hipStream_t stream) {
+                           int32_t* n_path, int32_t* next_token, hipStream_t stream) {
     if (!valid_dtype(dt)) return KDA_ERR_BAD_DTYPE;
     if (B < 0 || N < 1 || N > KDA_MAX_TREE || V < 1 || V > KDA_MAX_VOCAB) return KDA_ERR_BAD_SHAPE;
     if (B > 0 && (!p || !tokens || !u || !path || !n_path || !next_token))
         return KDA_ERR_NULL_ARG;
-    if (!all_aligned({p, q, workspace}, 16) ||
+    if (!all_aligned({p, q}, 16) ||
         !all_aligned({tokens, parent, n_node, u, path, n_path, next_token}, 4))
         return KDA_ERR_MISALIGNED;
-    const size_t need = kda_tree_accept_workspace_size(B, N, V, dt);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return KDA_ERR_WORKSPACE;
 
     const uint64_t es = esize(dt), nodes = (uint64_t)B * N;
     const Span in[] = {span(p, nodes * V * es), span(q, (nodes - B) * V * es),
                        counts(tokens, nodes), counts(parent, nodes), counts(n_node, B),
                        span(u, nodes * 4)};
-    const Span out[] = {counts(path, nodes), counts(n_path, B), counts(next_token, B),
-                        span(workspace, need)};
-    for (int i = 0; i < 4; ++i) {
+    const Span out[] = {counts(path, nodes), counts(n_path, B), counts(next_token, B)};
+    for (int i = 0; i < 3; ++i) {
         for (const Span& s : in)
             if (overlaps(out[i], s)) return KDA_ERR_ALIAS;
-        for (int j = i + 1; j < 4; ++j)
+        for (int j = i + 1; j < 3; ++j)
             if (overlaps(out[i], out[j])) return KDA_ERR_ALIAS;
     }
     if (B == 0) return KDA_OK;
@@ -181,7 +169,6 @@ kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
     a.path = path;
     a.n_path = n_path;
     a.next_token = next_token;
-    a.workspace = workspace;
     if (kda::launch_tree_accept(a, (int)dt, stream) != hipSuccess) return KDA_ERR_DEVICE;
     return KDA_OK;
 }

@@ -482,22 +482,16 @@ kda_status kda_tree_decode(const void* q, const void* k, const void* v,
  * checked; a NaN or negative weight counts as 0, nothing out of range is
  * ever read or written, and the next token lies in [0, V)).
  * 1 <= V <= KDA_MAX_VOCAB.  p and q 16-byte aligned, the int32 and fp32
- * arrays 4-byte aligned.  The workspace (kda_tree_accept_workspace_size
- * bytes, 16-byte aligned; may be NULL when that is 0) need not be cleared;
- * calls that overlap in time need one each.  Any overlap of an output or
- * the workspace with another buffer is KDA_ERR_ALIAS.
+ * arrays 4-byte aligned.  Any overlap of an output with another buffer is
+ * KDA_ERR_ALIAS.
  */
 #define KDA_MAX_VOCAB (1 << 22)
-
-size_t kda_tree_accept_workspace_size(int32_t B, int32_t N, int32_t V,
-                                      kda_dtype dt);
 
 kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
                            const int32_t* parent, const int32_t* n_node,
                            const float* u, int32_t B, int32_t N, int32_t V,
                            kda_dtype dt, int32_t* path, int32_t* n_path,
-                           int32_t* next_token, void* workspace,
-                           size_t workspace_bytes, hipStream_t stream);
+                           int32_t* next_token, hipStream_t stream);
 
 /*
  * Moves cached states, and convolution histories, along one path of each

@@ -76,7 +76,7 @@ def test_tree_decode_refusals(L, kw, code):
 
 
 ACCEPT = dict(p=P(0), q=P(1), tokens=P(2), parent=P(3), n=P(4), u=P(5), B=4, N=8, V=1000, dt=F32,
-              path=P(6), m=P(7), next=P(8), ws=P(9), wsb=1 << 30, stream=None)
+              path=P(6), m=P(7), next=P(8), stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -86,7 +86,7 @@ ACCEPT = dict(p=P(0), q=P(1), tokens=P(2), parent=P(3), n=P(4), u=P(5), B=4, N=8
     (dict(p=None), NULL_ARG), (dict(tokens=None), NULL_ARG), (dict(u=None), NULL_ARG),
     (dict(path=None), NULL_ARG), (dict(m=None), NULL_ARG), (dict(next=None), NULL_ARG),
     (dict(p=P(0, 4)), MISALIGNED), (dict(q=P(1, 8)), MISALIGNED), (dict(u=P(5, 2)), MISALIGNED),
-    (dict(tokens=P(2, 1)), MISALIGNED), (dict(next=P(8, 2)), MISALIGNED), (dict(ws=P(9, 8)), MISALIGNED),
+    (dict(tokens=P(2, 1)), MISALIGNED), (dict(next=P(8, 2)), MISALIGNED),
     (dict(path=P(0)), ALIAS), (dict(path=P(2)), ALIAS), (dict(m=P(6)), ALIAS), (dict(next=P(7)), ALIAS),
     (dict(next=P(5)), ALIAS), (dict(m=P(4)), ALIAS), (dict(path=P(1, 16)), ALIAS),
     (dict(B=0, p=None, tokens=None), OK),
@@ -114,16 +114,6 @@ COMMIT = dict(k=P(0), v=P(1), la=P(2), beta=P(3), S=P(4), path=P(5), n=P(6), B=4
 ])
 def test_tree_commit_refusals(L, kw, code):
     assert call(L.kda_tree_commit, COMMIT, kw) == code
-
-
-def test_workspace_size_never_fails(L):
-    for B in (-5, 0, 1, 300, (1 << 31) - 1):
-        for N in (-1, 0, 1, 64, 1000):
-            for V in (-1, 0, 1, 160000, 1 << 22, (1 << 31) - 1):
-                for dt in (-1, 0, 1, 7):
-                    n = L.kda_tree_accept_workspace_size(B, N, V, dt)
-                    if B < 0 or not 1 <= N <= 64 or not 1 <= V <= 1 << 22 or dt not in (0, 1):
-                        assert n == 0, (B, N, V, dt, n)
 
 
 def meta(*shape, dtype=torch.float32):
