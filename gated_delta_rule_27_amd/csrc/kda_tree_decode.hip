@@ -333,11 +333,12 @@ struct TreeLds {
     static constexpr int kBytes = kBad + 4 * 8;
 };
 
-// Wavefronts per SIMD that the registers are cut for: what the LDS allows,
-// fp32 operands one less
+// Workgroups per CU that the registers are cut for: as many as fit without
+// spills (23 x 31 fp32 states, 21 nodes: 29.7 us at two, 26.3 at three).
 template <typename T, int NT>
 constexpr int tree_waves() {
-    return (NT == 1 ? 4 : (NT == 2 ? 3 : 2)) - (sizeof(T) == 4 ? 1 : 0);
+    constexpr bool wide = sizeof(T) == 4;
+    return NT == 1 ? (wide ? 3 : 4) : (NT == 2 ? 3 : (wide ? 1 : 2));
 }
 
 template <typename T, int NT>
@@ -495,6 +496,8 @@ __global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel
             } else {
                 y[I][t] = O::f32(GT[I][t]);
             }
+            // (one tile's conversions at a time: the registers are full)
+            if (L::kOver) __builtin_amdgcn_sched_barrier(0);
         }
     auto put_rows = [&](const Rows<T>& X, const O (&x)[NT][2]) {
 #pragma unroll
@@ -523,32 +526,32 @@ __global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel
             } else {
                 // pair by pair with e^{G_i - G_j}, node j's values from lane j of the row of 16
                 const rsrc_t xr = TT::q(t) ? qr_ : kr_;
-                floatx4 xi[2], kj[2];
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    xi[c] = widen(E::load4(xr, at_kq + 16 * I * row_b + 16 * c * es));
-                    kj[c] = widen(E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es));
+                for (int c = 0; c < 4; ++c) {   // (two channels at a time: the registers are full)
+                    const uint32_t off = at_kq + 16 * (c >> 1) * es + 2 * (c & 1) * es;
+                    const typename E::two x2 = E::load2(xr, off + 16 * I * row_b);
+                    const typename E::two k2 = E::load2(kr_, off + 16 * J * row_b);
+                    const floatx4 gi = y[I][c >> 1].as_f32(), gj = y[J][c >> 1].as_f32();
+                    float xi[2], kj[2];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        if (!TT::q(t)) xi[c][e] = finite_or_0(xi[c][e]);
-                        kj[c][e] = finite_or_0(kj[c][e]);
+                    for (int e = 0; e < 2; ++e) {
+                        xi[e] = TT::q(t) ? (float)x2[e] : finite_or_0((float)x2[e]);
+                        kj[e] = finite_or_0((float)k2[e]);
                     }
-                }
-                for (int j = 0; j < 16; ++j) {
-                    const int src = (lane & 48) | j;
-                    float s = 0.f;
+                    for (int j = 0; j < 16; ++j) {
+                        const int src = (lane & 48) | j;
+                        float s = 0.f;
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        const floatx4 gi = y[I][c].as_f32(), gj = y[J][c].as_f32();
+                        for (int e = 0; e < 2; ++e) {
+                            const int ge = 2 * (c & 1) + e;
+                            s += xi[e] * (__shfl(kj[e], src, 64) * exp_t<T>(gi[ge] - __shfl(gj[ge], src, 64)));
+                        }
+                        s += __shfl_xor(s, 16, 64);
+                        s += __shfl_xor(s, 32, 64);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            s += xi[c][e] * (__shfl(kj[c][e], src, 64) * exp_t<T>(gi[e] - __shfl(gj[e], src, 64)));
+                            if (4 * g + e == j) acc[e] += s;
                     }
-                    s += __shfl_xor(s, 16, 64);
-                    s += __shfl_xor(s, 32, 64);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (4 * g + e == j) acc[e] = s;
                 }
             }
             part[(u() * 4 + w) * 64 + lane] = acc;
