@@ -639,7 +639,8 @@ def _need(t, name, shape, dtype, device):
     if t is None:
         return None
     try:
-        if t.dtype is dtype and t.shape == shape and t.device == device and t.is_contiguous():
+        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
+                and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass

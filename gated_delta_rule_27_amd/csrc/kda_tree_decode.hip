@@ -180,6 +180,8 @@ __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const
     }
 }
 
+typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
+
 // Elements through a buffer resource of the sequence's nodes: 32-bit
 // offsets, and rows past the nodes read 0 and drop their stores.
 template <typename T>
@@ -193,12 +195,15 @@ struct Elems<bf16> {
         return __builtin_bit_cast(bf16x2, __builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
     }
     static __device__ __forceinline__ four load4(rsrc_t r, uint32_t off) { return buf_load_bf16x4(r, off); }
+    // the one of two that is not 0
+    static __device__ __forceinline__ four either(four a, four b) {
+        return __builtin_bit_cast(four, __builtin_bit_cast(uintx2_t, a) | __builtin_bit_cast(uintx2_t, b));
+    }
     static __device__ __forceinline__ void store2(rsrc_t r, uint32_t off, float x, float y) {   // RNE
         __builtin_amdgcn_raw_buffer_store_b32(
             __builtin_bit_cast(int, __builtin_convertvector((floatx2{x, y}), bf16x2)), r, (int)off, 0, 0);
     }
 };
-typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
 template <>
 struct Elems<float> {
     typedef floatx2 two;
@@ -211,6 +216,10 @@ struct Elems<float> {
     }
     static __device__ __forceinline__ four load4(rsrc_t r, uint32_t off) {
         return __builtin_bit_cast(floatx4, __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0));
+    }
+    static __device__ __forceinline__ four either(four a, four b) {
+        typedef unsigned int uintx4_t __attribute__((ext_vector_type(4)));
+        return __builtin_bit_cast(four, __builtin_bit_cast(uintx4_t, a) | __builtin_bit_cast(uintx4_t, b));
     }
     static __device__ __forceinline__ void store2(rsrc_t r, uint32_t off, float x, float y) {
         __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(uintx2_t, floatx2{x, y}), r, (int)off, 0, 0);
@@ -289,6 +298,36 @@ __device__ __forceinline__ void each(std::integer_sequence<int, I...>, F&& f) {
 template <int N, typename F>
 __device__ __forceinline__ void each(F&& f) {
     each(std::make_integer_sequence<int, N>{}, f);
+}
+
+// A (sequence, head)'s state columns c0, c0 + 1, rows 32 kb + 4 g + 0..3 and
+// 32 kb + 16 + 4 g + 0..3: read once, streamed past the caches
+__device__ __forceinline__ void load_state(const float* S, floatx2 (&st)[4][8], int g, int c0) {
+    const rsrc_t sr = make_rsrc_u32(S, kHeadDim * kHeadDim * 4);
+    const int at = (4 * g * kHeadDim + c0) * 4;
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            st[kb][e] = __builtin_bit_cast(
+                floatx2, __builtin_amdgcn_raw_buffer_load_b64(
+                             sr, at + (e & 3) * kHeadDim * 4, (32 * kb + 16 * (e >> 2)) * kHeadDim * 4, 2));
+}
+
+// Ancestor masks, lane = node, by doubling: a lane joins the mask of the node
+// it points at, then points where that node points.
+template <typename Mask>
+__device__ __forceinline__ Mask ancestors(int par, int lane, int nodes) {
+    Mask mask = lane < nodes ? (Mask)1 << (lane & (nodes - 1)) : 0;
+    while (__ballot(par >= 0)) {
+        const Mask pm = __shfl(mask, par < 0 ? lane : par, 64);
+        const int pp = __shfl(par, par < 0 ? lane : par, 64);
+        if (par >= 0) {
+            mask |= pm;
+            par = pp;
+        }
+    }
+    return mask;
 }
 
 // The Gram tiles (I, J <= I) of both matrices, in the order in which they
@@ -373,7 +412,7 @@ __global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel
     Mask* bad = reinterpret_cast<Mask*>(lds + L::kBad);
 
     // ---- everything this workgroup reads, in the order it is needed ---------
-    int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
+    const int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
     typename E::four lar[2][NT], kr[NT][2], qr[NT][2];
     const uint32_t at_g = 4 * g * row_b, at_l = l16 * row_b;
     const uint32_t at_kq = at_l + (32 * w + 4 * g) * es;
@@ -403,31 +442,10 @@ __global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel
     };
     if (!L::kOver) load_v();
     floatx2 st[4][8];
-    {
-        const rsrc_t sr = make_rsrc_u32(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim),
-                                        kHeadDim * kHeadDim * 4);
-        const int at = (4 * g * kHeadDim + c0) * 4;
-#pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
-#pragma unroll
-            for (int e = 0; e < 8; ++e)   // read once: streamed past the caches
-                st[kb][e] = __builtin_bit_cast(
-                    floatx2, __builtin_amdgcn_raw_buffer_load_b64(
-                                 sr, at + (e & 3) * kHeadDim * 4, (32 * kb + 16 * (e >> 2)) * kHeadDim * 4, 2));
-    }
+    load_state(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim), st, g, c0);
     __builtin_amdgcn_sched_barrier(0);
 
-    // ---- ancestor masks, lane = node, by doubling: a lane joins the mask of the node it points at, then
-    // points where that node points
-    Mask mask = lane < L::kN ? (Mask)1 << (lane & (L::kN - 1)) : 0;
-    while (__ballot(par >= 0)) {
-        const Mask pm = __shfl(mask, par < 0 ? lane : par, 64);
-        const int pp = __shfl(par, par < 0 ? lane : par, 64);
-        if (par >= 0) {
-            mask |= pm;
-            par = pp;
-        }
-    }
+    const Mask mask = ancestors<Mask>(par, lane, L::kN);
 
     // ---- G^T, scaled rows: this wavefront's 32 channels ----------------------
     Mask bad_node = (Mask)__ballot(!(bt - bt == 0.f));   // non-finite beta, log alpha, k
@@ -694,6 +712,218 @@ __global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel
     }
 }
 
+// Up to 8 nodes: k's rows and q's share one tile of 16, rows 0..7 and 8..15
+// (lane l16: node l16 % 8).  One product with the state gives what is held
+// (accumulator rows 0..7) and what is read (8..15), one Gram tile the
+// couplings of both, and the outputs accumulate onto the read rows: half the
+// operands, exponentials and matrix instructions of the general kernel.
+constexpr int kSmall = 8;
+
+template <typename T>
+struct __attribute__((aligned(16))) SmallLds {
+    unsigned char rows[16 * Rows<T>::kBytes];
+    floatx4 part[4][64];      // the wavefronts' parts of the Gram tile
+    Op<T> gram[64];           // rows 0..7 strictly lower k k, 8..15 lower q k
+    float inv[256];           // (I + L)^{-1}
+    float beta[16];
+    uint32_t anc[kSmall];
+    uint32_t bad[4];
+};
+
+template <typename T>
+__global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArgs a) {
+    using E = Elems<T>;
+    using O = Op<T>;
+    __shared__ SmallLds<T> lds;
+    const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
+    const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int H = a.H, N = a.N;
+    const int64_t b = blockIdx.x / (unsigned)H;
+    const int h = blockIdx.x % (unsigned)H;
+    const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, N));
+    if (n == 0) return;
+    constexpr uint32_t es = sizeof(T);
+    constexpr uint32_t kOut = 0xffffff00u;                    // an offset past every resource
+    const uint32_t row_b = (uint32_t)H * kHeadDim * es;       // from node to node
+    const size_t base = ((size_t)b * N * H + h) * kHeadDim;   // node 0's row
+    const uint32_t rows_b = (uint32_t)(n - 1) * row_b + kHeadDim * es;
+    auto rows = [&](const void* p) { return make_rsrc_u32(static_cast<const T*>(p) + base, rows_b); };
+    const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
+    const Rows<T> X(lds.rows, 16);
+    const bool isq = l16 >= kSmall;
+    const int i = l16 & (kSmall - 1);
+
+    // ---- everything this workgroup reads -------------------------------------
+    const int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
+    typename E::four lar[2][1], x[2];
+    {
+        const rsrc_t lr = rows(a.log_alpha), kr = rows(a.k), qr = rows(a.q);
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                lar[t][0][e] = E::load1(lr, (4 * g + e) * row_b + (32 * w + 16 * t + l16) * es);
+        // lanes of k and of q read 0 from the other's tensor
+        const uint32_t off = i * row_b + (32 * w + 4 * g) * es;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const typename E::four kx = E::load4(kr, (isq ? kOut : off) + 16 * t * es);
+            const typename E::four qx = E::load4(qr, (isq ? off : kOut) + 16 * t * es);
+            x[t] = E::either(kx, qx);
+        }
+    }
+    float bt = to_f32(E::load1(make_rsrc_u32(static_cast<const T*>(a.beta) + (size_t)b * N * H + h,
+                                             ((uint32_t)(n - 1) * H + 1) * es),
+                               (uint32_t)lane * H * es));
+    typename E::two vv[4];
+    {
+        const rsrc_t vr = rows(a.v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) vv[e] = E::load2(vr, (4 * g + e) * row_b + c0 * es);
+    }
+    floatx2 st[4][8];
+    load_state(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim), st, g, c0);
+    __builtin_amdgcn_sched_barrier(0);
+
+    const uint32_t mask = ancestors<uint32_t>(par, lane, kSmall);
+    uint32_t bad_node = (uint32_t)__ballot(!(bt - bt == 0.f));   // non-finite beta, log alpha, k
+    bt = finite_or_0(bt);
+    if (w == 0 && lane < 16) {
+        lds.beta[lane] = bt;   // (0 past the nodes)
+        if (lane < kSmall) lds.anc[lane] = mask;
+    }
+    {
+        float s = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) s = probe4(probe4(s, lar[t][0]), x[t]);
+        if (__any(s != 0.f)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float z = (float)lar[t][0][e];   // node 4 g + e
+                    uint64_t off = __ballot(!(z - z == 0.f));
+#pragma unroll
+                    for (int gg = 0; gg < 2; ++gg)
+                        if ((off >> (16 * gg)) & 0xffff) bad_node |= 1u << (4 * gg + e);
+                    lar[t][0][e] = (T)finite_or_0(z);
+                    z = (float)x[t][e];              // k of node l16; q's rows keep theirs to themselves
+                    off = __ballot(!isq && !(z - z == 0.f));
+                    off |= off >> 32;
+                    off |= off >> 16;
+                    bad_node |= (uint32_t)(off & 0xff);
+                    if (!isq) x[t][e] = (T)finite_or_0(z);
+                }
+        }
+    }
+    if (lane == 0) lds.bad[w] = bad_node;
+
+    // ---- G^T, scaled rows, this wavefront's part of the Gram tile -------------
+    const uint32_t m = __shfl(mask, i, 64);
+    floatx4 GT[2];
+    float least = 0.f;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        GT[t] = gather_decay<1>(lar[t], m, 0, g);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) least = fminf(least, GT[t][e]);
+    }
+    O xo[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        floatx4 ex;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[t][e]);
+        xo[t] = O::of(widen(x[t]) * ex);
+        X.put(l16, 32 * w + 16 * t + 4 * g, xo[t]);
+    }
+    // (8 levels at the decay bound: |G| <= 40 where the inputs keep their contract)
+    O y[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        floatx4 ex;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[t][e]);
+        y[t] = O::of(widen(x[t]) * ex);
+    }
+    lds.part[w][lane] = mma(y[0], y[1], xo[0], xo[1], zero4());
+    __syncthreads();
+
+    if (w == 0) {   // summed, masked, and the solve's inverse
+        const floatx4* p = &lds.part[0][lane];
+        floatx4 z = (p[0] + p[64]) + (p[128] + p[192]);
+        const float scale = isq ? 1.f : __shfl(bt, i, 64);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = 4 * g + e;
+            const bool on = ((m >> j) & 1) && (isq || j != i);
+            z[e] = on ? scale * z[e] : 0.f;
+        }
+        lds.gram[lane] = O::of(z);
+        *reinterpret_cast<floatx4*>(lds.inv + 4 * lane) = isq ? zero4() : z;
+        __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+        invert<kSmall>(lds.inv, l16, g);
+    }
+
+    // ---- held and read, this wavefront's columns ------------------------------
+    floatx4 acc[1][2] = {{zero4(), zero4()}};
+#pragma unroll
+    for (int kb = 0; kb < 4; ++kb) {
+        const StateOp<T> so[2] = {StateOp<T>::of(st[kb], 0), StateOp<T>::of(st[kb], 1)};
+        state_product<1>(X, 32 * kb, so, acc, 1, l16, g);
+    }
+    __syncthreads();
+
+    // ---- pseudo-values and outputs --------------------------------------------
+    bad_node = lds.bad[0] | lds.bad[1] | lds.bad[2] | lds.bad[3];
+    uint32_t bad_col[2] = {bad_node, bad_node};
+    {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s = probe(s, vv[e]);
+        if (__any(s != 0.f)) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                uint32_t z = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float u = (float)vv[e][t];
+                    vv[e][t] = (T)finite_or_0(u);
+                    z |= (u - u == 0.f ? 0u : 1u) << (4 * g + e);
+                }
+                z |= __shfl_xor(z, 16, 64);
+                z |= __shfl_xor(z, 32, 64);
+                bad_col[t] |= z;
+            }
+        }
+    }
+    const floatx4 bt4 = *reinterpret_cast<const floatx4*>(lds.beta + 4 * g);
+    const floatx4 ia = *reinterpret_cast<const floatx4*>(lds.inv + 4 * lane);
+    const O gm = lds.gram[lane];
+    floatx4 out[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        floatx4 rhs;   // (rows 8..15: beta is 0)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) rhs[e] = g < 2 ? bt4[e] * ((float)vv[e][t] - acc[0][t][e]) : 0.f;
+        out[t] = mma(gm, O::of(mma_f32_k16(ia, rhs, zero4())), acc[0][t]);
+    }
+    // rows 8..15 are the outputs of nodes 0..7
+    if (__any((bad_col[0] | bad_col[1]) != 0)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t z = lds.anc[(4 * g + e) & (kSmall - 1)];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (z & bad_col[t]) out[t][e] = __builtin_nanf("");
+        }
+    }
+    const rsrc_t orr = rows(a.o);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        E::store2(orr, g < 2 ? kOut : (4 * g + e - kSmall) * row_b + c0 * es, out[0][e], out[1][e]);
+}
+
 template <typename T, int NT>
 hipError_t launch_nt(const TreeDecodeArgs& a, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
@@ -709,6 +939,10 @@ hipError_t launch_nt(const TreeDecodeArgs& a, hipStream_t stream) {
 
 template <typename T>
 hipError_t launch_t(const TreeDecodeArgs& a, hipStream_t stream) {
+    if (a.N <= kSmall) {
+        tree_decode_small_kernel<T><<<dim3((unsigned)((int64_t)a.B * a.H)), dim3(256), 0, stream>>>(a);
+        return hipGetLastError();
+    }
     if (a.N <= 16) return launch_nt<T, 1>(a, stream);
     if (a.N <= 32) return launch_nt<T, 2>(a, stream);
     return launch_nt<T, 4>(a, stream);

@@ -21,7 +21,9 @@ __device__ __forceinline__ float exp_f32(float x) {
 }
 
 // (I + L)^{-1} of a strictly lower triangular tile in place; element (i, j)
-// lies at lane 16 (j / 4) + i, j % 4.  One lane per column, row by row.
+// lies at lane 16 (j / 4) + i, j % 4.  One lane per column, row by row; rows
+// at and past R are zeros of L (the inverse's are the identity's).
+template <int R = 16>
 __device__ __forceinline__ void invert(float* tile, int l16, int g) {
     if (g != 0) return;
     float x[16];
@@ -30,7 +32,7 @@ __device__ __forceinline__ void invert(float* tile, int l16, int g) {
     for (int r = 1; r < 16; ++r) {
         float s = r == l16 ? 1.f : 0.f;
 #pragma unroll
-        for (int jq = 0; jq < (r + 3) / 4; ++jq) {
+        for (int jq = 0; jq < (r < R ? (r + 3) / 4 : 0); ++jq) {
             const floatx4 c = *reinterpret_cast<const floatx4*>(tile + (16 * jq + r) * 4);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
