@@ -318,7 +318,7 @@ __device__ __forceinline__ void load_state(const float* S, floatx2 (&st)[4][8], 
 // it points at, then points where that node points.
 template <typename Mask>
 __device__ __forceinline__ Mask ancestors(int par, int lane, int nodes) {
-    Mask mask = lane < nodes ? (Mask)1 << (lane & (nodes - 1)) : 0;
+    Mask mask = lane < nodes ? (Mask)1 << (lane & (8 * (int)sizeof(Mask) - 1)) : 0;
     while (__ballot(par >= 0)) {
         const Mask pm = __shfl(mask, par < 0 ? lane : par, 64);
         const int pp = __shfl(par, par < 0 ? lane : par, 64);
@@ -372,16 +372,10 @@ struct TreeLds {
     static constexpr int kBytes = kBad + 4 * 8;
 };
 
-// Workgroups per CU that the registers are cut for: as many as fit without
-// spills (23 x 31 fp32 states, 21 nodes: 29.7 us at two, 26.3 at three).
+// (workgroups per CU: as many as fit without spills; 23 x 31 fp32 states of
+// 21 nodes take 29.7 us at two, 26.3 at three)
 template <typename T, int NT>
-constexpr int tree_waves() {
-    constexpr bool wide = sizeof(T) == 4;
-    return NT == 1 ? (wide ? 3 : 4) : (NT == 2 ? 3 : (wide ? 1 : 2));
-}
-
-template <typename T, int NT>
-__global__ __launch_bounds__(256, (tree_waves<T, NT>())) void tree_decode_kernel(TreeDecodeArgs a) {
+__global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_decode_kernel(TreeDecodeArgs a) {
     using L = TreeLds<T, NT>;
     using E = Elems<T>;
     using O = Op<T>;
@@ -945,6 +939,7 @@ hipError_t launch_t(const TreeDecodeArgs& a, hipStream_t stream) {
     }
     if (a.N <= 16) return launch_nt<T, 1>(a, stream);
     if (a.N <= 32) return launch_nt<T, 2>(a, stream);
+    if (a.N <= 48) return launch_nt<T, 3>(a, stream);
     return launch_nt<T, 4>(a, stream);
 }
 
