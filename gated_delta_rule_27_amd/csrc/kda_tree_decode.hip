@@ -151,32 +151,27 @@ struct StateOp {
 // acc += row tiles of X times them
 template <int RT>
 __device__ __forceinline__ void state_product(const Rows<float>& X, int kb, const StateOp<float> (&s)[2],
-                                              floatx4 (&acc)[RT][2], int nrt, int l16, int g) {
+                                              floatx4 (&acc)[RT][2], int l16, int g) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-        if (r < nrt) {
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const Op<float> a{frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g)};
+        for (int half = 0; half < 2; ++half) {
+            const Op<float> a{frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g)};
 #pragma unroll
-                for (int t = 0; t < 2; ++t) acc[r][t] = mma(a, s[t].half[half], acc[r][t]);
-            }
+            for (int t = 0; t < 2; ++t) acc[r][t] = mma(a, s[t].half[half], acc[r][t]);
         }
-    }
 }
 template <int RT>
 __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const StateOp<bf16> (&s)[2],
-                                              floatx4 (&acc)[RT][2], int nrt, int l16, int g) {
+                                              floatx4 (&acc)[RT][2], int l16, int g) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        if (r < nrt) {
-            const bf16* hi = X.hi + (16 * r + l16) * kBP;
-            const bf16* lo = X.lo + (16 * r + l16) * kBP;
-            const Op<bf16> a0{frag_k16(hi, kb, g), frag_k16(lo, kb, g)};
-            const Op<bf16> a1{frag_k16(hi, kb + 16, g), frag_k16(lo, kb + 16, g)};
+        const bf16* hi = X.hi + (16 * r + l16) * kBP;
+        const bf16* lo = X.lo + (16 * r + l16) * kBP;
+        const Op<bf16> a0{frag_k16(hi, kb, g), frag_k16(lo, kb, g)};
+        const Op<bf16> a1{frag_k16(hi, kb + 16, g), frag_k16(lo, kb + 16, g)};
 #pragma unroll
-            for (int t = 0; t < 2; ++t) acc[r][t] = mma(a0, a1, s[t].half[0], s[t].half[1], acc[r][t]);
-        }
+        for (int t = 0; t < 2; ++t) acc[r][t] = mma(a0, a1, s[t].half[0], s[t].half[1], acc[r][t]);
     }
 }
 
@@ -350,8 +345,16 @@ struct Tiles {
         for (; left >= (q(t) ? i + 1 : i); ++i) left -= q(t) ? i + 1 : i;
         return left;
     }
+    // both for every tile, 2 bits each, to look up by a tile that is not a constant
+    static constexpr uint64_t packed(bool rows) {
+        uint64_t p = 0;
+        for (int t = 0; t < kAll; ++t) p |= (uint64_t)(rows ? row(t) : col(t)) << (2 * t);
+        return p;
+    }
     // place of a finished tile
-    static constexpr int place(bool q, int I, int J) { return (q ? kHalf : 0) + I * (I + 1) / 2 + J; }
+    static constexpr __host__ __device__ int place(bool q, int I, int J) {
+        return (q ? kHalf : 0) + I * (I + 1) / 2 + J;
+    }
 };
 
 // LDS of a workgroup for up to 16 NT nodes
@@ -372,24 +375,17 @@ struct TreeLds {
     static constexpr int kBytes = kBad + 4 * 8;
 };
 
-// (workgroups per CU: as many as fit without spills; 23 x 31 fp32 states of
-// 21 nodes take 29.7 us at two, 26.3 at three)
+// One sequence of n <= 16 NT nodes and one head.
 template <typename T, int NT>
-__global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_decode_kernel(TreeDecodeArgs a) {
+__device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned char* lds, int64_t b, int h, int n) {
     using L = TreeLds<T, NT>;
     using E = Elems<T>;
     using O = Op<T>;
     using TT = Tiles<NT>;
     using Mask = typename std::conditional<NT <= 2, uint32_t, uint64_t>::type;   // a bit per node
-    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int H = a.H, N = a.N;
-    const int64_t b = blockIdx.x / (unsigned)H;
-    const int h = blockIdx.x % (unsigned)H;
-    const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, N));
-    if (n == 0) return;
-    const int nt = (n + 15) / 16;
     constexpr uint32_t es = sizeof(T);
     const uint32_t row_b = (uint32_t)H * kHeadDim * es;       // from node to node (64 rows: < 2^32 bytes)
     const size_t base = ((size_t)b * N * H + h) * kHeadDim;   // node 0's row
@@ -399,7 +395,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
     const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
 
     const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN);
-    floatx4* part = reinterpret_cast<floatx4*>(lds + L::kPart);   // [tile of the round][wavefront][lane]
+    floatx4* part = reinterpret_cast<floatx4*>(lds + L::kPart);   // [wavefront][tile of the round][lane]
     O* gram = reinterpret_cast<O*>(lds + L::kGram);               // [tile][lane]
     float* sbeta = reinterpret_cast<float*>(lds + L::kBeta);
     Mask* anc = reinterpret_cast<Mask*>(lds + L::kAnc);
@@ -408,8 +404,14 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
     // ---- everything this workgroup reads, in the order it is needed ---------
     const int par = lane < n ? tree_parent(a.parent, b, N, lane) : -1;
     typename E::four lar[2][NT], kr[NT][2], qr[NT][2];
-    const uint32_t at_g = 4 * g * row_b, at_l = l16 * row_b;
-    const uint32_t at_kq = at_l + (32 * w + 4 * g) * es;
+    const uint32_t at_g = 4 * g * row_b;
+    const uint32_t at_kq = l16 * row_b + (32 * w + 4 * g) * es;
+    auto load_rows = [&](typename E::four (&x)[NT][2], rsrc_t r) {
+#pragma unroll
+        for (int I = 0; I < NT; ++I)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) x[I][t] = E::load4(r, at_kq + 16 * I * row_b + 16 * t * es);
+    };
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -417,13 +419,8 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 lar[t][J][e] = E::load1(lr_, at_g + (32 * w + l16) * es + (16 * J + e) * row_b + 16 * t * es);
-#pragma unroll
-    for (int I = 0; I < NT; ++I)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            kr[I][t] = E::load4(kr_, at_kq + 16 * I * row_b + 16 * t * es);
-            qr[I][t] = E::load4(qr_, at_kq + 16 * I * row_b + 16 * t * es);
-        }
+    load_rows(kr, kr_);
+    load_rows(qr, qr_);
     float bt = to_f32(E::load1(make_rsrc_u32(static_cast<const T*>(a.beta) + (size_t)b * N * H + h,
                                              ((uint32_t)(n - 1) * H + 1) * es),
                                (uint32_t)lane * H * es));
@@ -527,19 +524,23 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
         constexpr int t0 = round() * TT::kRound;
         constexpr int count = TT::kAll - t0 < TT::kRound ? TT::kAll - t0 : TT::kRound;
         if (t0 > 0) __syncthreads();   // (the round before has been summed)
-        each<count>([&](auto u) {
-            constexpr int t = t0 + u();
-            constexpr int I = TT::row(t), J = TT::col(t);
-            if (I >= nt) return;
-            const O(&x)[2] = TT::q(t) ? xq[I] : xk[I];
-            floatx4 acc = zero4();
-            if (!deep) {
-                acc = mma(y[J][0], y[J][1], x[0], x[1], acc);
-            } else {
-                // pair by pair with e^{G_i - G_j}, node j's values from lane j of the row of 16
+        if (!deep) {
+            each<count>([&](auto u) {
+                constexpr int t = t0 + u();
+                constexpr int I = TT::row(t), J = TT::col(t);
+                const O(&x)[2] = TT::q(t) ? xq[I] : xk[I];
+                part[(w * TT::kRound + u()) * 64 + lane] = mma(y[J][0], y[J][1], x[0], x[1], zero4());
+            });
+        } else {
+            // pair by pair with e^{G_i - G_j}, node j's values from lane j of the row of 16
+            each<count>([&](auto u) {
+                constexpr int t = t0 + u();
+                constexpr int I = TT::row(t), J = TT::col(t);
                 const rsrc_t xr = TT::q(t) ? qr_ : kr_;
+                floatx4 acc = zero4();
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {   // (two channels at a time: the registers are full)
+                    __builtin_amdgcn_sched_barrier(0);
                     const uint32_t off = at_kq + 16 * (c >> 1) * es + 2 * (c & 1) * es;
                     const typename E::two x2 = E::load2(xr, off + 16 * I * row_b);
                     const typename E::two k2 = E::load2(kr_, off + 16 * J * row_b);
@@ -550,46 +551,54 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
                         xi[e] = TT::q(t) ? (float)x2[e] : finite_or_0((float)x2[e]);
                         kj[e] = finite_or_0((float)k2[e]);
                     }
-                    for (int j = 0; j < 16; ++j) {
-                        const int src = (lane & 48) | j;
-                        float s = 0.f;
+                    for (int jq = 0; jq < 4; ++jq) {
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int ge = 2 * (c & 1) + e;
-                            s += xi[e] * (__shfl(kj[e], src, 64) * exp_t<T>(gi[ge] - __shfl(gj[ge], src, 64)));
+                        for (int e = 0; e < 4; ++e) {
+                            const int src = (lane & 48) | (4 * jq + e);
+                            float s = 0.f;
+#pragma unroll
+                            for (int f = 0; f < 2; ++f) {
+                                const int cf = 2 * (c & 1) + f;
+                                s += xi[f] * (__shfl(kj[f], src, 64) * exp_t<T>(gi[cf] - __shfl(gj[cf], src, 64)));
+                            }
+                            s += __shfl_xor(s, 16, 64);
+                            s += __shfl_xor(s, 32, 64);
+                            if (g == jq) acc[e] += s;
+                            __builtin_amdgcn_sched_barrier(0);
                         }
-                        s += __shfl_xor(s, 16, 64);
-                        s += __shfl_xor(s, 32, 64);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (4 * g + e == j) acc[e] += s;
                     }
                 }
-            }
-            part[(u() * 4 + w) * 64 + lane] = acc;
-        });
+                part[(w * TT::kRound + u()) * 64 + lane] = acc;
+            });
+        }
         __syncthreads();
-        // summed by wavefront t % 4; masked by ancestry, rows of k k scaled by beta
-        each<count>([&](auto u) {
-            constexpr int t = t0 + u();
-            constexpr int I = TT::row(t), J = TT::col(t);
-            if ((t & 3) != w || I >= nt) return;
-            const floatx4* p = part + u() * 256 + lane;
-            floatx4 x = (p[0] + p[64]) + (p[128] + p[192]);
-            const Mask m = __shfl(mask, 16 * I + l16, 64) >> (16 * J + 4 * g);   // node i = 16 I + l16
-            const float scale = TT::q(t) ? 1.f : __shfl(bt, 16 * I + l16, 64);
+        // tile t is summed by wavefront t % 4 and masked by ancestry, rows of k k scaled by beta
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const bool on = ((m >> e) & 1) && (TT::q(t) || I != J || 4 * g + e != l16);
-                x[e] = on ? scale * x[e] : 0.f;
+        for (int j = 0; j < (count + 3) / 4; ++j) {
+            const int u = 4 * j + ((w - t0) & 3), t = t0 + u;
+            if (u >= count) break;
+            constexpr uint64_t kRowOf = TT::packed(true), kColOf = TT::packed(false);
+            const int I = (kRowOf >> (2 * t)) & 3, J = (kColOf >> (2 * t)) & 3;
+            const bool isq = t >= TT::kHalf;
+            const floatx4* p = part + u * 64 + lane;
+            constexpr int kW = TT::kRound * 64;   // from wavefront to wavefront
+            floatx4 x = (p[0] + p[kW]) + (p[2 * kW] + p[3 * kW]);
+            const Mask m = __shfl(mask, 16 * I + l16, 64) >> (16 * J + 4 * g);   // node i = 16 I + l16
+            const float scale = isq ? 1.f : __shfl(bt, 16 * I + l16, 64);
+            const int diag = !isq && I == J ? l16 : 64;   // (no node is its own ancestor in k k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] = ((m >> e) & 1) && 4 * g + e != diag ? scale * x[e] : 0.f;
+            O* to = gram + TT::place(isq, I, J) * 64;
+            if (t < NT) {
+                to[lane] = O::f32(x);
+                if (!L::kOver) {
+                    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+                    invert(reinterpret_cast<float*>(to), l16, g);
+                }
+            } else {
+                to[lane] = O::of(x);
             }
-            O* to = gram + TT::place(TT::q(t), I, J) * 64;
-            to[lane] = t < NT ? O::f32(x) : O::of(x);
-            if (t < NT && !L::kOver) {
-                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-                invert(reinterpret_cast<float*>(to), l16, g);
-            }
-        });
+        }
     });
 
     // ---- held and read: X S, this wavefront's columns -----------------------
@@ -600,7 +609,7 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
         __syncthreads();   // the last round has been summed
         put_rows(Xk, xk);
         if (!L::kTurns) put_rows(Xq, xq);
-        if (w < nt) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
+        if (w < NT) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
         __syncthreads();
     }
     if (L::kOver) load_v();   // (registers are free only now)
@@ -609,15 +618,15 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
     for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) so[kb][t] = StateOp<T>::of(st[kb], t);
-        state_product<NT>(Xk, 32 * kb, so[kb], held, nt, l16, g);
-        if (!L::kTurns) state_product<NT>(Xq, 32 * kb, so[kb], read, nt, l16, g);
+        state_product<NT>(Xk, 32 * kb, so[kb], held, l16, g);
+        if (!L::kTurns) state_product<NT>(Xq, 32 * kb, so[kb], read, l16, g);
     }
     if (L::kTurns) {
         __syncthreads();
         put_rows(Xq, xq);
         __syncthreads();
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) state_product<NT>(Xq, 32 * kb, so[kb], read, nt, l16, g);
+        for (int kb = 0; kb < 4; ++kb) state_product<NT>(Xq, 32 * kb, so[kb], read, l16, g);
     } else if (!L::kOver) {
         __syncthreads();   // (the Gram tiles are there)
     }
@@ -650,10 +659,11 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
         }
     }
     const bool tainted = __any((bad_col[0] | bad_col[1]) != 0);
+    uint32_t at_o = at_g + c0 * es;
+    asm volatile("" : "+v"(at_o));   // (store offsets are formed here, not kept since v's loads)
     O uo[NT][2];   // pseudo-values as operands
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
-        if (I >= nt) break;
         const floatx4 bt4 = *reinterpret_cast<const floatx4*>(sbeta + 16 * I + 4 * g);
         const floatx4 ia = gram[TT::place(false, I, I) * 64 + lane].as_f32();
         floatx4 prev[2] = {zero4(), zero4()};
@@ -702,8 +712,27 @@ __global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2)) void tree_dec
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            E::store2(or_, at_g + c0 * es + (16 * I + e) * row_b, out[0][e], out[1][e]);
+            E::store2(or_, at_o + (16 * I + e) * row_b, out[0][e], out[1][e]);
     }
+}
+
+// (workgroups per CU: as many as fit without spills; 23 x 31 fp32 states of
+// 21 nodes take 29.7 us at two, 26.3 at three.)  A sequence with fewer nodes
+// than the batch's N allows runs the code of one tile (N <= 32) or two where
+// that holds it; the code of a size has no branches on the number of tiles
+// (64 x 96 bf16 states of 64 nodes: 280 us with them, 266 without).
+template <typename T, int NT>
+__global__ __launch_bounds__(256, NT == 1 ? (sizeof(T) == 4 ? 3 : 4) : (NT == 2 ? 3 : 2))
+void tree_decode_kernel(TreeDecodeArgs a) {
+    extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
+    const int64_t b = blockIdx.x / (unsigned)a.H;
+    const int h = blockIdx.x % (unsigned)a.H;
+    const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
+    if (n == 0) return;
+    constexpr int kLess = NT > 2 ? 2 : 1;
+    static_assert(TreeLds<T, kLess>::kBytes <= TreeLds<T, NT>::kBytes, "both fit the launch's LDS");
+    if (kLess < NT && n <= 16 * kLess) tree_decode<T, kLess>(a, lds, b, h, n);
+    else tree_decode<T, NT>(a, lds, b, h, n);
 }
 
 // Up to 8 nodes: k's rows and q's share one tile of 16, rows 0..7 and 8..15
@@ -864,7 +893,7 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
         const StateOp<T> so[2] = {StateOp<T>::of(st[kb], 0), StateOp<T>::of(st[kb], 1)};
-        state_product<1>(X, 32 * kb, so, acc, 1, l16, g);
+        state_product<1>(X, 32 * kb, so, acc, l16, g);
     }
     __syncthreads();
 
