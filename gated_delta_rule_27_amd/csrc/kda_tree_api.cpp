@@ -15,13 +15,16 @@ using namespace kda::check;
 
 namespace {
 
-constexpr uint64_t kMaxUnits = (uint64_t)std::numeric_limits<int32_t>::max();
+// A launch holds fewer than 2^32 threads: workgroups of 256, of which a call
+// has twice as many as (sequence, head) pairs at the most; kda_tree_accept's
+// are of 1024, one per sequence.
+constexpr uint64_t kMaxUnits = (((uint64_t)1 << 32) - 1) / 256 / 2;
+constexpr int32_t kMaxAccept = (((int64_t)1 << 32) - 1) / 1024;
 
-// B sequences of N nodes with H heads; twice as many workgroups as (sequence,
-// head) pairs at the most
+// B sequences of N nodes with H heads
 bool tree_shape(int32_t B, int32_t N, int32_t H, int32_t most) {
     if (B < 0 || N < 1 || N > most || H < 1 || H > KDA_MAX_HEADS) return false;
-    if ((uint64_t)B * (uint64_t)H > kMaxUnits / 2) return false;
+    if ((uint64_t)B * (uint64_t)H > kMaxUnits) return false;
     return (uint64_t)B * (uint64_t)N * (uint64_t)H <= kMaxElems / kda::kHeadDim;
 }
 
@@ -136,7 +139,8 @@ kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
                            int32_t B, int32_t N, int32_t V, kda_dtype dt, int32_t* path,
                            int32_t* n_path, int32_t* next_token, hipStream_t stream) {
     if (!valid_dtype(dt)) return KDA_ERR_BAD_DTYPE;
-    if (B < 0 || N < 1 || N > KDA_MAX_TREE || V < 1 || V > KDA_MAX_VOCAB) return KDA_ERR_BAD_SHAPE;
+    if (B < 0 || B > kMaxAccept || N < 1 || N > KDA_MAX_TREE || V < 1 || V > KDA_MAX_VOCAB)
+        return KDA_ERR_BAD_SHAPE;
     if (B > 0 && (!p || !tokens || !u || !path || !n_path || !next_token))
         return KDA_ERR_NULL_ARG;
     if (!all_aligned({p, q}, 16) ||

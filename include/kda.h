@@ -396,7 +396,10 @@ kda_status kda_decode_multi(const void* q, const void* k, const void* v,
  *   n_node : [B] int32 device, nodes of each sequence, clamped to [0, N] by
  *            the kernels; NULL = N for every sequence.  Nodes at or past it
  *            take no part and their output rows are not written.
- *   1 <= N <= KDA_MAX_TREE.  B == 0 is allowed (nothing is launched).
+ *   1 <= N <= KDA_MAX_TREE; B * H < 2^23 (kda_tree_accept: B < 2^22), else
+ *   KDA_ERR_BAD_SHAPE.  B == 0 is allowed (nothing is launched).
+ * No call keeps anything between calls or uses scratch memory: calls may run
+ * at the same time on several streams, and in captured graphs.
  */
 #define KDA_MAX_TREE 64
 

@@ -141,3 +141,19 @@ def test_binding_names_what_is_missing_or_misshapen():
         kda.kda_tree_decode(meta(4, 3, 128), x, x, x, meta(2, 4, 3), meta(2, 3, 128, 128))
     with pytest.raises(TypeError, match="p must be a torch.Tensor"):
         kda.kda_tree_accept([1], None, meta(2, 4), meta(2, 4))
+
+
+@pytest.mark.parametrize("fn,defaults,most,rest", [
+    ("kda_tree_prologue", PROLOGUE, (1 << 23) - 1, dict(N=1, H=1)),
+    ("kda_tree_decode", DECODE, (1 << 23) - 1, dict(N=1, H=1)),
+    ("kda_tree_commit", COMMIT, (1 << 23) - 1, dict(N=1, P=1, H=1)),
+    ("kda_tree_accept", ACCEPT, (1 << 22) - 1, dict(N=1, V=1, path=P(0))),
+])
+def test_batches_larger_than_a_launch_are_refused(L, fn, defaults, most, rest):
+    """One more sequence than a launch holds is a bad shape; the most that it
+    holds gets past the shapes (to the alias check of overlapping buffers)."""
+    alias = dict(rest, **({"path": P(0)} if fn == "kda_tree_accept" else
+                          {"S": P(0)} if fn == "kda_tree_commit" else
+                          {"o": P(0)} if fn == "kda_tree_decode" else {"q": P(0)}))
+    assert call(getattr(L, fn), defaults, dict(alias, B=most + 1)) == BAD_SHAPE
+    assert call(getattr(L, fn), defaults, dict(alias, B=most)) == ALIAS
