@@ -75,3 +75,24 @@ def test_tree_prologue_of_a_chain_has_the_prologues_bits(dtype):
     torch.cuda.synchronize()
     for name, g, r in zip(NAMES, got, ref):
         assert torch.equal(g.reshape(r.shape), r), name
+
+
+@pytest.mark.parametrize("dtype,B,N,H", [("bf16", 1101, 5, 1), ("f32", 2051, 33, 2), ("bf16", 643, 20, 9)])
+def test_tree_prologue_of_large_batches_has_the_bits_of_small_ones(dtype, B, N, H):
+    """Workgroups take several sequences each from some thousands of slices
+    on: the outputs, and the rows left as they were, are those of the same
+    sequences in calls of 100."""
+    kda = need_gpu()
+    case(f"tree_prologue in groups {dtype} B={B} N={N} H={H}")
+    d, x = _inputs(B, N, H, dtype, 5, True)
+    par = i32(random_trees(B, N, 8, "forest"))
+    counts = i32(np.random.default_rng(1).integers(-1, N + 2, size=B))
+    fill = lambda n: tuple(torch.full((n,) + x[j].shape[1:], SENTINEL, dtype=x[0].dtype, device="cuda")
+                           for j in range(5))
+    got = kda.kda_tree_prologue(*x, d["conv_w"], d["a_bias"], par, counts, d["conv_state"], out=fill(B))
+    for b in range(0, B, 100):
+        s = slice(b, min(b + 100, B))
+        ref = kda.kda_tree_prologue(*[t[s].contiguous() for t in x], d["conv_w"], d["a_bias"], par[s].contiguous(),
+                                    counts[s].contiguous(), d["conv_state"][s].contiguous(), out=fill(s.stop - b))
+        for name, g, r in zip(NAMES, got, ref):
+            assert torch.equal(g[s], r), (name, b)
