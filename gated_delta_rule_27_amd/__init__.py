@@ -632,10 +632,24 @@ MAX_VOCAB = 1 << 22    # KDA_MAX_VOCAB
 MAX_PATH = 1 << 24     # KDA_MAX_PATH
 
 
-def _need(t, name, shape, dtype, device):
-    """A tensor argument of the tree calls: shape, dtype, device, contiguous;
-    its address, or None for one that is not given.  (One test when all is
+def _need(names, tensors, shape, dtype, device):
+    """Tensor arguments of the tree calls that share shape and dtype, each of
+    them on `device` and contiguous; their addresses.  (One pass when all is
     well: these calls are a few microseconds of GPU work at batch 1.)"""
+    index = device.index
+    try:
+        ptrs = [t.data_ptr() for t in tensors if t.dtype is dtype and t.shape == shape
+                and t.get_device() == index and t.is_contiguous()]
+        if len(ptrs) == len(tensors):
+            return ptrs
+    except AttributeError:
+        pass
+    for name, t in zip(names, tensors):
+        _refuse(t, name, shape, dtype, device)
+
+
+def _one(t, name, shape, dtype, device):
+    """The same for one argument that may be None (its address is then None)."""
     if t is None:
         return None
     try:
@@ -644,6 +658,11 @@ def _need(t, name, shape, dtype, device):
             return t.data_ptr()
     except AttributeError:
         pass
+    _refuse(t, name, shape, dtype, device)
+
+
+def _refuse(t, name, shape, dtype, device):
+    """Raise what is wrong with one argument, if anything."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.shape != shape:
@@ -652,7 +671,8 @@ def _need(t, name, shape, dtype, device):
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
     if t.device != device:
         raise ValueError(f"{name} must be on {device} like the first argument (got {t.device})")
-    raise ValueError(f"{name} must be contiguous")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name, dim):
@@ -660,12 +680,12 @@ def _first(t, name, dim):
     dtype code."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dim() != dim:
-        raise ValueError(f"{name} must have {dim} dimensions (got {tuple(t.shape)})")
-    device = t.device
-    if device.type != "cuda":
-        raise ValueError(f"{name} must be on a ROCm device (got {device})")
-    return t.shape, t.dtype, device, _dtype_code(t)
+    shape = t.shape
+    if len(shape) != dim:
+        raise ValueError(f"{name} must have {dim} dimensions (got {tuple(shape)})")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a ROCm device (got {t.device})")
+    return shape, t.dtype, t.device, _dtype_code(t)
 
 
 def _required(**named):
@@ -679,8 +699,9 @@ def _on_device(device, fn, *args):
     device of the stream, whichever device the caller has current."""
     torch = _torch()
     index = device.index
-    if index == torch.cuda.current_device():
-        # (the address that torch.cuda.current_stream(index).cuda_stream holds, without the object)
+    # (what torch.cuda.current_device() and current_stream(index).cuda_stream give, without the
+    # lazy start and the object: a tensor on the device is already there)
+    if index == torch._C._cuda_getDevice():
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
     with torch.cuda.device(device):
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
@@ -699,25 +720,30 @@ def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_n
     history).  Returns (q, k, v, log_alpha, beta); rows at or past n_node[b]
     are not written (`out` may supply the five tensors)."""
     torch = _torch()
-    _required(xq=xq, xk=xk, xv=xv, a_raw=a_raw, b_raw=b_raw, conv_w=conv_w, a_bias=a_bias)
+    if xq is None or xk is None or xv is None or a_raw is None or b_raw is None or conv_w is None or a_bias is None:
+        _required(xq=xq, xk=xk, xv=xv, a_raw=a_raw, b_raw=b_raw, conv_w=conv_w, a_bias=a_bias)
     shape, dt, dev, code = _first(xq, "xq", 4)
     B, N, H, D = shape
     i32, f32 = torch.int32, torch.float32
-    ins = [_need(xq, "xq", shape, dt, dev),
-           _need(xk, "xk", shape, dt, dev), _need(xv, "xv", shape, dt, dev),
-           _need(a_raw, "a_raw", shape, dt, dev), _need(b_raw, "b_raw", (B, N, H), dt, dev),
-           _need(conv_w, "conv_w", (3, H, D, 4), f32, dev),
-           _need(a_bias, "a_bias", (H, D), f32, dev),
-           _need(parent, "parent", (B, N), i32, dev), _need(n_node, "n_node", (B,), i32, dev)]
-    hist = _need(conv_state, "conv_state", (B, 3, 3, H, D), dt, dev)
+    rows = (B, N, H)
+    x = _need(("xq", "xk", "xv", "a_raw"), (xq, xk, xv, a_raw), shape, dt, dev)
+    b = _one(b_raw, "b_raw", rows, dt, dev)
+    w = _one(conv_w, "conv_w", (3, H, D, 4), f32, dev)
+    bias = _one(a_bias, "a_bias", (H, D), f32, dev)
+    par, count = _one(parent, "parent", (B, N), i32, dev), _one(n_node, "n_node", (B,), i32, dev)
+    hist = _one(conv_state, "conv_state", (B, 3, 3, H, D), dt, dev)
     if out is None:
-        out = tuple(torch.empty_like(xq) for _ in range(4)) + (torch.empty_like(b_raw),)
-    elif len(out) != 5 or any(t is None for t in out):
-        raise ValueError("out must be (q, k, v, log_alpha, beta)")
-    outs = [_need(t, "out", shape, dt, dev) for t in out[:4]]
-    _check(_on_device(dev, lib().kda_tree_prologue, *ins, B, N, H, D, code, hist, float(l2_eps),
-                      *outs, _need(out[4], "out[4]", (B, N, H), dt, dev)))
-    return tuple(out)
+        new = torch.empty_like
+        out = (new(xq), new(xq), new(xq), new(xq), new(b_raw))
+        outs = [t.data_ptr() for t in out]
+    else:
+        out = tuple(out)
+        if len(out) != 5 or any(t is None for t in out):
+            raise ValueError("out must be (q, k, v, log_alpha, beta)")
+        outs = _need(("out",) * 4, out[:4], shape, dt, dev) + [_one(out[4], "out[4]", rows, dt, dev)]
+    _check(_on_device(dev, lib().kda_tree_prologue, *x, b, w, bias, par, count, B, N, H, D, code,
+                      hist, float(l2_eps), *outs))
+    return out
 
 
 def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=None):
@@ -730,19 +756,19 @@ def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=
     kda_tree_prologue.  Returns o [B, N, H, 128] in the input dtype; rows at
     or past n_node[b] are not written."""
     torch = _torch()
-    _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, S=S)
+    if q is None or k is None or v is None or log_alpha is None or beta is None or S is None:
+        _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, S=S)
     shape, dt, dev, code = _first(q, "q", 4)
     B, N, H, D = shape
-    ins = [_need(q, "q", shape, dt, dev), _need(k, "k", shape, dt, dev),
-           _need(v, "v", shape, dt, dev), _need(log_alpha, "log_alpha", shape, dt, dev),
-           _need(beta, "beta", (B, N, H), dt, dev),
-           _need(S, "S", (B, H, D, D), torch.float32, dev),
-           _need(parent, "parent", (B, N), torch.int32, dev),
-           _need(n_node, "n_node", (B,), torch.int32, dev)]
+    ins = _need(("q", "k", "v", "log_alpha"), (q, k, v, log_alpha), shape, dt, dev)
+    b = _one(beta, "beta", (B, N, H), dt, dev)
+    state = _one(S, "S", (B, H, D, D), torch.float32, dev)
+    par = _one(parent, "parent", (B, N), torch.int32, dev)
+    count = _one(n_node, "n_node", (B,), torch.int32, dev)
     if o is None:
         o = torch.empty_like(q)
-    _check(_on_device(dev, lib().kda_tree_decode, *ins, B, N, H, D, D, code,
-                      _need(o, "o", shape, dt, dev)))
+    _check(_on_device(dev, lib().kda_tree_decode, *ins, b, state, par, count, B, N, H, D, D, code,
+                      _one(o, "o", shape, dt, dev)))
     return o
 
 
@@ -762,23 +788,27 @@ def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_p
     n_tok of kda_decode_multi for a chain and the n_path of kda_tree_commit
     for any tree."""
     torch = _torch()
-    _required(p=p, tokens=tokens, u=u)
+    if p is None or tokens is None or u is None:
+        _required(p=p, tokens=tokens, u=u)
     shape, dt, dev, code = _first(p, "p", 3)
     B, N, V = shape
     i32 = torch.int32
-    ins = [_need(p, "p", shape, dt, dev), _need(q, "q", (B, max(N - 1, 0), V), dt, dev),
-           _need(tokens, "tokens", (B, N), i32, dev), _need(parent, "parent", (B, N), i32, dev),
-           _need(n_node, "n_node", (B,), i32, dev), _need(u, "u", (B, N), torch.float32, dev)]
+    nodes = (B, N)
+    pp = _one(p, "p", shape, dt, dev)
+    pq = _one(q, "q", (B, max(N - 1, 0), V), dt, dev)
+    tok = _one(tokens, "tokens", nodes, i32, dev)
+    uu = _one(u, "u", nodes, torch.float32, dev)
+    par, count = _one(parent, "parent", nodes, i32, dev), _one(n_node, "n_node", (B,), i32, dev)
     if path is None:
         path = torch.empty_like(tokens)
+    # (empty_like, where there is something like it, takes two thirds of new_empty's time)
     if n_path is None:
-        n_path = tokens.new_empty(B)
+        n_path = tokens.new_empty(B) if n_node is None else torch.empty_like(n_node)
     if next_token is None:
-        next_token = tokens.new_empty(B)
-    _check(_on_device(dev, lib().kda_tree_accept, *ins, B, N, V, code,
-                      _need(path, "path", (B, N), i32, dev),
-                      _need(n_path, "n_path", (B,), i32, dev),
-                      _need(next_token, "next_token", (B,), i32, dev)))
+        next_token = torch.empty_like(n_path)
+    to = _need(("n_path", "next_token"), (n_path, next_token), (B,), i32, dev)
+    _check(_on_device(dev, lib().kda_tree_accept, pp, pq, tok, par, count, uu, B, N, V, code,
+                      _one(path, "path", nodes, i32, dev), *to))
     return path, n_path, next_token
 
 
@@ -794,27 +824,28 @@ def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
     moved in place to the last three of (history, inputs along the path).
     Returns S."""
     torch = _torch()
-    _required(k=k, v=v, log_alpha=log_alpha, beta=beta, S=S, path=path)
+    if k is None or v is None or log_alpha is None or beta is None or S is None or path is None:
+        _required(k=k, v=v, log_alpha=log_alpha, beta=beta, S=S, path=path)
     shape, dt, dev, code = _first(k, "k", 4)
     B, N, H, D = shape
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
         raise ValueError("path must be an int32 tensor [B, P]")
     P = path.shape[1]
-    ins = [_need(k, "k", shape, dt, dev), _need(v, "v", shape, dt, dev),
-           _need(log_alpha, "log_alpha", shape, dt, dev), _need(beta, "beta", (B, N, H), dt, dev),
-           _need(S, "S", (B, H, D, D), torch.float32, dev),
-           _need(path, "path", (B, P), torch.int32, dev),
-           _need(n_path, "n_path", (B,), torch.int32, dev)]
+    ins = _need(("k", "v", "log_alpha"), (k, v, log_alpha), shape, dt, dev)
+    b = _one(beta, "beta", (B, N, H), dt, dev)
+    state = _one(S, "S", (B, H, D, D), torch.float32, dev)
+    way = _one(path, "path", (B, P), torch.int32, dev)
+    count = _one(n_path, "n_path", (B,), torch.int32, dev)
     if conv is None:
-        hist = [None] * 4
+        hist = (None,) * 4
     else:
         if len(conv) != 4:
             raise ValueError("conv must be (xq, xk, xv, conv_state)")
-        names = ("xq", "xk", "xv", "conv_state")
-        _required(**dict(zip(names, conv)))
-        hist = [_need(t, name, shape if i < 3 else (B, 3, 3, H, D), dt, dev)
-                for i, (name, t) in enumerate(zip(names, conv))]
-    _check(_on_device(dev, lib().kda_tree_commit, *ins, B, N, P, H, D, D, code, *hist))
+        _required(**dict(zip(("xq", "xk", "xv", "conv_state"), conv)))
+        hist = _need(("xq", "xk", "xv"), conv[:3], shape, dt, dev) \
+            + [_one(conv[3], "conv_state", (B, 3, 3, H, D), dt, dev)]
+    _check(_on_device(dev, lib().kda_tree_commit, *ins, b, state, way, count, B, N, P, H, D, D, code,
+                      *hist))
     return S
 
 
