@@ -59,6 +59,7 @@ namespace kda {
 namespace {
 
 constexpr float kMaxDecay = 64.f;   // |G| up to which e^{-G} is formed
+constexpr int kLevels = 8;          // steps of it beyond
 constexpr int kFP = kHeadDim + 4;   // fp32 LDS row
 constexpr int kBP = kHeadDim + 8;   // bf16 LDS row
 
@@ -117,9 +118,10 @@ __device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> a1, Op<bf16> b0, Op
     return mma_bf16_k32(ah, bh, acc);
 }
 __device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> b0, floatx4 acc) {
-    const bf16 z = (bf16)0.f;
-    const Op<bf16> zero{{z, z, z, z}, {z, z, z, z}};
-    return mma(a0, zero, b0, zero, acc);
+    // (16 k fill half an instruction: a's two parts side by side meet b's one after the other)
+    const bf16x8 a = join(a0.hi, a0.lo);
+    acc = mma_bf16_k32(a, join(b0.lo, b0.lo), acc);
+    return mma_bf16_k32(a, join(b0.hi, b0.hi), acc);
 }
 
 // Rows of 128 channels in LDS, as A operands of the state product
@@ -495,7 +497,11 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             for (int e = 0; e < 4; ++e) least = fminf(least, GT[I][t][e]);
         }
     }
-    const bool deep = __any(least < -kMaxDecay);   // (of this wavefront's channels)
+    // (of this wavefront's channels; log alpha >= -5 leaves 64 nodes six levels)
+    const bool deep = __any(least < -kMaxDecay);
+    int deepest = 0;
+#pragma unroll 1
+    for (int m = 1; m < kLevels && __any(least <= -kMaxDecay * m); ++m) deepest = m;
     O xk[NT][2], xq[NT][2], y[NT][2];
 #pragma unroll
     for (int I = 0; I < NT; ++I)
@@ -541,40 +547,40 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
                 part[(w * TT::kRound + u()) * 64 + lane] = mma(y[J][0], y[J][1], x[0], x[1], zero4());
             });
         } else {
-            // pair by pair with e^{G_i - G_j}, node j's values from lane j of the row of 16
+            // level by level: the j whose -G_j lies in [64 m, 64 m + 64), referred to e^{-64 m}
             each<count>([&](auto u) {
                 constexpr int t = t0 + u();
                 constexpr int I = TT::row(t), J = TT::col(t);
                 const rsrc_t xr = TT::q(t) ? qr_ : kr_;
                 floatx4 acc = zero4();
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {   // (two channels at a time: the registers are full)
+                for (int c = 0; c < 2; ++c) {   // (16 channels at a time: the registers are full)
                     __builtin_amdgcn_sched_barrier(0);
-                    const uint32_t off = at_kq + 16 * (c >> 1) * es + 2 * (c & 1) * es;
-                    const typename E::two x2 = E::load2(xr, off + 16 * I * row_b);
-                    const typename E::two k2 = E::load2(kr_, off + 16 * J * row_b);
-                    const floatx4 gi = y[I][c >> 1].as_f32(), gj = y[J][c >> 1].as_f32();
-                    float xi[2], kj[2];
+                    typename E::four xi = E::load4(xr, at_kq + 16 * I * row_b + 16 * c * es);
+                    typename E::four kj = E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es);
+                    const floatx4 Gi = y[I][c].as_f32(), Gj = y[J][c].as_f32();
+#pragma unroll 1
+                    for (int m = 0; m <= deepest; ++m) {
+                        const float from = -kMaxDecay * m, to = m < kLevels - 1 ? from - kMaxDecay : -INFINITY;
+                        bool some = false;
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        xi[e] = TT::q(t) ? (float)x2[e] : finite_or_0((float)x2[e]);
-                        kj[e] = finite_or_0((float)k2[e]);
-                    }
-                    for (int jq = 0; jq < 4; ++jq) {
+                        for (int e = 0; e < 4; ++e) some |= Gj[e] > to && (m == 0 || Gj[e] <= from);
+                        if (!__any(some)) continue;
+                        asm volatile("" : "+v"(xi), "+v"(kj));   // (widened here, not kept so over the loop)
+                        floatx4 z;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            z[e] = Gj[e] > to && (m == 0 || Gj[e] <= from)
+                                       ? finite_or_0((float)kj[e]) * exp_t<T>(from - Gj[e]) : 0.f;
+                        const O ks = O::of(z);
+                        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const int src = (lane & 48) | (4 * jq + e);
-                            float s = 0.f;
-#pragma unroll
-                            for (int f = 0; f < 2; ++f) {
-                                const int cf = 2 * (c & 1) + f;
-                                s += xi[f] * (__shfl(kj[f], src, 64) * exp_t<T>(gi[cf] - __shfl(gj[cf], src, 64)));
-                            }
-                            s += __shfl_xor(s, 16, 64);
-                            s += __shfl_xor(s, 32, 64);
-                            if (g == jq) acc[e] += s;
-                            __builtin_amdgcn_sched_barrier(0);
+                            // (a descendant's G is no greater than G_j: only masked entries meet the bound 0)
+                            const float x = TT::q(t) ? (float)xi[e] : finite_or_0((float)xi[e]);
+                            z[e] = x * exp_t<T>(fminf(Gi[e] - from, 0.f));
                         }
+                        acc = mma(ks, O::of(z), acc);
                     }
                 }
                 part[(w * TT::kRound + u()) * 64 + lane] = acc;
