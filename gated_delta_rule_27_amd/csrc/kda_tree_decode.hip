@@ -60,6 +60,7 @@ namespace {
 
 constexpr float kMaxDecay = 64.f;   // |G| up to which e^{-G} is formed
 constexpr int kLevels = 8;          // steps of it beyond
+constexpr float kNothing = -90.f;   // e^ of which is 0 in fp32
 constexpr int kFP = kHeadDim + 4;   // fp32 LDS row
 constexpr int kBP = kHeadDim + 8;   // bf16 LDS row
 
@@ -90,6 +91,8 @@ struct __attribute__((aligned(16))) Op<float> {
     static __device__ __forceinline__ Op of(floatx4 v) { return Op{v}; }
     static __device__ __forceinline__ Op f32(floatx4 v) { return Op{v}; }   // kept whole
     __device__ __forceinline__ floatx4 as_f32() const { return x; }
+    static __device__ __forceinline__ Op raw(floatx4 v) { return Op{v}; }   // inputs as they are
+    __device__ __forceinline__ floatx4 as_raw() const { return x; }
 };
 template <>
 struct __attribute__((aligned(16))) Op<bf16> {
@@ -103,6 +106,8 @@ struct __attribute__((aligned(16))) Op<bf16> {
     // fp32 values kept whole in its place
     static __device__ __forceinline__ Op f32(floatx4 v) { return __builtin_bit_cast(Op, v); }
     __device__ __forceinline__ floatx4 as_f32() const { return __builtin_bit_cast(floatx4, *this); }
+    static __device__ __forceinline__ Op raw(bf16x4 v) { return Op{v, v}; }
+    __device__ __forceinline__ bf16x4 as_raw() const { return hi; }
 };
 // acc += a b over 16 (a0, b0) or 32 k
 __device__ __forceinline__ floatx4 mma(Op<float> a0, Op<float> b0, floatx4 acc) {
@@ -509,10 +514,15 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
         for (int t = 0; t < 2; ++t) {
             const floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]);
             floatx4 ex;
+            if (!L::kOver || !deep) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
-            xk[I][t] = O::of(kx * ex);
-            xq[I][t] = O::of(qx * ex);
+                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
+                xk[I][t] = O::of(kx * ex);
+                xq[I][t] = O::of(qx * ex);
+            } else {   // (scaled once the Gram tiles are formed)
+                xk[I][t] = O::raw(kr[I][t]);
+                xq[I][t] = O::raw(qr[I][t]);
+            }
             if (!deep) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[I][t][e]);
@@ -551,33 +561,42 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             each<count>([&](auto u) {
                 constexpr int t = t0 + u();
                 constexpr int I = TT::row(t), J = TT::col(t);
-                const rsrc_t xr = TT::q(t) ? qr_ : kr_;
                 floatx4 acc = zero4();
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {   // (16 channels at a time: the registers are full)
                     __builtin_amdgcn_sched_barrier(0);
-                    typename E::four xi = E::load4(xr, at_kq + 16 * I * row_b + 16 * c * es);
-                    typename E::four kj = E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es);
+                    typename E::four xi, kj;
+                    if (L::kOver) {
+                        xi = (TT::q(t) ? xq : xk)[I][c].as_raw();
+                        kj = xk[J][c].as_raw();
+                    } else {   // (the rows are scaled already)
+                        xi = E::load4(TT::q(t) ? qr_ : kr_, at_kq + 16 * I * row_b + 16 * c * es);
+                        kj = E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es);
+                    }
                     const floatx4 Gi = y[I][c].as_f32(), Gj = y[J][c].as_f32();
 #pragma unroll 1
                     for (int m = 0; m <= deepest; ++m) {
                         const float from = -kMaxDecay * m, to = m < kLevels - 1 ? from - kMaxDecay : -INFINITY;
-                        bool some = false;
+                        bool some = false, felt = false;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) some |= Gj[e] > to && (m == 0 || Gj[e] <= from);
-                        if (!__any(some)) continue;
+                        for (int e = 0; e < 4; ++e) {
+                            some |= Gj[e] > to && (m == 0 || Gj[e] <= from);
+                            felt |= Gi[e] - from > kNothing;
+                        }
+                        if (!__any(some) || !__any(felt)) continue;
                         asm volatile("" : "+v"(xi), "+v"(kj));   // (widened here, not kept so over the loop)
                         floatx4 z;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            z[e] = Gj[e] > to && (m == 0 || Gj[e] <= from)
-                                       ? finite_or_0((float)kj[e]) * exp_t<T>(from - Gj[e]) : 0.f;
+                        for (int e = 0; e < 4; ++e) {
+                            const float x = L::kOver ? (float)kj[e] : finite_or_0((float)kj[e]);
+                            z[e] = Gj[e] > to && (m == 0 || Gj[e] <= from) ? x * exp_t<T>(from - Gj[e]) : 0.f;
+                        }
                         const O ks = O::of(z);
                         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             // (a descendant's G is no greater than G_j: only masked entries meet the bound 0)
-                            const float x = TT::q(t) ? (float)xi[e] : finite_or_0((float)xi[e]);
+                            const float x = L::kOver || TT::q(t) ? (float)xi[e] : finite_or_0((float)xi[e]);
                             z[e] = x * exp_t<T>(fminf(Gi[e] - from, 0.f));
                         }
                         acc = mma(ks, O::of(z), acc);
@@ -615,6 +634,20 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             }
         }
     });
+
+    if (L::kOver && deep) {
+#pragma unroll
+        for (int I = 0; I < NT; ++I)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                floatx4 ex;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(y[I][t].as_f32()[e]);
+                xk[I][t] = O::of(widen(xk[I][t].as_raw()) * ex);
+                xq[I][t] = O::of(widen(xq[I][t].as_raw()) * ex);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+    }
 
     // ---- held and read: X S, this wavefront's columns -----------------------
     floatx4 held[NT][2], read[NT][2];
