@@ -99,6 +99,29 @@ def test_tree_decode_mixed_decay(dtype):
     _check_decode(kda, w, par, [N, 33], dtype)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N,shape", [(16, "chain"), (30, "chain"), (33, "forest"), (48, "chain"), (64, "chain"),
+                                     (64, "forest"), (64, "comb")])
+def test_tree_decode_levels_of_decay(dtype, N, shape):
+    """Decays of 0, -0.01 and -5 mixed over nodes and channels, so that a tile
+    holds nodes of every depth of decay (to -320) beside each other: pairs
+    near each other far below keep their entries' precision."""
+    kda = need_gpu()
+    case(f"tree_decode levels of decay {dtype} N={N} {shape}")
+    w = node_inputs(3, N, 2, dtype, seed=300 + N)
+    g = torch.Generator(device="cuda").manual_seed(N)
+    pick = torch.randint(0, 3, w["log_alpha"].shape, generator=g, device="cuda")
+    w["log_alpha"].copy_(torch.tensor([0.0, -0.01, -5.0], device="cuda")[pick])
+    w["log_alpha"][1, :, :, :40] = -5.0
+    if shape == "comb":   # a long spine; on it and on the cached state, short branches in turn
+        par = np.full((3, N), -1, dtype=np.int32)
+        for i in range(1, N):
+            par[:, i] = i - 1 if i < N // 2 else ([N // 2 - 1, -1, i - 2][i % 3])
+    else:
+        par = random_trees(3, N, N, shape)
+    _check_decode(kda, w, par, [N, N, N - 3], dtype)
+
+
 def test_tree_decode_of_a_chain_is_the_chain_verify():
     """parent = None gives kda_decode_multi's verify pass, to rounding."""
     kda = need_gpu()
