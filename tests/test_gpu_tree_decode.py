@@ -76,7 +76,7 @@ def test_tree_decode_matches_oracle(dtype, B, N, H, shape, counts, mu):
 @pytest.mark.parametrize("N", [12, 13, 16, 40, 64])
 def test_tree_decode_at_the_decay_bound(dtype, N):
     """log alpha = -5 everywhere on a chain: |G| reaches 60 at 12 nodes (the
-    factored Gram entries), 65 at 13 (the pairwise ones), 320 at 64."""
+    factored Gram entries), 65 at 13 (levels of decay), 320 at 64."""
     kda = need_gpu()
     case(f"tree_decode at the decay bound {dtype} N={N}")
     w = node_inputs(2, N, 2, dtype, seed=77 + N)
