@@ -632,11 +632,10 @@ MAX_VOCAB = 1 << 22    # KDA_MAX_VOCAB
 MAX_PATH = 1 << 24     # KDA_MAX_PATH
 
 
-def _need(names, tensors, shape, dtype, device):
+def _need(names, tensors, shape, dtype, index):
     """Tensor arguments of the tree calls that share shape and dtype, each of
-    them on `device` and contiguous; their addresses.  (One pass when all is
+    them on GPU `index` and contiguous; their addresses.  (One pass when all is
     well: these calls are a few microseconds of GPU work at batch 1.)"""
-    index = device.index
     try:
         ptrs = [t.data_ptr() for t in tensors if t.dtype is dtype and t.shape == shape
                 and t.get_device() == index and t.is_contiguous()]
@@ -645,23 +644,23 @@ def _need(names, tensors, shape, dtype, device):
     except AttributeError:
         pass
     for name, t in zip(names, tensors):
-        _refuse(t, name, shape, dtype, device)
+        _refuse(t, name, shape, dtype, index)
 
 
-def _one(t, name, shape, dtype, device):
+def _one(t, name, shape, dtype, index):
     """The same for one argument that may be None (its address is then None)."""
     if t is None:
         return None
     try:
-        if t.dtype is dtype and t.shape == shape and t.get_device() == device.index \
+        if t.dtype is dtype and t.shape == shape and t.get_device() == index \
                 and t.is_contiguous():
             return t.data_ptr()
     except AttributeError:
         pass
-    _refuse(t, name, shape, dtype, device)
+    _refuse(t, name, shape, dtype, index)
 
 
-def _refuse(t, name, shape, dtype, device):
+def _refuse(t, name, shape, dtype, index):
     """Raise what is wrong with one argument, if anything."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -669,23 +668,24 @@ def _refuse(t, name, shape, dtype, device):
         raise ValueError(f"{name} must have shape {tuple(shape)} (got {tuple(t.shape)})")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype} (got {t.dtype})")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device} like the first argument (got {t.device})")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index} like the first argument (got {t.device})")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
 
 
 def _first(t, name, dim):
-    """The argument the others are measured by: its shape, dtype, device and
+    """The argument the others are measured by: its shape, dtype, GPU and
     dtype code."""
     if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     shape = t.shape
     if len(shape) != dim:
         raise ValueError(f"{name} must have {dim} dimensions (got {tuple(shape)})")
-    if not t.is_cuda:
+    index = t.get_device()
+    if index < 0:
         raise ValueError(f"{name} must be on a ROCm device (got {t.device})")
-    return shape, t.dtype, t.device, _dtype_code(t)
+    return shape, t.dtype, index, _dtype_code(t)
 
 
 def _required(**named):
@@ -694,16 +694,15 @@ def _required(**named):
             raise TypeError(f"{name} is required")
 
 
-def _on_device(device, fn, *args):
-    """fn(*args, stream) with `device` current: the launch then goes to the
+def _on_device(index, fn, *args):
+    """fn(*args, stream) with GPU `index` current: the launch then goes to the
     device of the stream, whichever device the caller has current."""
     torch = _torch()
-    index = device.index
     # (what torch.cuda.current_device() and current_stream(index).cuda_stream give, without the
     # lazy start and the object: a tensor on the device is already there)
     if index == torch._C._cuda_getDevice():
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
-    with torch.cuda.device(device):
+    with torch.cuda.device(index):
         return fn(*args, torch._C._cuda_getCurrentRawStream(index))
 
 
@@ -722,26 +721,27 @@ def kda_tree_prologue(xq, xk, xv, a_raw, b_raw, conv_w, a_bias, parent=None, n_n
     torch = _torch()
     if xq is None or xk is None or xv is None or a_raw is None or b_raw is None or conv_w is None or a_bias is None:
         _required(xq=xq, xk=xk, xv=xv, a_raw=a_raw, b_raw=b_raw, conv_w=conv_w, a_bias=a_bias)
-    shape, dt, dev, code = _first(xq, "xq", 4)
+    shape, dt, gpu, code = _first(xq, "xq", 4)
     B, N, H, D = shape
     i32, f32 = torch.int32, torch.float32
     rows = (B, N, H)
-    x = _need(("xq", "xk", "xv", "a_raw"), (xq, xk, xv, a_raw), shape, dt, dev)
-    b = _one(b_raw, "b_raw", rows, dt, dev)
-    w = _one(conv_w, "conv_w", (3, H, D, 4), f32, dev)
-    bias = _one(a_bias, "a_bias", (H, D), f32, dev)
-    par, count = _one(parent, "parent", (B, N), i32, dev), _one(n_node, "n_node", (B,), i32, dev)
-    hist = _one(conv_state, "conv_state", (B, 3, 3, H, D), dt, dev)
+    x = _need(("xq", "xk", "xv", "a_raw"), (xq, xk, xv, a_raw), shape, dt, gpu)
+    b = _one(b_raw, "b_raw", rows, dt, gpu)
+    w = _one(conv_w, "conv_w", (3, H, D, 4), f32, gpu)
+    bias = _one(a_bias, "a_bias", (H, D), f32, gpu)
+    par, count = _one(parent, "parent", (B, N), i32, gpu), _one(n_node, "n_node", (B,), i32, gpu)
+    hist = _one(conv_state, "conv_state", (B, 3, 3, H, D), dt, gpu)
     if out is None:
         new = torch.empty_like
         out = (new(xq), new(xq), new(xq), new(xq), new(b_raw))
         outs = [t.data_ptr() for t in out]
     else:
         out = tuple(out)
-        if len(out) != 5 or any(t is None for t in out):
+        if len(out) != 5 or out[0] is None or out[1] is None or out[2] is None or out[3] is None \
+                or out[4] is None:
             raise ValueError("out must be (q, k, v, log_alpha, beta)")
-        outs = _need(("out",) * 4, out[:4], shape, dt, dev) + [_one(out[4], "out[4]", rows, dt, dev)]
-    _check(_on_device(dev, lib().kda_tree_prologue, *x, b, w, bias, par, count, B, N, H, D, code,
+        outs = _need(("out",) * 4, out[:4], shape, dt, gpu) + [_one(out[4], "out[4]", rows, dt, gpu)]
+    _check(_on_device(gpu, lib().kda_tree_prologue, *x, b, w, bias, par, count, B, N, H, D, code,
                       hist, float(l2_eps), *outs))
     return out
 
@@ -758,17 +758,17 @@ def kda_tree_decode(q, k, v, log_alpha, beta, S, parent=None, n_node=None, *, o=
     torch = _torch()
     if q is None or k is None or v is None or log_alpha is None or beta is None or S is None:
         _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, S=S)
-    shape, dt, dev, code = _first(q, "q", 4)
+    shape, dt, gpu, code = _first(q, "q", 4)
     B, N, H, D = shape
-    ins = _need(("q", "k", "v", "log_alpha"), (q, k, v, log_alpha), shape, dt, dev)
-    b = _one(beta, "beta", (B, N, H), dt, dev)
-    state = _one(S, "S", (B, H, D, D), torch.float32, dev)
-    par = _one(parent, "parent", (B, N), torch.int32, dev)
-    count = _one(n_node, "n_node", (B,), torch.int32, dev)
+    ins = _need(("q", "k", "v", "log_alpha"), (q, k, v, log_alpha), shape, dt, gpu)
+    b = _one(beta, "beta", (B, N, H), dt, gpu)
+    state = _one(S, "S", (B, H, D, D), torch.float32, gpu)
+    par = _one(parent, "parent", (B, N), torch.int32, gpu)
+    count = _one(n_node, "n_node", (B,), torch.int32, gpu)
     if o is None:
         o = torch.empty_like(q)
-    _check(_on_device(dev, lib().kda_tree_decode, *ins, b, state, par, count, B, N, H, D, D, code,
-                      _one(o, "o", shape, dt, dev)))
+    _check(_on_device(gpu, lib().kda_tree_decode, *ins, b, state, par, count, B, N, H, D, D, code,
+                      _one(o, "o", shape, dt, gpu)))
     return o
 
 
@@ -790,15 +790,15 @@ def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_p
     torch = _torch()
     if p is None or tokens is None or u is None:
         _required(p=p, tokens=tokens, u=u)
-    shape, dt, dev, code = _first(p, "p", 3)
+    shape, dt, gpu, code = _first(p, "p", 3)
     B, N, V = shape
     i32 = torch.int32
     nodes = (B, N)
-    pp = _one(p, "p", shape, dt, dev)
-    pq = _one(q, "q", (B, max(N - 1, 0), V), dt, dev)
-    tok = _one(tokens, "tokens", nodes, i32, dev)
-    uu = _one(u, "u", nodes, torch.float32, dev)
-    par, count = _one(parent, "parent", nodes, i32, dev), _one(n_node, "n_node", (B,), i32, dev)
+    pp = _one(p, "p", shape, dt, gpu)
+    pq = _one(q, "q", (B, max(N - 1, 0), V), dt, gpu)
+    tok = _one(tokens, "tokens", nodes, i32, gpu)
+    uu = _one(u, "u", nodes, torch.float32, gpu)
+    par, count = _one(parent, "parent", nodes, i32, gpu), _one(n_node, "n_node", (B,), i32, gpu)
     if path is None:
         path = torch.empty_like(tokens)
     # (empty_like, where there is something like it, takes two thirds of new_empty's time)
@@ -806,9 +806,9 @@ def kda_tree_accept(p, q, tokens, u, parent=None, n_node=None, *, path=None, n_p
         n_path = tokens.new_empty(B) if n_node is None else torch.empty_like(n_node)
     if next_token is None:
         next_token = torch.empty_like(n_path)
-    to = _need(("n_path", "next_token"), (n_path, next_token), (B,), i32, dev)
-    _check(_on_device(dev, lib().kda_tree_accept, pp, pq, tok, par, count, uu, B, N, V, code,
-                      _one(path, "path", nodes, i32, dev), *to))
+    to = _need(("n_path", "next_token"), (n_path, next_token), (B,), i32, gpu)
+    _check(_on_device(gpu, lib().kda_tree_accept, pp, pq, tok, par, count, uu, B, N, V, code,
+                      _one(path, "path", nodes, i32, gpu), *to))
     return path, n_path, next_token
 
 
@@ -826,25 +826,26 @@ def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
     torch = _torch()
     if k is None or v is None or log_alpha is None or beta is None or S is None or path is None:
         _required(k=k, v=v, log_alpha=log_alpha, beta=beta, S=S, path=path)
-    shape, dt, dev, code = _first(k, "k", 4)
+    shape, dt, gpu, code = _first(k, "k", 4)
     B, N, H, D = shape
     if not isinstance(path, torch.Tensor) or path.dim() != 2:
         raise ValueError("path must be an int32 tensor [B, P]")
     P = path.shape[1]
-    ins = _need(("k", "v", "log_alpha"), (k, v, log_alpha), shape, dt, dev)
-    b = _one(beta, "beta", (B, N, H), dt, dev)
-    state = _one(S, "S", (B, H, D, D), torch.float32, dev)
-    way = _one(path, "path", (B, P), torch.int32, dev)
-    count = _one(n_path, "n_path", (B,), torch.int32, dev)
+    ins = _need(("k", "v", "log_alpha"), (k, v, log_alpha), shape, dt, gpu)
+    b = _one(beta, "beta", (B, N, H), dt, gpu)
+    state = _one(S, "S", (B, H, D, D), torch.float32, gpu)
+    way = _one(path, "path", (B, P), torch.int32, gpu)
+    count = _one(n_path, "n_path", (B,), torch.int32, gpu)
     if conv is None:
         hist = (None,) * 4
     else:
         if len(conv) != 4:
             raise ValueError("conv must be (xq, xk, xv, conv_state)")
-        _required(**dict(zip(("xq", "xk", "xv", "conv_state"), conv)))
-        hist = _need(("xq", "xk", "xv"), conv[:3], shape, dt, dev) \
-            + [_one(conv[3], "conv_state", (B, 3, 3, H, D), dt, dev)]
-    _check(_on_device(dev, lib().kda_tree_commit, *ins, b, state, way, count, B, N, P, H, D, D, code,
+        if conv[0] is None or conv[1] is None or conv[2] is None or conv[3] is None:
+            _required(xq=conv[0], xk=conv[1], xv=conv[2], conv_state=conv[3])
+        hist = _need(("xq", "xk", "xv"), conv[:3], shape, dt, gpu) \
+            + [_one(conv[3], "conv_state", (B, 3, 3, H, D), dt, gpu)]
+    _check(_on_device(gpu, lib().kda_tree_commit, *ins, b, state, way, count, B, N, P, H, D, D, code,
                       *hist))
     return S
 

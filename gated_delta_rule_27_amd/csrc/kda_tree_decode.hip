@@ -918,13 +918,8 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
     // ---- G^T, scaled rows, this wavefront's part of the Gram tile -------------
     const uint32_t m = __shfl(mask, i, 64);
     floatx4 GT[2];
-    float least = 0.f;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        GT[t] = gather_decay<1>(lar[t], m, 0, g);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) least = fminf(least, GT[t][e]);
-    }
+    for (int t = 0; t < 2; ++t) GT[t] = gather_decay<1>(lar[t], m, 0, g);
     O xo[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
