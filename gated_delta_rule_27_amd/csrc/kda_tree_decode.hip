@@ -20,9 +20,9 @@
 // from the greatest G_j of its tile of ancestors down: in a level the factors
 // are e^{r - G_j} <= e^64 and, for descendants, e^{G_i - r} <= 1, r the level's
 // upper end, per channel.  What underflows there is below e^{-23} of the
-// level's largest entries.  (Pair by pair, with e^{G_i - G_j}: chains of 64,
-// 64 x 96 bf16 states, 1330 us against 375, 250 without levels; at log alpha
-// of -2.5 2540 against 500.)
+// level's largest entries.  (64 x 96 bf16 states, chains of 64: 508 us where
+// log alpha is -0.7 on average and some |G| pass 64, 619 at -2.5, 370 where
+// none does; pair by pair, with e^{G_i - G_j}, the first two took 1330 and 2540.)
 //
 // Masking.  Products with masked (zero) entries would spread a NaN or
 // infinity of one node to its siblings.  Non-finite k, log alpha, beta (per
@@ -42,17 +42,27 @@
 // From the state product on wavefront w owns value columns 32 w .. 32 w + 31
 // (lane: columns 2 (l % 16), +1) over all 128 state rows, and pseudo-values,
 // solve and outputs stay in its own accumulators.  The scaled rows are all
-// that every wavefront needs of the others' work; beyond 32 nodes k's and
-// q's rows take turns in LDS, so that two workgroups share a compute unit.
+// that every wavefront needs of the others' work; beyond 32 nodes (16 for bf16
+// inputs) k's and q's rows take turns in LDS, so that two (three) workgroups
+// share a compute unit.
 //
-// What bounds it, measured on bf16 inputs: the states' read while four
-// workgroups share a compute unit (256 x 96 states, 8 nodes: 307 us, 6.1 TB/s
-// of everything read and written; 64 x 96: 16 nodes 89 us, 5.9 TB/s, 32 nodes
-// 121 us, 5.4 TB/s); beyond 32 nodes, at two workgroups, the chain of load,
-// Gram rounds, solve and outputs of each (64 x 96, 64 nodes: 269 us, 3.4 TB/s
-// and 96 TFLOP/s).  fp32 inputs: fp32 MFMA from 17 nodes on (64 x 96: 16 nodes
-// 109 us, 32 nodes 238 us, 64 nodes 490 us).  One sequence of 8 nodes x 96
-// heads: 6.3 us, the latency of one workgroup.
+// Bits.  Whatever the inputs' type, everything between them and the one
+// rounding of the outputs is held in 24 bits or more: fp32 MFMA for the Gram
+// tiles, the solve and the outputs, and for the product with the state fp32
+// MFMA or bf16 MFMA on both operands in three bf16 parts.  (In two parts, 16
+// bits, a read of neighbouring state rows with opposite signs lost what
+// differs between them, as kda_decode_multi does not; 64 x 96 states of 64
+// nodes took 254 us in two parts, 365 now, 32 nodes 128 against 170, 256 x 96
+// of 8 nodes 304 against 307.)
+//
+// What bounds it, measured on bf16 inputs: the states' read up to 16 nodes,
+// while four workgroups share a compute unit (256 x 96 states, 8 nodes: 307
+// us, 6.1 TB/s of everything read and written, 16 nodes 411 us, 5.3 TB/s);
+// from then on MFMA (fp32 for Gram tiles and solve) and the chain of load,
+// Gram rounds, solve and outputs of a workgroup (64 x 96: 32 nodes 170 us, 3.9
+// TB/s, 64 nodes 365 us, 2.5 TB/s and 71 TFLOP/s).  fp32 inputs: fp32 MFMA from
+// 17 nodes on (64 x 96: 16 nodes 116 us, 32 nodes 221 us, 64 nodes 454 us).
+// One sequence of 8 nodes x 96 heads: 6.6 us, the latency of one workgroup.
 #include <type_traits>
 #include <utility>
 
@@ -72,70 +82,31 @@ constexpr int kBP = kHeadDim + 8;   // bf16 LDS row
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
-// x, y as bf16 (hi) and the bf16 of what that leaves out (lo)
-__device__ __forceinline__ void split2(float x, float y, bf16x2& hi, bf16x2& lo) {
-    hi = __builtin_convertvector((floatx2{x, y}), bf16x2);
-    const uint32_t u = __builtin_bit_cast(uint32_t, hi);
-    lo = __builtin_convertvector((floatx2{x - __builtin_bit_cast(float, u << 16),
-                                          y - __builtin_bit_cast(float, u & 0xffff0000u)}), bf16x2);
+// x, y as bf16 and, in their place, what that leaves out
+__device__ __forceinline__ bf16x2 take(float& x, float& y) {
+    const bf16x2 h = __builtin_convertvector((floatx2{x, y}), bf16x2);
+    const uint32_t u = __builtin_bit_cast(uint32_t, h);
+    x -= __builtin_bit_cast(float, u << 16);
+    y -= __builtin_bit_cast(float, u & 0xffff0000u);
+    return h;
 }
-__device__ __forceinline__ bf16x4 join(bf16x2 a, bf16x2 b) { return __builtin_shufflevector(a, b, 0, 1, 2, 3); }
+__device__ __forceinline__ bf16x4 take4(floatx4& v) {
+    float x[4] = {v[0], v[1], v[2], v[3]};
+    const bf16x2 a = take(x[0], x[1]), b = take(x[2], x[3]);
+    v = floatx4{x[0], x[1], x[2], x[3]};
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3);
+}
 __device__ __forceinline__ bf16x8 join(bf16x4 a, bf16x4 b) {
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// Four consecutive k of a row or column of an MFMA operand.  fp32 values as
-// they are; for bf16 inputs a scaled value is no longer a bf16, so it is held
-// as the sum of two (hi and what its rounding leaves, lo): the products
-// hi hi + hi lo + lo hi leave a relative error of 2^-17, and the one rounding
-// that counts is the output's.
-template <typename T>
-struct Op;
-template <>
-struct __attribute__((aligned(16))) Op<float> {
-    floatx4 x;
-    static __device__ __forceinline__ Op of(floatx4 v) { return Op{v}; }
-    static __device__ __forceinline__ Op f32(floatx4 v) { return Op{v}; }   // kept whole
-    __device__ __forceinline__ floatx4 as_f32() const { return x; }
-    static __device__ __forceinline__ Op raw(floatx4 v) { return Op{v}; }   // inputs as they are
-    __device__ __forceinline__ floatx4 as_raw() const { return x; }
-};
-template <>
-struct __attribute__((aligned(16))) Op<bf16> {
-    bf16x4 hi, lo;
-    static __device__ __forceinline__ Op of(floatx4 v) {
-        bf16x2 h[2], l[2];
-        split2(v[0], v[1], h[0], l[0]);
-        split2(v[2], v[3], h[1], l[1]);
-        return Op{join(h[0], h[1]), join(l[0], l[1])};
-    }
-    // fp32 values kept whole in its place
-    static __device__ __forceinline__ Op f32(floatx4 v) { return __builtin_bit_cast(Op, v); }
-    __device__ __forceinline__ floatx4 as_f32() const { return __builtin_bit_cast(floatx4, *this); }
-    static __device__ __forceinline__ Op raw(bf16x4 v) { return Op{v, v}; }
-    __device__ __forceinline__ bf16x4 as_raw() const { return hi; }
-};
-// acc += a b over 16 (a0, b0) or 32 k
-__device__ __forceinline__ floatx4 mma(Op<float> a0, Op<float> b0, floatx4 acc) {
-    return mma_f32_k16(a0.x, b0.x, acc);
-}
-__device__ __forceinline__ floatx4 mma(Op<float> a0, Op<float> a1, Op<float> b0, Op<float> b1, floatx4 acc) {
-    return mma_f32_k16(a1.x, b1.x, mma_f32_k16(a0.x, b0.x, acc));
-}
-__device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> a1, Op<bf16> b0, Op<bf16> b1, floatx4 acc) {
-    const bf16x8 ah = join(a0.hi, a1.hi), bh = join(b0.hi, b1.hi);
-    acc = mma_bf16_k32(join(a0.lo, a1.lo), bh, acc);
-    acc = mma_bf16_k32(ah, join(b0.lo, b1.lo), acc);
-    return mma_bf16_k32(ah, bh, acc);
-}
-__device__ __forceinline__ floatx4 mma(Op<bf16> a0, Op<bf16> b0, floatx4 acc) {
-    // (16 k fill half an instruction: a's two parts side by side meet b's one after the other)
-    const bf16x8 a = join(a0.hi, a0.lo);
-    acc = mma_bf16_k32(a, join(b0.lo, b0.lo), acc);
-    return mma_bf16_k32(a, join(b0.hi, b0.hi), acc);
+// acc += a b over 32 k, fp32
+__device__ __forceinline__ floatx4 mma(floatx4 a0, floatx4 a1, floatx4 b0, floatx4 b1, floatx4 acc) {
+    return mma_f32_k16(a1, b1, mma_f32_k16(a0, b0, acc));
 }
 
-// Rows of 128 channels in LDS, as A operands of the state product
+// Rows of 128 channels in LDS, as A operands of the state product: fp32, or
+// for bf16 inputs the same value as three bf16 (hi, mid, lo: 24 bits, exact).
 template <typename T>
 struct Rows;
 template <>
@@ -143,31 +114,46 @@ struct Rows<float> {
     static constexpr int kBytes = kFP * 4;   // of a row
     float* p;
     __device__ __forceinline__ Rows(unsigned char* base, int) : p(reinterpret_cast<float*>(base)) {}
-    __device__ __forceinline__ void put(int row, int c, Op<float> x) const {
-        *reinterpret_cast<floatx4*>(p + row * kFP + c) = x.x;
+    __device__ __forceinline__ void put(int row, int c, floatx4 x) const {
+        *reinterpret_cast<floatx4*>(p + row * kFP + c) = x;
     }
 };
 template <>
 struct Rows<bf16> {
-    static constexpr int kBytes = 2 * kBP * 2;
-    bf16* hi;
-    bf16* lo;
+    static constexpr int kBytes = 3 * kBP * 2;
+    bf16* p;
+    int part;   // from part to part
     __device__ __forceinline__ Rows(unsigned char* base, int rows)
-        : hi(reinterpret_cast<bf16*>(base)), lo(hi + rows * kBP) {}
-    __device__ __forceinline__ void put(int row, int c, Op<bf16> x) const {
-        *reinterpret_cast<bf16x4*>(hi + row * kBP + c) = x.hi;
-        *reinterpret_cast<bf16x4*>(lo + row * kBP + c) = x.lo;
+        : p(reinterpret_cast<bf16*>(base)), part(rows * kBP) {}
+    __device__ __forceinline__ void put(int row, int c, floatx4 x) const {
+#pragma unroll
+        for (int i = 0; i < 3; ++i) *reinterpret_cast<bf16x4*>(p + i * part + row * kBP + c) = take4(x);
     }
 };
 
 // 32 rows kb .. kb + 31 of one state column as the other operand: rows
-// kb + 4 g + 0..3 and kb + 16 + 4 g + 0..3, in the place of the fp32 values
+// kb + 4 g + 0..3 and kb + 16 + 4 g + 0..3
 template <typename T>
-struct StateOp {
-    Op<T> half[2];
+struct StateOp;
+template <>
+struct StateOp<float> {
+    floatx4 half[2];
     static __device__ __forceinline__ StateOp of(const floatx2 (&s)[8], int t) {
-        return StateOp{{Op<T>::of(floatx4{s[0][t], s[1][t], s[2][t], s[3][t]}),
-                        Op<T>::of(floatx4{s[4][t], s[5][t], s[6][t], s[7][t]})}};
+        return StateOp{{floatx4{s[0][t], s[1][t], s[2][t], s[3][t]}, floatx4{s[4][t], s[5][t], s[6][t], s[7][t]}}};
+    }
+};
+template <>
+struct StateOp<bf16> {
+    bf16x8 part[3];
+    static __device__ __forceinline__ StateOp of(const floatx2 (&s)[8], int t) {
+        floatx4 a = {s[0][t], s[1][t], s[2][t], s[3][t]}, b = {s[4][t], s[5][t], s[6][t], s[7][t]};
+        StateOp o;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            const bf16x4 x = take4(a), y = take4(b);
+            o.part[i] = join(x, y);
+        }
+        return o;
     }
 };
 // acc += row tiles of X times them
@@ -178,9 +164,9 @@ __device__ __forceinline__ void state_product(const Rows<float>& X, int kb, cons
     for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-            const Op<float> a{frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g)};
+            const floatx4 a = frag_k16(X.p + (16 * r + l16) * kFP, kb + 16 * half, g);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) acc[r][t] = mma(a, s[t].half[half], acc[r][t]);
+            for (int t = 0; t < 2; ++t) acc[r][t] = mma_f32_k16(a, s[t].half[half], acc[r][t]);
         }
 }
 template <int RT>
@@ -188,12 +174,19 @@ __device__ __forceinline__ void state_product(const Rows<bf16>& X, int kb, const
                                               floatx4 (&acc)[RT][2], int l16, int g) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-        const bf16* hi = X.hi + (16 * r + l16) * kBP;
-        const bf16* lo = X.lo + (16 * r + l16) * kBP;
-        const Op<bf16> a0{frag_k16(hi, kb, g), frag_k16(lo, kb, g)};
-        const Op<bf16> a1{frag_k16(hi, kb + 16, g), frag_k16(lo, kb + 16, g)};
+        bf16x8 a[3];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) acc[r][t] = mma(a0, a1, s[t].half[0], s[t].half[1], acc[r][t]);
+        for (int i = 0; i < 3; ++i) {
+            const bf16* row = X.p + i * X.part + (16 * r + l16) * kBP;
+            a[i] = join(frag_k16(row, kb, g), frag_k16(row, kb + 16, g));
+        }
+        // the parts' products down to 2^-18 of the value; the three left out are below 2^-25
+#pragma unroll
+        for (int i = 2; i >= 0; --i)
+#pragma unroll
+            for (int j = 2 - i; j >= 0; --j)
+#pragma unroll
+                for (int t = 0; t < 2; ++t) acc[r][t] = mma_bf16_k32(a[i], s[t].part[j], acc[r][t]);
     }
 }
 
@@ -299,13 +292,6 @@ __device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], M m, int 
     return acc;
 }
 
-// e^x: for bf16 results the hardware's 2^x (x log2 e rounds to |x| 2^-24, at
-// |x| <= 64 some 2^-18 of the result), for fp32 with the remainder put back
-template <typename T>
-__device__ __forceinline__ float exp_t(float x) { return __expf(x); }
-template <>
-__device__ __forceinline__ float exp_t<float>(float x) { return exp_f32(x); }
-
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
 // f(0), ..., f(N - 1) with the index a constant expression
 template <typename F, int... I>
@@ -392,12 +378,20 @@ __device__ __forceinline__ float row_max(float x) {
     return fmaxf(x, row_turned<1>(x));
 }
 
+// Rows of the state product: fp32 up to 16 nodes, where fp32 MFMA hides behind
+// the states' read (256 x 96 bf16 states of 16 nodes: 406 us, in three bf16
+// 460); beyond, for bf16 inputs, three bf16, six products of them in less than
+// half the time of one in fp32 (64 x 96, 64 nodes: 365 us against 418).
+template <typename T, int NT>
+using RowType = typename std::conditional<NT == 1, float, T>::type;
+
 // LDS of a workgroup for up to 16 NT nodes
 template <typename T, int NT>
 struct TreeLds {
     static constexpr int kN = 16 * NT;
-    static constexpr int kRowsB = kN * Rows<T>::kBytes;       // an operand array
-    static constexpr bool kTurns = NT > 2;                    // k's and q's rows in the same place
+    using R = RowType<T, NT>;
+    static constexpr int kRowsB = kN * Rows<R>::kBytes;       // an operand array
+    static constexpr bool kTurns = NT > (sizeof(R) == 2 ? 1 : 2);                    // k's and q's rows in the same place
     static constexpr bool kOver = NT > 1;                     // partial tiles in the place of the rows
     static constexpr int kPartB = Tiles<NT>::kRound * 4 * 1024;
     static constexpr int kXk = 0, kXq = kTurns ? 0 : kRowsB;
@@ -415,7 +409,7 @@ template <typename T, int NT>
 __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned char* lds, int64_t b, int h, int n) {
     using L = TreeLds<T, NT>;
     using E = Elems<T>;
-    using O = Op<T>;
+    using R = typename L::R;
     using TT = Tiles<NT>;
     using Mask = typename std::conditional<NT <= 2, uint32_t, uint64_t>::type;   // a bit per node
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
@@ -429,9 +423,9 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
     const rsrc_t kr_ = rows(a.k), qr_ = rows(a.q), vr_ = rows(a.v), lr_ = rows(a.log_alpha), or_ = rows(a.o);
     const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
 
-    const Rows<T> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN);
+    const Rows<R> Xk(lds + L::kXk, L::kN), Xq(lds + L::kXq, L::kN);
     floatx4* part = reinterpret_cast<floatx4*>(lds + L::kPart);   // [wavefront][tile of the round][lane]
-    O* gram = reinterpret_cast<O*>(lds + L::kGram);               // [tile][lane]
+    floatx4* gram = reinterpret_cast<floatx4*>(lds + L::kGram);   // [tile][lane]
     float* sbeta = reinterpret_cast<float*>(lds + L::kBeta);
     Mask* anc = reinterpret_cast<Mask*>(lds + L::kAnc);
     Mask* bad = reinterpret_cast<Mask*>(lds + L::kBad);
@@ -466,7 +460,6 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 #pragma unroll
             for (int e = 0; e < 4; ++e) vv[I][e] = E::load2(vr_, at_g + c0 * es + (16 * I + e) * row_b);
     };
-    if (!L::kOver) load_v();
     floatx2 st[4][8];
     load_state(a.S + ((size_t)b * H + h) * (kHeadDim * kHeadDim), st, g, c0);
     __builtin_amdgcn_sched_barrier(0);
@@ -522,7 +515,7 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
         }
     }
     const bool deep = __any(least < -kMaxDecay);   // (of this wavefront's channels)
-    O xk[NT][2], xq[NT][2], y[NT][2];
+    floatx4 xk[NT][2], xq[NT][2], y[NT][2];
 #pragma unroll
     for (int I = 0; I < NT; ++I)
 #pragma unroll
@@ -531,24 +524,24 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             floatx4 ex;
             if (!L::kOver || !deep) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[I][t][e]);
-                xk[I][t] = O::of(kx * ex);
-                xq[I][t] = O::of(qx * ex);
+                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(GT[I][t][e]);
+                xk[I][t] = kx * ex;
+                xq[I][t] = qx * ex;
             } else {   // (scaled once the Gram tiles are formed)
-                xk[I][t] = O::raw(kr[I][t]);
-                xq[I][t] = O::raw(qr[I][t]);
+                xk[I][t] = widen(kr[I][t]);
+                xq[I][t] = widen(qr[I][t]);
             }
             if (!deep) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[I][t][e]);
-                y[I][t] = O::of(kx * ex);
+                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(-GT[I][t][e]);
+                y[I][t] = kx * ex;
             } else {
-                y[I][t] = O::f32(GT[I][t]);
+                y[I][t] = GT[I][t];
             }
             // (one tile's conversions at a time: the registers are full)
             if (L::kOver) __builtin_amdgcn_sched_barrier(0);
         }
-    auto put_rows = [&](const Rows<T>& X, const O (&x)[NT][2]) {
+    auto put_rows = [&](const Rows<R>& X, const floatx4 (&x)[NT][2]) {
 #pragma unroll
         for (int I = 0; I < NT; ++I)
 #pragma unroll
@@ -568,7 +561,7 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             each<count>([&](auto u) {
                 constexpr int t = t0 + u();
                 constexpr int I = TT::row(t), J = TT::col(t);
-                const O(&x)[2] = TT::q(t) ? xq[I] : xk[I];
+                const floatx4(&x)[2] = TT::q(t) ? xq[I] : xk[I];
                 part[(w * TT::kRound + u()) * 64 + lane] = mma(y[J][0], y[J][1], x[0], x[1], zero4());
             });
         } else {
@@ -581,15 +574,15 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {   // (16 channels at a time: the registers are full)
                     __builtin_amdgcn_sched_barrier(0);
-                    typename E::four xi, kj;
+                    floatx4 xi, kj;
                     if (L::kOver) {
-                        xi = (TT::q(t) ? xq : xk)[I][c].as_raw();
-                        kj = xk[J][c].as_raw();
+                        xi = (TT::q(t) ? xq : xk)[I][c];
+                        kj = xk[J][c];
                     } else {   // (the rows are scaled already)
-                        xi = E::load4(TT::q(t) ? qr_ : kr_, at_kq + 16 * I * row_b + 16 * c * es);
-                        kj = E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es);
+                        xi = widen(E::load4(TT::q(t) ? qr_ : kr_, at_kq + 16 * I * row_b + 16 * c * es));
+                        kj = widen(E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es));
                     }
-                    const floatx4 Gi = y[I][c].as_f32(), Gj = y[J][c].as_f32();
+                    const floatx4 Gi = y[I][c], Gj = y[J][c];
                     floatx4 top;   // (per channel)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) top[e] = L::kOver ? row_max(Gj[e]) : 0.f;
@@ -609,22 +602,21 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
                             if (!more) break;
                             continue;
                         }
-                        asm volatile("" : "+v"(xi), "+v"(kj));   // (widened here, not kept so over the loop)
                         floatx4 z;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            const float x = L::kOver ? (float)kj[e] : finite_or_0((float)kj[e]);
-                            z[e] = in(e) ? x * exp_t<T>((top[e] - down) - Gj[e]) : 0.f;
+                            const float x = L::kOver ? kj[e] : finite_or_0(kj[e]);
+                            z[e] = in(e) ? x * exp_f32((top[e] - down) - Gj[e]) : 0.f;
                         }
-                        const O ks = O::of(z);
+                        const floatx4 ks = z;
                         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
                             // (a descendant's G is no greater than G_j: only masked entries meet the bound 0)
-                            const float x = L::kOver || TT::q(t) ? (float)xi[e] : finite_or_0((float)xi[e]);
-                            z[e] = x * exp_t<T>(fminf(Gi[e] - (top[e] - down), 0.f));
+                            const float x = L::kOver || TT::q(t) ? xi[e] : finite_or_0(xi[e]);
+                            z[e] = x * exp_f32(fminf(Gi[e] - (top[e] - down), 0.f));
                         }
-                        acc = mma(ks, O::of(z), acc);
+                        acc = mma_f32_k16(ks, z, acc);
                         if (!more) break;
                     }
                 }
@@ -648,15 +640,11 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             const int diag = !isq && I == J ? l16 : 64;   // (no node is its own ancestor in k k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = ((m >> e) & 1) && 4 * g + e != diag ? scale * x[e] : 0.f;
-            O* to = gram + TT::place(isq, I, J) * 64;
-            if (t < NT) {
-                to[lane] = O::f32(x);
-                if (!L::kOver) {
-                    __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-                    invert(reinterpret_cast<float*>(to), l16, g);
-                }
-            } else {
-                to[lane] = O::of(x);
+            floatx4* to = gram + TT::place(isq, I, J) * 64;
+            to[lane] = x;
+            if (t < NT && !L::kOver) {
+                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+                invert(reinterpret_cast<float*>(to), l16, g);
             }
         }
     });
@@ -668,9 +656,9 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             for (int t = 0; t < 2; ++t) {
                 floatx4 ex;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(y[I][t].as_f32()[e]);
-                xk[I][t] = O::of(widen(xk[I][t].as_raw()) * ex);
-                xq[I][t] = O::of(widen(xq[I][t].as_raw()) * ex);
+                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(y[I][t][e]);
+                xk[I][t] *= ex;
+                xq[I][t] *= ex;
                 __builtin_amdgcn_sched_barrier(0);
             }
     }
@@ -686,12 +674,12 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
         if (w < NT) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
         __syncthreads();
     }
-    if (L::kOver) load_v();   // (registers are free only now)
-    StateOp<T> so[4][2];
+    load_v();   // (registers are free only now)
+    StateOp<R> so[4][2];
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) so[kb][t] = StateOp<T>::of(st[kb], t);
+        for (int t = 0; t < 2; ++t) so[kb][t] = StateOp<R>::of(st[kb], t);
         state_product<NT>(Xk, 32 * kb, so[kb], held, l16, g);
         if (!L::kTurns) state_product<NT>(Xq, 32 * kb, so[kb], read, l16, g);
     }
@@ -735,23 +723,23 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
     const bool tainted = __any((bad_col[0] | bad_col[1]) != 0);
     uint32_t at_o = at_g + c0 * es;
     asm volatile("" : "+v"(at_o));   // (store offsets are formed here, not kept since v's loads)
-    O uo[NT][2];   // pseudo-values as operands
+    floatx4 uo[NT][2];   // pseudo-values as operands
 #pragma unroll
     for (int I = 0; I < NT; ++I) {
         const floatx4 bt4 = *reinterpret_cast<const floatx4*>(sbeta + 16 * I + 4 * g);
-        const floatx4 ia = gram[TT::place(false, I, I) * 64 + lane].as_f32();
+        const floatx4 ia = gram[TT::place(false, I, I) * 64 + lane];
         floatx4 prev[2] = {zero4(), zero4()};
         auto tile = [&](bool q, int J) { return gram[TT::place(q, I, J) * 64 + lane]; };
 #pragma unroll
         for (int J = 0; J + 1 < I; J += 2) {
-            const O a0 = tile(false, J), a1 = tile(false, J + 1);
+            const floatx4 a0 = tile(false, J), a1 = tile(false, J + 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) prev[t] = mma(a0, a1, uo[J][t], uo[J + 1][t], prev[t]);
         }
         if (I & 1) {
-            const O a0 = tile(false, I - 1);
+            const floatx4 a0 = tile(false, I - 1);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) prev[t] = mma(a0, uo[I - 1][t], prev[t]);
+            for (int t = 0; t < 2; ++t) prev[t] = mma_f32_k16(a0, uo[I - 1][t], prev[t]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -759,19 +747,19 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 #pragma unroll
             for (int e = 0; e < 4; ++e) rhs[e] = bt4[e] * ((float)vv[I][e][t] - held[I][t][e]);
             if (I > 0) rhs -= prev[t];
-            uo[I][t] = O::of(mma_f32_k16(ia, rhs, zero4()));
+            uo[I][t] = mma_f32_k16(ia, rhs, zero4());
         }
         floatx4 out[2] = {zero4(), zero4()};
 #pragma unroll
         for (int J = 0; J < I; J += 2) {
-            const O a0 = tile(true, J), a1 = tile(true, J + 1);
+            const floatx4 a0 = tile(true, J), a1 = tile(true, J + 1);
 #pragma unroll
             for (int t = 0; t < 2; ++t) out[t] = mma(a0, a1, uo[J][t], uo[J + 1][t], out[t]);
         }
         if (!(I & 1)) {
-            const O a0 = tile(true, I);
+            const floatx4 a0 = tile(true, I);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) out[t] = mma(a0, uo[I][t], out[t]);
+            for (int t = 0; t < 2; ++t) out[t] = mma_f32_k16(a0, uo[I][t], out[t]);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t) out[t] += read[I][t];
@@ -794,7 +782,14 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 // 21 nodes take 29.7 us at two, 26.3 at three.)  A sequence with fewer nodes
 // than the batch's N allows runs the code of one tile (N <= 32) or two where
 // that holds it; the code of a size has no branches on the number of tiles
-// (64 x 96 bf16 states of 64 nodes: 280 us with them, 266 without).
+// (64 x 96 bf16 states of 64 nodes, operands in two bf16 parts: 280 us with
+// them, 266 without).
+constexpr int smaller(int NT) { return NT > 2 ? 2 : 1; }
+template <typename T, int NT>
+constexpr int launch_lds() {
+    constexpr int less = TreeLds<T, smaller(NT)>::kBytes, own = TreeLds<T, NT>::kBytes;
+    return less > own ? less : own;
+}
 template <typename T, int NT>
 __global__ __launch_bounds__(256, NT == 1 ? (sizeof(T) == 4 ? 3 : 4) : (NT == 2 ? 3 : 2))
 void tree_decode_kernel(TreeDecodeArgs a) {
@@ -803,8 +798,7 @@ void tree_decode_kernel(TreeDecodeArgs a) {
     const int h = blockIdx.x % (unsigned)a.H;
     const int n = __builtin_amdgcn_readfirstlane(tree_count(a.n_node, b, a.N));
     if (n == 0) return;
-    constexpr int kLess = NT > 2 ? 2 : 1;
-    static_assert(TreeLds<T, kLess>::kBytes <= TreeLds<T, NT>::kBytes, "both fit the launch's LDS");
+    constexpr int kLess = smaller(NT);
     if (kLess < NT && n <= 16 * kLess) tree_decode<T, kLess>(a, lds, b, h, n);
     else tree_decode<T, NT>(a, lds, b, h, n);
 }
@@ -818,9 +812,9 @@ constexpr int kSmall = 8;
 
 template <typename T>
 struct __attribute__((aligned(16))) SmallLds {
-    unsigned char rows[16 * Rows<T>::kBytes];
+    unsigned char rows[16 * Rows<float>::kBytes];
     floatx4 part[4][64];      // the wavefronts' parts of the Gram tile
-    Op<T> gram[64];           // rows 0..7 strictly lower k k, 8..15 lower q k
+    floatx4 gram[64];         // rows 0..7 strictly lower k k, 8..15 lower q k
     float inv[256];           // (I + L)^{-1}
     float beta[16];
     uint32_t anc[kSmall];
@@ -830,7 +824,6 @@ struct __attribute__((aligned(16))) SmallLds {
 template <typename T>
 __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArgs a) {
     using E = Elems<T>;
-    using O = Op<T>;
     __shared__ SmallLds<T> lds;
     const int tid = threadIdx.x, lane = tid & 63, l16 = lane & 15, g = lane >> 4;
     const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -846,7 +839,7 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
     const uint32_t rows_b = (uint32_t)(n - 1) * row_b + kHeadDim * es;
     auto rows = [&](const void* p) { return make_rsrc_u32(static_cast<const T*>(p) + base, rows_b); };
     const int c0 = 32 * w + 2 * l16;                          // this lane's first value column
-    const Rows<T> X(lds.rows, 16);
+    const Rows<float> X(lds.rows, 16);
     const bool isq = l16 >= kSmall;
     const int i = l16 & (kSmall - 1);
 
@@ -920,23 +913,23 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
     floatx4 GT[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) GT[t] = gather_decay<1>(lar[t], m, 0, g);
-    O xo[2];
+    floatx4 xo[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         floatx4 ex;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(GT[t][e]);
-        xo[t] = O::of(widen(x[t]) * ex);
+        for (int e = 0; e < 4; ++e) ex[e] = exp_f32(GT[t][e]);
+        xo[t] = widen(x[t]) * ex;
         X.put(l16, 32 * w + 16 * t + 4 * g, xo[t]);
     }
     // (8 levels at the decay bound: |G| <= 40 where the inputs keep their contract)
-    O y[2];
+    floatx4 y[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         floatx4 ex;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ex[e] = exp_t<T>(-GT[t][e]);
-        y[t] = O::of(widen(x[t]) * ex);
+        for (int e = 0; e < 4; ++e) ex[e] = exp_f32(-GT[t][e]);
+        y[t] = widen(x[t]) * ex;
     }
     lds.part[w][lane] = mma(y[0], y[1], xo[0], xo[1], zero4());
     __syncthreads();
@@ -951,7 +944,7 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
             const bool on = ((m >> j) & 1) && (isq || j != i);
             z[e] = on ? scale * z[e] : 0.f;
         }
-        lds.gram[lane] = O::of(z);
+        lds.gram[lane] = z;
         *reinterpret_cast<floatx4*>(lds.inv + 4 * lane) = isq ? zero4() : z;
         __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
         invert<kSmall>(lds.inv, l16, g);
@@ -961,7 +954,7 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
     floatx4 acc[1][2] = {{zero4(), zero4()}};
 #pragma unroll
     for (int kb = 0; kb < 4; ++kb) {
-        const StateOp<T> so[2] = {StateOp<T>::of(st[kb], 0), StateOp<T>::of(st[kb], 1)};
+        const StateOp<float> so[2] = {StateOp<float>::of(st[kb], 0), StateOp<float>::of(st[kb], 1)};
         state_product<1>(X, 32 * kb, so, acc, l16, g);
     }
     __syncthreads();
@@ -991,14 +984,14 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
     }
     const floatx4 bt4 = *reinterpret_cast<const floatx4*>(lds.beta + 4 * g);
     const floatx4 ia = *reinterpret_cast<const floatx4*>(lds.inv + 4 * lane);
-    const O gm = lds.gram[lane];
+    const floatx4 gm = lds.gram[lane];
     floatx4 out[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         floatx4 rhs;   // (rows 8..15: beta is 0)
 #pragma unroll
         for (int e = 0; e < 4; ++e) rhs[e] = g < 2 ? bt4[e] * ((float)vv[e][t] - acc[0][t][e]) : 0.f;
-        out[t] = mma(gm, O::of(mma_f32_k16(ia, rhs, zero4())), acc[0][t]);
+        out[t] = mma_f32_k16(gm, mma_f32_k16(ia, rhs, zero4()), acc[0][t]);
     }
     // rows 8..15 are the outputs of nodes 0..7
     if (__any((bad_col[0] | bad_col[1]) != 0)) {
@@ -1019,7 +1012,7 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
 template <typename T, int NT>
 hipError_t launch_nt(const TreeDecodeArgs& a, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
-    constexpr int bytes = TreeLds<T, NT>::kBytes;
+    constexpr int bytes = launch_lds<T, NT>();
     const auto kern = tree_decode_kernel<T, NT>;
     if (bytes > 64 * 1024) {
         const hipError_t e = raise_lds_limit_once(reinterpret_cast<const void*>(kern), bytes, done);
