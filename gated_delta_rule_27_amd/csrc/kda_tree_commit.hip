@@ -9,7 +9,12 @@
 //   S <- Diag(e^{G_e}) S + sum_t (k_t o e^{G_e - G_t}) u_t^T.
 // 16 tokens at the decay bound keep e^{-G} below e^80, finite in fp32.
 // Everything is fp32 on fp32 MFMA: the state is fp32 and carries every
-// rounding on to the tokens after it.
+// rounding on to the tokens after it.  G in one float would be off by up to
+// 2^-18 at |G| of 64 to 80, and e^{G_t} e^{-G_j} by that of its value (4e-6 to
+// 7e-6 of the state where 12 tokens decay strongly and 4 hardly, token by token
+// 1.5e-7; with two floats 1.7e-7).  So log alpha is summed as multiples of
+// 2^-17, exactly (16 of them at the bound stay below 2^7), and the rests of
+// at most 2^-18 beside them.
 //
 // Mapping.  One workgroup of four wavefronts per (sequence, head) (two heads
 // of eight wavefronts stream whole 128 KB blocks but wait for each other:
@@ -40,6 +45,7 @@ namespace {
 
 constexpr int kTok = 16;              // path tokens of a block
 constexpr int kXP = kHeadDim + 4;     // a token row in LDS
+constexpr float kGrid = 96.f;         // added and taken off: a multiple of 2^-17, for |x| <= 32
 constexpr int kStream = 2;            // states pass the caches by (the non-temporal policy)
 typedef unsigned int uintx2_t __attribute__((ext_vector_type(2)));
 
@@ -198,10 +204,12 @@ __global__ __launch_bounds__(256, kLong ? 2 : 4) void tree_commit_kernel(TreeCom
             floatx4 x, y, kk, gm;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const float G = row_prefix_sum(lr[t][e]), ex = exp_f32(G);
+                const float whole = (lr[t][e] + kGrid) - kGrid;
+                const float G = row_prefix_sum(whole), rest = row_prefix_sum(lr[t][e] - whole);
+                const float ex = exp_f32(G, rest);
                 x[e] = kr[t][e] * ex;
-                y[e] = kr[t][e] * exp_f32(-G);
-                kk[e] = kr[t][e] * exp_f32(row_bcast<15>(G) - G);
+                y[e] = kr[t][e] * exp_f32(-G, -rest);
+                kk[e] = kr[t][e] * exp_f32(row_bcast<15>(G) - G, row_bcast<15>(rest) - rest);
                 gm[e] = row_bcast<15>(ex);
             }
             *reinterpret_cast<floatx4*>(lds.X + l16 * kXP + c) = x;
