@@ -12,16 +12,21 @@
 // state is ever formed: all nodes share one product with the cached state,
 // two N x N Gram tiles masked by ancestry, and a unit lower triangular solve
 // (nodes are in topological order).  G itself is a product of the 0/1
-// ancestor matrix with the nodes' log alpha.
+// ancestor matrix with the nodes' log alpha.  In one float it would be off by
+// 2^-18 at |G| of 64 and by 2^-16 at 320, and every coupling of the node by
+// that of its value (outputs of nodes that keep their state below a strongly
+// decayed one: 2e-5 to 3e-5 off; now at most 2e-6, where 1e-6 comes with
+// any factors e^{G_i}, e^{-G_j} of 24 bits).  So it is summed in two parts, the
+// first exactly, and held as a whole number of 2^-22.
 //
 // Range.  e^{-G_j} stays finite for at most 16 levels at the decay bound
-// (log alpha >= -5).  Where some |G| of a wavefront's channels passes
-// kMaxDecay, a Gram tile is the sum of products over levels of G_j, 64 wide,
-// from the greatest G_j of its tile of ancestors down: in a level the factors
-// are e^{r - G_j} <= e^64 and, for descendants, e^{G_i - r} <= 1, r the level's
+// (log alpha >= -5).  Where some |G| of a wavefront's channels passes 64, a
+// Gram tile is the sum of products over levels of G_j, 64 wide, from the
+// greatest G_j of its tile of ancestors down: in a level the factors are
+// e^{r - G_j} <= e^64 and, for descendants, e^{G_i - r} <= 1, r the level's
 // upper end, per channel.  What underflows there is below e^{-23} of the
-// level's largest entries.  (64 x 96 bf16 states, chains of 64: 508 us where
-// log alpha is -0.7 on average and some |G| pass 64, 619 at -2.5, 370 where
+// level's largest entries.  (64 x 96 bf16 states, chains of 64: 495 us where
+// log alpha is -0.7 on average and some |G| pass 64, 586 at -2.5, 362 where
 // none does; pair by pair, with e^{G_i - G_j}, the first two took 1330 and 2540.)
 //
 // Masking.  Products with masked (zero) entries would spread a NaN or
@@ -52,17 +57,17 @@
 // MFMA or bf16 MFMA on both operands in three bf16 parts.  (In two parts, 16
 // bits, a read of neighbouring state rows with opposite signs lost what
 // differs between them, as kda_decode_multi does not; 64 x 96 states of 64
-// nodes took 254 us in two parts, 365 now, 32 nodes 128 against 170, 256 x 96
-// of 8 nodes 304 against 307.)
+// nodes took 254 us in two parts, 359 now, 32 nodes 128 against 171, 256 x 96
+// of 8 nodes 304 against 308.)
 //
 // What bounds it, measured on bf16 inputs: the states' read up to 16 nodes,
-// while four workgroups share a compute unit (256 x 96 states, 8 nodes: 307
-// us, 6.1 TB/s of everything read and written, 16 nodes 411 us, 5.3 TB/s);
+// while four workgroups share a compute unit (256 x 96 states, 8 nodes: 308
+// us, 6.0 TB/s of everything read and written, 16 nodes 418 us, 5.1 TB/s);
 // from then on MFMA (fp32 for Gram tiles and solve) and the chain of load,
-// Gram rounds, solve and outputs of a workgroup (64 x 96: 32 nodes 170 us, 3.9
-// TB/s, 64 nodes 365 us, 2.5 TB/s and 71 TFLOP/s).  fp32 inputs: fp32 MFMA from
-// 17 nodes on (64 x 96: 16 nodes 116 us, 32 nodes 221 us, 64 nodes 454 us).
-// One sequence of 8 nodes x 96 heads: 6.6 us, the latency of one workgroup.
+// Gram rounds, solve and outputs of a workgroup (64 x 96: 32 nodes 171 us, 3.8
+// TB/s, 64 nodes 359 us, 2.5 TB/s and 72 TFLOP/s).  fp32 inputs: fp32 MFMA from
+// 17 nodes on (64 x 96: 16 nodes 117 us, 32 nodes 221 us, 64 nodes 444 us).
+// One sequence of 8 nodes x 96 heads: 6.9 us, the latency of one workgroup.
 #include <type_traits>
 #include <utility>
 
@@ -74,9 +79,8 @@ namespace kda {
 
 namespace {
 
-constexpr float kMaxDecay = 64.f;   // |G| up to which e^{-G} is formed
+constexpr float kGrid = 768.f;      // added and taken off: a multiple of 2^-14, for |x| <= 256
 constexpr int kLevels = 8;          // steps of it below a tile's greatest G (64 nodes of log alpha >= -5: five)
-constexpr float kNothing = -90.f;   // e^ of which is 0 in fp32
 constexpr int kFP = kHeadDim + 4;   // fp32 LDS row
 constexpr int kBP = kHeadDim + 8;   // bf16 LDS row
 
@@ -260,37 +264,79 @@ __device__ __forceinline__ bf16x4 bits4(uint32_t b) {
     return __builtin_bit_cast(bf16x4, u2{lo * 0x3f80u, hi * 0x3f80u});
 }
 
-// G^T of 16 nodes (columns) and 16 channels: log alpha^T (a: channel l16,
-// nodes 16 J + 4 g + 0..3) times the ancestor bits of node l16
-template <int NT, typename M>
-__device__ __forceinline__ floatx4 gather_decay(const floatx4 (&a)[NT], M m, int I, int g) {
-    floatx4 acc = zero4();
-#pragma unroll
-    for (int J = 0; J < NT; ++J) {
-        if (J > I) break;
-        const uint32_t bits = (uint32_t)(m >> (16 * J + 4 * g));
-        acc = mma_f32_k16(a[J], floatx4{(bits & 1) ? 1.f : 0.f, (bits & 2) ? 1.f : 0.f,
-                                        (bits & 4) ? 1.f : 0.f, (bits & 8) ? 1.f : 0.f}, acc);
-    }
-    return acc;
+typedef int intx4 __attribute__((ext_vector_type(4)));
+
+// G as a whole number of 2^-22, down to -511
+constexpr int kOne = 1 << 22;
+constexpr int kLevelBits = 28;
+constexpr int kDecay = 1 << kLevelBits;   // |G| of 64: up to it e^{-G} is formed
+constexpr int kNothing = 90 * kOne;       // e^ of minus which is 0 in fp32
+// e^G, and e^{-G}: the exponent in two parts, the first exact in fp32
+__device__ __forceinline__ floatx2 exp_both(int G) {
+    return exp_both_f32((float)(G >> 8) * 0x1p-14f, (float)(G & 255) * 0x1p-22f);
 }
-// (bf16 log alpha times 0 or 1 is exact)
-template <int NT, typename M>
-__device__ __forceinline__ floatx4 gather_decay(const bf16x4 (&a)[NT], M m, int I, int g) {
-    floatx4 acc = zero4();
+__device__ __forceinline__ float exp_whole(int G) { return exp_both(G)[0]; }
+
+// log alpha^T of 16 channels as operands: multiples of 2^-14, of which sums
+// down to -320 are exact in fp32, and the rests of at most 2^-15 (their sums
+// are off by 2^-33); a fp32 value takes two bf16 for each (17 bits hold the
+// first where log alpha >= -5), a bf16 value one
+template <typename T, int NT>
+struct Decays {
+    static constexpr int kParts = sizeof(T) == 4 ? 2 : 1, kPairs = (NT + 1) / 2;
+    bf16x8 whole[kParts][kPairs], rest[kParts][kPairs];   // of nodes 32 J + 4 g + 0..3, 32 J + 16 + 4 g + 0..3
+
+    template <typename V>
+    __device__ __forceinline__ void split(const V (&a)[NT]) {
 #pragma unroll
-    for (int J = 0; J < NT; J += 2) {
-        if (J > I) break;
-        const bf16 z = (bf16)0.f;
-        const bf16x4 zero = {z, z, z, z};
-        const bool two = J + 1 < NT;
-        acc = mma_bf16_k32(join(a[J], two ? a[two ? J + 1 : J] : zero),
-                           join(bits4((uint32_t)(m >> (16 * J + 4 * g))),
-                                two ? bits4((uint32_t)(m >> (two ? 16 * J + 16 + 4 * g : 0))) : zero),
-                           acc);
+        for (int J = 0; J < kPairs; ++J) {
+            floatx4 w[2], r[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const floatx4 x = 2 * J + h < NT ? widen(a[2 * J + h < NT ? 2 * J + h : 0]) : zero4();
+                w[h] = (x + kGrid) - kGrid;
+                r[h] = x - w[h];
+            }
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const bf16x4 w0 = take4(w[0]), w1 = take4(w[1]);
+                whole[p][J] = join(w0, w1);
+            }
+            r[0] += w[0];   // (0 within the bound)
+            r[1] += w[1];
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                const bf16x4 r0 = take4(r[0]), r1 = take4(r[1]);
+                rest[p][J] = join(r0, r1);
+            }
+        }
     }
-    return acc;
-}
+    // G^T of 16 nodes (columns) and the 16 channels: times the ancestor bits
+    // of node l16
+    template <typename M>
+    __device__ __forceinline__ intx4 gather(M m, int I, int g) const {
+        floatx4 x = zero4(), r = zero4();
+#pragma unroll
+        for (int J = 0; J < kPairs; ++J) {
+            if (2 * J > I) break;
+            const bool two = 2 * J + 1 < NT;
+            const bf16x4 b0 = bits4((uint32_t)(m >> (32 * J + 4 * g)));
+            const bf16x4 b1 = bits4(two ? (uint32_t)(m >> (two ? 32 * J + 16 + 4 * g : 0)) : 0u);
+            const bf16x8 b = join(b0, b1);
+#pragma unroll
+            for (int p = 0; p < kParts; ++p) {
+                x = mma_bf16_k32(whole[p][J], b, x);
+                r = mma_bf16_k32(rest[p][J], b, r);
+            }
+        }
+        intx4 G;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)   // (the bounds are met outside the contract of log alpha only)
+            G[e] = (int)(__builtin_amdgcn_fmed3f(x[e], -510.f, 510.f) * kOne) +
+                   (int)__builtin_rintf(__builtin_amdgcn_fmed3f(r[e], -1.f, 1.f) * kOne);
+        return G;
+    }
+};
 
 __device__ __forceinline__ float finite_or_0(float x) { return x - x == 0.f ? x : 0.f; }
 // f(0), ..., f(N - 1) with the index a constant expression
@@ -367,21 +413,20 @@ struct Tiles {
 
 // greatest x of a row of 16 lanes, in all of them (rotations by 8, 4, 2, 1)
 template <int kBy>
-__device__ __forceinline__ float row_turned(float x) {
-    return __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), 0x120 + kBy, 0xf, 0xf,
-                                                                 false));
+__device__ __forceinline__ int row_turned(int x) {
+    return __builtin_amdgcn_update_dpp(0, x, 0x120 + kBy, 0xf, 0xf, false);
 }
-__device__ __forceinline__ float row_max(float x) {
-    x = fmaxf(x, row_turned<8>(x));
-    x = fmaxf(x, row_turned<4>(x));
-    x = fmaxf(x, row_turned<2>(x));
-    return fmaxf(x, row_turned<1>(x));
+__device__ __forceinline__ int row_max(int x) {
+    x = max(x, row_turned<8>(x));
+    x = max(x, row_turned<4>(x));
+    x = max(x, row_turned<2>(x));
+    return max(x, row_turned<1>(x));
 }
 
 // Rows of the state product: fp32 up to 16 nodes, where fp32 MFMA hides behind
 // the states' read (256 x 96 bf16 states of 16 nodes: 406 us, in three bf16
 // 460); beyond, for bf16 inputs, three bf16, six products of them in less than
-// half the time of one in fp32 (64 x 96, 64 nodes: 365 us against 418).
+// half the time of one in fp32 (64 x 96, 64 nodes: 365 us against 418 then).
 template <typename T, int NT>
 using RowType = typename std::conditional<NT == 1, float, T>::type;
 
@@ -392,12 +437,11 @@ struct TreeLds {
     using R = RowType<T, NT>;
     static constexpr int kRowsB = kN * Rows<R>::kBytes;       // an operand array
     static constexpr bool kTurns = NT > (sizeof(R) == 2 ? 1 : 2);                    // k's and q's rows in the same place
-    static constexpr bool kOver = NT > 1;                     // partial tiles in the place of the rows
     static constexpr int kPartB = Tiles<NT>::kRound * 4 * 1024;
     static constexpr int kXk = 0, kXq = kTurns ? 0 : kRowsB;
     static constexpr int kRowsEnd = (kTurns ? 1 : 2) * kRowsB;
-    static constexpr int kPart = kOver ? 0 : kRowsEnd;
-    static constexpr int kGram = kOver ? (kRowsEnd > kPartB ? kRowsEnd : kPartB) : kRowsEnd + kPartB;
+    static constexpr int kPart = 0;                           // partial tiles in the place of the rows
+    static constexpr int kGram = kRowsEnd > kPartB ? kRowsEnd : kPartB;
     static constexpr int kBeta = kGram + Tiles<NT>::kAll * 1024;
     static constexpr int kAnc = kBeta + kN * 4;               // (8 bytes a node)
     static constexpr int kBad = kAnc + kN * 8;                // per wavefront: nodes with non-finite inputs
@@ -502,44 +546,43 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
         }
     }
     if (lane == 0) bad[w] = bad_node;
-    floatx4 GT[NT][2];
-    float least = 0.f;
+    intx4 GT[NT][2];
+    int least = 0;
 #pragma unroll
-    for (int I = 0; I < NT; ++I) {
-        const Mask m = __shfl(mask, 16 * I + l16, 64);
+    for (int t = 0; t < 2; ++t) {
+        Decays<T, NT> d;
+        d.split(lar[t]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            GT[I][t] = gather_decay<NT>(lar[t], m, I, g);
+        for (int I = 0; I < NT; ++I) {
+            GT[I][t] = d.gather(__shfl(mask, 16 * I + l16, 64), I, g);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) least = fminf(least, GT[I][t][e]);
+            for (int e = 0; e < 4; ++e) least = min(least, GT[I][t][e]);
         }
     }
-    const bool deep = __any(least < -kMaxDecay);   // (of this wavefront's channels)
+    const bool deep = __any(least < -kDecay);   // (of this wavefront's channels)
     floatx4 xk[NT][2], xq[NT][2], y[NT][2];
 #pragma unroll
     for (int I = 0; I < NT; ++I)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const floatx4 kx = widen(kr[I][t]), qx = widen(qr[I][t]);
-            floatx4 ex;
-            if (!L::kOver || !deep) {
+            floatx4 ex, over;
+            if (!deep) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(GT[I][t][e]);
+                for (int e = 0; e < 4; ++e) {
+                    const floatx2 both = exp_both(GT[I][t][e]);
+                    ex[e] = both[0];
+                    over[e] = both[1];
+                }
                 xk[I][t] = kx * ex;
                 xq[I][t] = qx * ex;
             } else {   // (scaled once the Gram tiles are formed)
-                xk[I][t] = widen(kr[I][t]);
-                xq[I][t] = widen(qr[I][t]);
+                xk[I][t] = kx;
+                xq[I][t] = qx;
             }
-            if (!deep) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(-GT[I][t][e]);
-                y[I][t] = kx * ex;
-            } else {
-                y[I][t] = GT[I][t];
-            }
+            y[I][t] = deep ? __builtin_bit_cast(floatx4, GT[I][t]) : kx * over;
             // (one tile's conversions at a time: the registers are full)
-            if (L::kOver) __builtin_amdgcn_sched_barrier(0);
+            __builtin_amdgcn_sched_barrier(0);
         }
     auto put_rows = [&](const Rows<R>& X, const floatx4 (&x)[NT][2]) {
 #pragma unroll
@@ -547,10 +590,6 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 #pragma unroll
             for (int t = 0; t < 2; ++t) X.put(16 * I + l16, 32 * w + 16 * t + 4 * g, x[I][t]);
     };
-    if (!L::kOver) {
-        put_rows(Xk, xk);
-        put_rows(Xq, xq);
-    }
 
     // ---- Gram tiles, transposed: ancestors x nodes --------------------------
     each<(TT::kAll + TT::kRound - 1) / TT::kRound>([&](auto round) {
@@ -565,8 +604,8 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
                 part[(w * TT::kRound + u()) * 64 + lane] = mma(y[J][0], y[J][1], x[0], x[1], zero4());
             });
         } else {
-            // level by level down from the tile's greatest G_j (0 for 16 nodes): those of 64 at a time,
-            // referred to the greatest that they may have
+            // level by level down from the tile's greatest G_j: those of 64 at a time, referred to the
+            // greatest that they may have
             each<count>([&](auto u) {
                 constexpr int t = t0 + u();
                 constexpr int I = TT::row(t), J = TT::col(t);
@@ -574,48 +613,42 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {   // (16 channels at a time: the registers are full)
                     __builtin_amdgcn_sched_barrier(0);
-                    floatx4 xi, kj;
-                    if (L::kOver) {
-                        xi = (TT::q(t) ? xq : xk)[I][c];
-                        kj = xk[J][c];
-                    } else {   // (the rows are scaled already)
-                        xi = widen(E::load4(TT::q(t) ? qr_ : kr_, at_kq + 16 * I * row_b + 16 * c * es));
-                        kj = widen(E::load4(kr_, at_kq + 16 * J * row_b + 16 * c * es));
-                    }
-                    const floatx4 Gi = y[I][c], Gj = y[J][c];
-                    floatx4 top;   // (per channel)
+                    const floatx4 xi = (TT::q(t) ? xq : xk)[I][c], kj = xk[J][c];
+                    const intx4 Gi = __builtin_bit_cast(intx4, y[I][c]), Gj = __builtin_bit_cast(intx4, y[J][c]);
+                    intx4 below;   // of G_j under the tile's greatest, per channel
+                    intx4 under;   // of G_i
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) top[e] = L::kOver ? row_max(Gj[e]) : 0.f;
+                    for (int e = 0; e < 4; ++e) {
+                        const int top = row_max(Gj[e]);
+                        below[e] = top - Gj[e];
+                        under[e] = top - Gi[e];
+                    }
 #pragma unroll 1
                     for (int m = 0; m < kLevels; ++m) {
-                        const float down = kMaxDecay * m, to = m < kLevels - 1 ? kMaxDecay + down : INFINITY;
-                        auto in = [&](int e) { return Gj[e] <= top[e] - down && Gj[e] > top[e] - to; };
-                        bool some = false, felt = false, below = false;
+                        const int down = kDecay * m;
+                        // (formed from these each time, not kept over the loop)
+                        if (NT == 1) asm volatile("" : "+v"(below), "+v"(under));
+                        bool some = false, felt = false, further = false;
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            some |= in(e);
-                            below |= Gj[e] <= top[e] - to;
-                            felt |= Gi[e] - (top[e] - down) > kNothing;
+                            some |= (below[e] >> kLevelBits) == m;
+                            further |= (below[e] >> kLevelBits) > m;
+                            felt |= under[e] - down < kNothing;
                         }
-                        const bool more = __any(below);
+                        const bool more = __any(further);
                         if (!__any(some) || !__any(felt)) {
                             if (!more) break;
                             continue;
                         }
-                        floatx4 z;
+                        floatx4 ks, z;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float x = L::kOver ? kj[e] : finite_or_0(kj[e]);
-                            z[e] = in(e) ? x * exp_f32((top[e] - down) - Gj[e]) : 0.f;
-                        }
-                        const floatx4 ks = z;
+                        for (int e = 0; e < 4; ++e)
+                            ks[e] = (below[e] >> kLevelBits) == m ? kj[e] * exp_whole(below[e] - down) : 0.f;
                         __builtin_amdgcn_sched_barrier(0);
+                        // (a descendant's G is no greater than G_j but for its rounding: only masked entries
+                        // meet the bound)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            // (a descendant's G is no greater than G_j: only masked entries meet the bound 0)
-                            const float x = L::kOver || TT::q(t) ? xi[e] : finite_or_0(xi[e]);
-                            z[e] = x * exp_f32(fminf(Gi[e] - (top[e] - down), 0.f));
-                        }
+                        for (int e = 0; e < 4; ++e) z[e] = xi[e] * exp_whole(min(down - under[e], kOne));
                         acc = mma_f32_k16(ks, z, acc);
                         if (!more) break;
                     }
@@ -642,21 +675,17 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             for (int e = 0; e < 4; ++e) x[e] = ((m >> e) & 1) && 4 * g + e != diag ? scale * x[e] : 0.f;
             floatx4* to = gram + TT::place(isq, I, J) * 64;
             to[lane] = x;
-            if (t < NT && !L::kOver) {
-                __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-                invert(reinterpret_cast<float*>(to), l16, g);
-            }
         }
     });
 
-    if (L::kOver && deep) {
+    if (deep) {
 #pragma unroll
         for (int I = 0; I < NT; ++I)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 floatx4 ex;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ex[e] = exp_f32(y[I][t][e]);
+                for (int e = 0; e < 4; ++e) ex[e] = exp_whole(__builtin_bit_cast(intx4, y[I][t])[e]);
                 xk[I][t] *= ex;
                 xq[I][t] *= ex;
                 __builtin_amdgcn_sched_barrier(0);
@@ -667,13 +696,11 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
     floatx4 held[NT][2], read[NT][2];
 #pragma unroll
     for (int r = 0; r < NT; ++r) held[r][0] = held[r][1] = read[r][0] = read[r][1] = zero4();
-    if (L::kOver) {
-        __syncthreads();   // the last round has been summed
-        put_rows(Xk, xk);
-        if (!L::kTurns) put_rows(Xq, xq);
-        if (w < NT) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
-        __syncthreads();
-    }
+    __syncthreads();   // the last round has been summed
+    put_rows(Xk, xk);
+    if (!L::kTurns) put_rows(Xq, xq);
+    if (w < NT) invert(reinterpret_cast<float*>(gram + TT::place(false, w, w) * 64), l16, g);
+    __syncthreads();
     load_v();   // (registers are free only now)
     StateOp<R> so[4][2];
 #pragma unroll
@@ -689,8 +716,6 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
         __syncthreads();
 #pragma unroll
         for (int kb = 0; kb < 4; ++kb) state_product<NT>(Xq, 32 * kb, so[kb], read, l16, g);
-    } else if (!L::kOver) {
-        __syncthreads();   // (the Gram tiles are there)
     }
 
     // ---- pseudo-values and outputs, block by block --------------------------
@@ -791,7 +816,7 @@ constexpr int launch_lds() {
     return less > own ? less : own;
 }
 template <typename T, int NT>
-__global__ __launch_bounds__(256, NT == 1 ? (sizeof(T) == 4 ? 3 : 4) : (NT == 2 ? 3 : 2))
+__global__ __launch_bounds__(256, NT == 1 ? 4 : (NT == 2 ? 3 : 2))
 void tree_decode_kernel(TreeDecodeArgs a) {
     extern __shared__ __attribute__((aligned(16))) unsigned char lds[];
     const int64_t b = blockIdx.x / (unsigned)a.H;
@@ -910,26 +935,24 @@ __global__ __launch_bounds__(256, 4) void tree_decode_small_kernel(TreeDecodeArg
 
     // ---- G^T, scaled rows, this wavefront's part of the Gram tile -------------
     const uint32_t m = __shfl(mask, i, 64);
-    floatx4 GT[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) GT[t] = gather_decay<1>(lar[t], m, 0, g);
-    floatx4 xo[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-        floatx4 ex;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) ex[e] = exp_f32(GT[t][e]);
-        xo[t] = widen(x[t]) * ex;
-        X.put(l16, 32 * w + 16 * t + 4 * g, xo[t]);
-    }
+    floatx4 xo[2], y[2];
     // (8 levels at the decay bound: |G| <= 40 where the inputs keep their contract)
-    floatx4 y[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-        floatx4 ex;
+        Decays<T, 1> d;
+        d.split(lar[t]);
+        const intx4 G = d.gather(m, 0, g);
+        const floatx4 z = widen(x[t]);
+        floatx4 ex, over;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) ex[e] = exp_f32(-GT[t][e]);
-        y[t] = widen(x[t]) * ex;
+        for (int e = 0; e < 4; ++e) {
+            const floatx2 both = exp_both(G[e]);
+            ex[e] = both[0];
+            over[e] = both[1];
+        }
+        xo[t] = z * ex;
+        y[t] = z * over;
+        X.put(l16, 32 * w + 16 * t + 4 * g, xo[t]);
     }
     lds.part[w][lane] = mma(y[0], y[1], xo[0], xo[1], zero4());
     __syncthreads();

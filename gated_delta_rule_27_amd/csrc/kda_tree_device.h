@@ -7,19 +7,21 @@
 
 namespace kda {
 
-// e^(x + rest) to an ulp or two for |x| <= 87, |rest| <= 2^-13, from the
-// hardware's 2^x: x log2 e as a product p and what its rounding leaves, with
-// log2 e in two parts, the remainder r put back as the factor 1 + r ln 2 + rest.
-// (Arguments here are finite and <= 88; below -87 the result may be flushed to
-// 0.)
-__device__ __forceinline__ float exp_f32(float x, float rest = 0.f) {
+// e^(x + rest), and e^-(x + rest), to an ulp or two for |x| <= 87, |rest| <=
+// 2^-13, from the hardware's 2^x: x log2 e as a product p and what its rounding
+// leaves, with log2 e in two parts, the remainder r put back as the factor 1 +
+// r ln 2 + rest.  (Arguments here are finite and <= 88; below -87 the result
+// may be flushed to 0.)
+__device__ __forceinline__ floatx2 exp_both_f32(float x, float rest) {
     constexpr float kL = 1.44269504088896340736f;                       // log2 e to 24 bits
     constexpr float kLlo = (float)(1.44269504088896340736 - (double)kL);
     const float p = x * kL;
     const float r = __builtin_fmaf(x, kLlo, __builtin_fmaf(x, kL, -p));
-    const float y = __builtin_amdgcn_exp2f(p);
-    return __builtin_fmaf(y, __builtin_fmaf(r, 0.69314718055994530942f, rest), y);
+    const float t = __builtin_fmaf(r, 0.69314718055994530942f, rest);
+    const float y = __builtin_amdgcn_exp2f(p), z = __builtin_amdgcn_exp2f(-p);
+    return floatx2{__builtin_fmaf(y, t, y), __builtin_fmaf(z, -t, z)};
 }
+__device__ __forceinline__ float exp_f32(float x, float rest) { return exp_both_f32(x, rest)[0]; }
 
 // (I + L)^{-1} of a strictly lower triangular tile in place; element (i, j)
 // lies at lane 16 (j / 4) + i, j % 4.  One lane per column, row by row; rows
