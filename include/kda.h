@@ -430,9 +430,12 @@ kda_status kda_tree_prologue(const void* xq, const void* xk, const void* xv,
  * The KDA outputs of every node of a tree from one read of the cached state,
  * which is not written: with S_i = (I - beta_i k_i k_i^T) Diag(alpha_i)
  * S_parent(i) + beta_i k_i v_i^T, o_i = S_i^T q_i.  Node i gives what
- * kda_decode_multi would on the path from the root to i, to rounding.  A NaN
- * or infinity among node i's inputs makes outputs NaN of i and of the nodes
- * that descend from it, of no other node.
+ * kda_decode_multi would on the path from the root to i, to the rounding of
+ * an evaluation that holds 24 bits of every operand, whatever dt, and rounds
+ * to dt once.  A NaN or infinity of node i reaches no other nodes than those
+ * that descend from it: in k, log_alpha or beta it makes NaN of all outputs of
+ * i and of its descendants, in v of that column of theirs, and in q it makes
+ * i's own outputs non-finite.
  *
  *   q, k, log_alpha : [B, N, H, Dk]  dt
  *   v               : [B, N, H, Dv]  dt
