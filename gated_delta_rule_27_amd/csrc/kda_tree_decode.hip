@@ -293,7 +293,10 @@ struct Decays {
             floatx4 w[2], r[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const floatx4 x = 2 * J + h < NT ? widen(a[2 * J + h < NT ? 2 * J + h : 0]) : zero4();
+                floatx4 x = 2 * J + h < NT ? widen(a[2 * J + h < NT ? 2 * J + h : 0]) : zero4();
+                // (the bounds are far outside the contract; past the greatest bf16 the parts would be infinite)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[e] = __builtin_amdgcn_fmed3f(x[e], -120.f, 120.f);
                 w[h] = (x + kGrid) - kGrid;
                 r[h] = x - w[h];
             }

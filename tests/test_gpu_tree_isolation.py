@@ -114,3 +114,28 @@ def test_the_decay_bound_at_small_sizes(dtype, shape, N):
         print(f"    sequence {b}: off by {err:.2e} (bound {bound:.2e}), outputs up to {np.abs(ref).max():.2e}", flush=True)
         assert err <= bound
         assert (o[b, n[b]:] == SENTINEL).all()
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("N", [12, 20, 40, 64])
+def test_the_lowest_log_alpha_reaches_descendants_only(dtype, N):
+    """A finite log alpha far outside its contract, the type's lowest value:
+    like an infinity it stays with its node and the nodes below it."""
+    kda = need_gpu()
+    case(f"tree_decode, lowest log alpha, {dtype} N={N}")
+    w = node_inputs(1, N, 2, dtype, seed=9 + N)
+    par = random_trees(1, N, 4, "tree")
+    a = [w[x] for x in ("q", "k", "v", "log_alpha", "beta")]
+    o1 = kda.kda_tree_decode(*a, w["S"], i32(par))
+    tol = torch.finfo(DT[dtype]).eps * (dtype == "bf16") + 2 * 50 * 2.0 ** -24   # (as above)
+    ways = otree.paths(par[0], N)
+    for node in (N // 2, 3):
+        old = w["log_alpha"][0, node, 1].clone()
+        w["log_alpha"][0, node, 1, COLUMN] = torch.finfo(DT[dtype]).min
+        o2 = kda.kda_tree_decode(*a, w["S"], i32(par))
+        torch.cuda.synchronize()
+        other = torch.tensor([node not in ways[i] for i in range(N)], device="cuda")
+        assert other.sum() >= 3 and torch.equal(o1[0, :, 0], o2[0, :, 0])
+        assert torch.isfinite(o2[0, other, 1]).all()
+        assert nerr(np_(o2[0, other, 1]), np_(o1[0, other, 1])) <= tol, node
+        w["log_alpha"][0, node, 1] = old
