@@ -74,8 +74,15 @@ hipError_t launch_tree_commit(const TreeCommitArgs& a, int dtype, hipStream_t st
 // Workgroups of the tree prologue per group of sequences: q, k, v x two-head
 // slices, then the gates' four-head slices.
 inline int64_t tree_prologue_tasks(int32_t H) { return 3 * (((int64_t)H + 1) / 2) + ((int64_t)H + 3) / 4; }
-// Sequences of a group: more than one once there are workgroups enough (256
-// sequences of 16 nodes x 96 heads: 200, 181, 180, 185 us at 1, 2, 4, 8).
+// Sequences of a group: more than one once there are workgroups enough.  At 1,
+// 2, 4, 8 (x 96 heads, us; * what the rule takes):
+//   256 x 16 nodes  bf16 196 175 172* 175   fp32 313 317 306* 325
+//   256 x  4 nodes  bf16  81  72  69*  70
+//    64 x 64 nodes  bf16 172 172 186* 211   fp32 304 311 318* 360
+//    64 x 16 nodes  bf16  43  45  49*  52
+//    32 x 16 nodes  bf16  25  26*  28  38
+//     8 x 64 nodes  bf16  30* 36  49   74
+// many short trees gain up to 15%, a few long ones lose up to 12%.
 inline int32_t tree_prologue_sequences(int32_t B, int32_t H) {
     const int64_t n = (int64_t)B * tree_prologue_tasks(H) / 2048;
     return n < 1 ? 1 : (n > 4 ? 4 : (int32_t)n);

@@ -28,13 +28,16 @@
 // the operand of X S and the accumulator of the update.
 //
 // What bounds it: reading and writing the states while paths are one block
-// (256 x 96 bf16, paths of up to 8, one in nine empty: 480 us, 6.4 TB/s; a
-// kernel that only copies the states' pattern reaches 5.9 to 6.1 without empty
-// ones); with paths of more blocks the blocks' chain, at two workgroups per
-// compute unit (64 x 96: 32 tokens 224 us against 149 for 16).  One sequence
+// (256 x 96 bf16, paths of up to 8, one in nine empty: 480 us, 2.89 GB by the
+// counters, 6.0 TB/s; a kernel that only copies the states' pattern reaches 5.9
+// to 6.1); with paths of more blocks the blocks' chain, at three workgroups per
+// compute unit (64 x 96: 32 tokens 217 us against 146 for 16).  One sequence
 // of 8 tokens x 96 heads: 9 us, the latency of one workgroup; fetching path
 // and count side by side and the first entries only once took off 0.15 us and
-// was not kept.
+// was not kept.  The instance goes by the width P of the path array, which the
+// host knows, not by the counts: 1 to 8 tokens in arrays of 64 instead of 8
+// take 580 us against 580 for 256 x 96 states, 43 against 41 for 16 x 96, 10.7
+// against 9.3 for one sequence.
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_tree_device.h"

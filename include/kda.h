@@ -509,6 +509,8 @@ kda_status kda_tree_accept(const void* p, const void* q, const int32_t* tokens,
  *   beta         : [B, N, H]      dt
  *   S            : [B, H, Dk, Dv] fp32, updated IN PLACE
  *   path         : [B, P] int32; a path ends before an entry outside [0, N)
+ *                  (P > 16 runs the code of long paths, 1 to 2 us a call slower
+ *                  on short ones in small batches, the same in large ones)
  *   n_path       : [B] int32, entries to apply, clamped to [0, P]; NULL = P
  *   xq, xk, xv   : [B, N, H, Dk]  dt, the inputs of the convolution
  *   conv_state   : [B, 3 (q, k, v), 3 (tokens), H, Dk] dt, updated IN PLACE
