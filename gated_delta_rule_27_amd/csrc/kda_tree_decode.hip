@@ -110,7 +110,7 @@ __device__ __forceinline__ floatx4 mma(floatx4 a0, floatx4 a1, floatx4 b0, float
 }
 
 // Rows of 128 channels in LDS, as A operands of the state product: fp32, or
-// for bf16 inputs the same value as three bf16 (hi, mid, lo: 24 bits, exact).
+// for bf16 inputs the same value as three bf16 (24 bits, exact).
 template <typename T>
 struct Rows;
 template <>
@@ -436,10 +436,10 @@ using RowType = typename std::conditional<NT == 1, float, T>::type;
 // LDS of a workgroup for up to 16 NT nodes
 template <typename T, int NT>
 struct TreeLds {
-    static constexpr int kN = 16 * NT;
     using R = RowType<T, NT>;
+    static constexpr int kN = 16 * NT;
     static constexpr int kRowsB = kN * Rows<R>::kBytes;       // an operand array
-    static constexpr bool kTurns = NT > (sizeof(R) == 2 ? 1 : 2);                    // k's and q's rows in the same place
+    static constexpr bool kTurns = NT > (sizeof(R) == 2 ? 1 : 2);   // k's and q's rows in the same place
     static constexpr int kPartB = Tiles<NT>::kRound * 4 * 1024;
     static constexpr int kXk = 0, kXq = kTurns ? 0 : kRowsB;
     static constexpr int kRowsEnd = (kTurns ? 1 : 2) * kRowsB;
@@ -676,8 +676,7 @@ __device__ __forceinline__ void tree_decode(const TreeDecodeArgs& a, unsigned ch
             const int diag = !isq && I == J ? l16 : 64;   // (no node is its own ancestor in k k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) x[e] = ((m >> e) & 1) && 4 * g + e != diag ? scale * x[e] : 0.f;
-            floatx4* to = gram + TT::place(isq, I, J) * 64;
-            to[lane] = x;
+            gram[TT::place(isq, I, J) * 64 + lane] = x;
         }
     });
 

@@ -487,9 +487,10 @@ kda_status kda_tree_decode(const void* q, const void* k, const void* v,
  * probabilities: finite, >= 0, rows summing to 1 up to rounding (not
  * checked; a NaN or negative weight counts as 0, nothing out of range is
  * ever read or written, and the next token lies in [0, V)).
- * 1 <= V <= KDA_MAX_VOCAB.  p and q 16-byte aligned, the int32 and fp32
- * arrays 4-byte aligned.  Any overlap of an output with another buffer is
- * KDA_ERR_ALIAS.
+ * 1 <= V <= KDA_MAX_VOCAB.  p and q 16-byte aligned (their rows need not be;
+ * a slice of a batch over an odd vocabulary may start where it is refused),
+ * the int32 and fp32 arrays 4-byte aligned.  Any overlap of an output with
+ * another buffer is KDA_ERR_ALIAS.
  */
 #define KDA_MAX_VOCAB (1 << 22)
 
