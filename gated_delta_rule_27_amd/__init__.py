@@ -31,6 +31,9 @@ Functions (same names as the C entry points):
   the layer's prologue and the KDA outputs of all nodes with the cached state
   untouched, the accepted path and next token, and state and convolution
   history moved along that path;
+* ``kda_cache_store``, ``kda_cache_load``, ``kda_cache_decode`` and
+  ``kda_cache_fold``  serving from a cache that holds states in 8 bits, with
+  the last few tokens' updates beside them;
 * ``kda_chunk_fwd_workspace_size``, ``kda_status_str``, ``kda_abi_version``.
 """
 import ctypes
@@ -116,6 +119,14 @@ def lib():
         L.kda_tree_commit.restype = ctypes.c_int
         L.kda_tree_commit.argtypes = [vp] * 7 + [i32, i32, i32, i32, i32, i32, ctypes.c_int] + \
             [vp] * 5
+        L.kda_cache_store.restype = ctypes.c_int
+        L.kda_cache_store.argtypes = [vp] * 2 + [i32] * 5 + [vp] * 3
+        L.kda_cache_load.restype = ctypes.c_int
+        L.kda_cache_load.argtypes = [vp] * 7 + [i32] * 6 + [ctypes.c_int, vp, vp]
+        L.kda_cache_decode.restype = ctypes.c_int
+        L.kda_cache_decode.argtypes = [vp] * 11 + [i32] * 5 + [ctypes.c_int, vp, vp]
+        L.kda_cache_fold.restype = ctypes.c_int
+        L.kda_cache_fold.argtypes = [vp] * 6 + [i32] * 5 + [ctypes.c_int, vp]
         _lib = L
     return _lib
 
@@ -850,6 +861,148 @@ def kda_tree_commit(k, v, log_alpha, beta, S, path, n_path=None, *, conv=None):
     return S
 
 
+MAX_WINDOW = 16        # KDA_MAX_WINDOW
+
+
+def _pages(codes):
+    """The measures of a cache: pages, heads, GPU."""
+    torch = _torch()
+    if not isinstance(codes, torch.Tensor):
+        raise TypeError("codes must be a torch.Tensor")
+    if codes.dim() != 4 or codes.shape[2:] != (HEAD_DIM, HEAD_DIM):
+        raise ValueError(f"codes must be [P, H, {HEAD_DIM}, {HEAD_DIM}] (got {tuple(codes.shape)})")
+    gpu = codes.get_device()
+    if gpu < 0:
+        raise ValueError(f"codes must be on a ROCm device (got {codes.device})")
+    return codes.shape[0], codes.shape[1], gpu
+
+
+def _window(window, P, H, gpu, dt=None):
+    """Addresses, length and dtype of a window (k, log_alpha, u)."""
+    if len(window) != 3:
+        raise ValueError("window must be (k, log_alpha, u)")
+    if window[0] is None or window[1] is None or window[2] is None:
+        raise ValueError("window must be (k, log_alpha, u)")
+    shape, own, _, code = _first(window[0], "window", 4)
+    W = shape[2]
+    dt = own if dt is None else dt
+    return _need(("window",) * 3, window, (P, H, W, HEAD_DIM), dt, gpu), W, code
+
+
+def kda_cache_store(S, codes=None, scale=None, page=None):
+    """fp32 states into a cache that holds them in 8 bits.
+
+    S: [B, H, 128, 128] fp32; codes: int8 [P, H, 128 (value), 128 (key)] and
+    scale: fp32 [P, H, 128 (key)], written in place (or made, of B pages, if
+    both are None); page: int32 [B], the page each state goes to (outside [0,
+    P): left out; of several states for one page the last one counts), or None
+    (state b to page b).  S[i][j] is held as scale[i] * codes[j][i].  Returns
+    (codes, scale)."""
+    torch = _torch()
+    shape, _, gpu, _ = _first(S, "S", 4)
+    B, H, Dk, Dv = shape
+    if codes is None and scale is None and page is None:
+        codes = torch.empty((B, H, Dv, Dk), dtype=torch.int8, device=S.device)
+        scale = torch.empty((B, H, Dk), dtype=torch.float32, device=S.device)
+    elif codes is None or scale is None:
+        raise TypeError("codes and scale are given together, and with page")
+    P = codes.shape[0] if isinstance(codes, torch.Tensor) and codes.dim() == 4 else B
+    st = _one(S, "S", shape, torch.float32, gpu)
+    to = (_one(codes, "codes", (P, H, Dv, Dk), torch.int8, gpu),
+          _one(scale, "scale", (P, H, Dk), torch.float32, gpu))
+    way = _one(page, "page", (B,), torch.int32, gpu)
+    _check(_on_device(gpu, lib().kda_cache_store, st, way, B, P, H, Dk, Dv, *to))
+    return codes, scale
+
+
+def kda_cache_load(codes, scale, page=None, window=None, n_win=None, *, S=None):
+    """Pages of an 8-bit cache back into fp32 states, with the updates of
+    their windows.
+
+    codes, scale as for kda_cache_store; page: int32 [B], the page each state
+    is read from (outside [0, P): the state is not written), or None (page b,
+    every page or as many as S has); window: (k, log_alpha, u), each [P, H, W, 128]
+    bf16 or fp32, or None; n_win: int32 [B], the window's tokens to apply to
+    each state (clamped to [0, W]), or None (W each).  Returns S [B, H, 128,
+    128] fp32."""
+    torch = _torch()
+    P, H, gpu = _pages(codes)
+    _required(scale=scale)
+    if page is not None:
+        if not isinstance(page, torch.Tensor) or page.dim() != 1:
+            raise ValueError("page must be an int32 tensor [B]")
+        B = page.shape[0]
+    else:
+        B = S.shape[0] if isinstance(S, torch.Tensor) and S.dim() == 4 else P
+    c = _one(codes, "codes", (P, H, HEAD_DIM, HEAD_DIM), torch.int8, gpu)
+    sc = _one(scale, "scale", (P, H, HEAD_DIM), torch.float32, gpu)
+    way = _one(page, "page", (B,), torch.int32, gpu)
+    if window is None:
+        if n_win is not None:
+            raise ValueError("n_win is given with a window")
+        win, W, code = (None,) * 3, 1, KDA_BF16
+    else:
+        win, W, code = _window(window, P, H, gpu)
+    count = _one(n_win, "n_win", (B,), torch.int32, gpu)
+    if S is None:
+        make = torch.zeros if page is not None else torch.empty   # (rows without a page)
+        S = make((B, H, HEAD_DIM, HEAD_DIM), dtype=torch.float32, device=codes.device)
+    _check(_on_device(gpu, lib().kda_cache_load, c, sc, way, *win, count, B, P, H, W, HEAD_DIM,
+                      HEAD_DIM, code,
+                      _one(S, "S", (B, H, HEAD_DIM, HEAD_DIM), torch.float32, gpu)))
+    return S
+
+
+def kda_cache_decode(q, k, v, log_alpha, beta, codes, scale, window, n_win, *, o=None):
+    """One recurrent step for a batch of states in an 8-bit cache.
+
+    q, k, log_alpha, v: [B, H, 128]; beta: [B, H] (bf16 or fp32, one dtype);
+    codes, scale: B pages as kda_cache_store writes them, read only; window:
+    (k, log_alpha, u), each [B, H, W, 128] in the input dtype, W <= 16: places
+    below n_win[b] are read and place n_win[b] is written; n_win: int32 [B]
+    (outside [0, W): an idle place of the batch, left as it is), which the
+    caller then counts up.  Returns o [B, H, 128] in the input dtype (rows of
+    idle places are not written)."""
+    torch = _torch()
+    if q is None or k is None or v is None or log_alpha is None or beta is None or codes is None or scale is None \
+            or window is None or n_win is None:
+        _required(q=q, k=k, v=v, log_alpha=log_alpha, beta=beta, codes=codes, scale=scale, window=window,
+                  n_win=n_win)
+    shape, dt, gpu, code = _first(q, "q", 3)
+    B, H, D = shape
+    ins = _need(("q", "k", "v", "log_alpha"), (q, k, v, log_alpha), shape, dt, gpu)
+    b = _one(beta, "beta", (B, H), dt, gpu)
+    c = _one(codes, "codes", (B, H, D, D), torch.int8, gpu)
+    sc = _one(scale, "scale", (B, H, D), torch.float32, gpu)
+    win, W, _ = _window(window, B, H, gpu, dt)
+    count = _one(n_win, "n_win", (B,), torch.int32, gpu)
+    if o is None:
+        o = torch.empty_like(q)
+    _check(_on_device(gpu, lib().kda_cache_decode, *ins, b, c, sc, *win, count, B, H, W, D, D, code,
+                      _one(o, "o", shape, dt, gpu)))
+    return o
+
+
+def kda_cache_fold(codes, scale, window, n_win=None):
+    """The updates of the windows taken into the 8-bit states, in place (after
+    which the caller counts the windows as empty).
+
+    codes, scale: B pages as kda_cache_store writes them; window: (k,
+    log_alpha, u), each [B, H, W, 128] bf16 or fp32; n_win: int32 [B], tokens
+    of each window (clamped to [0, W]; 0: the state stays as it is), or None
+    (W each).  Returns (codes, scale)."""
+    torch = _torch()
+    B, H, gpu = _pages(codes)
+    _required(scale=scale, window=window)
+    c = _one(codes, "codes", (B, H, HEAD_DIM, HEAD_DIM), torch.int8, gpu)
+    sc = _one(scale, "scale", (B, H, HEAD_DIM), torch.float32, gpu)
+    win, W, code = _window(window, B, H, gpu)
+    count = _one(n_win, "n_win", (B,), torch.int32, gpu)
+    _check(_on_device(gpu, lib().kda_cache_fold, c, sc, *win, count, B, H, W, HEAD_DIM, HEAD_DIM,
+                      code))
+    return codes, scale
+
+
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_step",
            "kda_decode_multi", "kda_segment_summary", "kda_segment_scan", "kda_prologue",
            "kda_epilogue", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size",
@@ -857,4 +1010,5 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_
            "kda_chunk_fwd_workspace_size", "kda_status_str", "kda_abi_version", "KDAError",
            "kda_tree_prologue", "kda_tree_decode", "kda_tree_accept",
            "kda_tree_commit", "MAX_TREE", "MAX_VOCAB",
-           "MAX_PATH", "lib", "LIB_PATH"]
+           "MAX_PATH", "kda_cache_store", "kda_cache_load", "kda_cache_decode",
+           "kda_cache_fold", "MAX_WINDOW", "lib", "LIB_PATH"]

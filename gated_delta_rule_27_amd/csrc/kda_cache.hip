@@ -1,0 +1,270 @@
+// kda_cache.hip -- fp32 states into the 8-bit cache, back, and a window's
+// updates taken into the 8-bit state in place.
+#include "kda.h"
+#include "kda_cache.h"
+#include "kda_device.h"
+#include "kda_tree_device.h"
+
+namespace kda {
+
+namespace {
+
+constexpr int kD = kHeadDim;
+constexpr int kLd = 36;   // dwords of a value channel's 128 codes in LDS, with padding
+
+typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
+
+// The workgroup's four wavefronts hold a state as blocks of four rows and
+// four columns a lane: block t of wavefront w, lane (half, l) covers rows
+// 32 w + 8 t + 4 half + 0..3 and columns 4 l + 0..3, so that a row's loads and
+// stores are whole lines and four rows' codes of a column are one dword.
+struct Place {
+    int l, half, wave;
+    __device__ Place() : l(threadIdx.x & 31), half((threadIdx.x >> 5) & 1), wave(threadIdx.x >> 6) {}
+    __device__ __forceinline__ int row(int t) const { return 32 * wave + 8 * t + 4 * half; }
+};
+typedef floatx4 State[4][4];   // [block][row], four columns
+
+// e^x of a sum of log alpha (exp_f32 takes arguments that are finite)
+__device__ __forceinline__ float decay(float x) { return exp_f32(x < -120.f ? -120.f : x, 0.f); }
+
+__device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
+// largest of 32 lanes (the magnitudes' bits: a NaN is larger than anything)
+template <int kCtrl>
+__device__ __forceinline__ uint32_t max_with(uint32_t x) {
+    return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, kCtrl, 0xf, 0xf, true));
+}
+__device__ __forceinline__ uint32_t max32(uint32_t x) {
+    x = max_with<0x128>(x);   // rotations of a row of 16 by 8, 4, 2, 1
+    x = max_with<0x124>(x);
+    x = max_with<0x122>(x);
+    x = max_with<0x121>(x);
+    return max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401f));   // the other row
+}
+
+// the code of x, in the low byte
+__device__ __forceinline__ uint32_t code(float x, float inverse) {
+#pragma clang fp contract(off)
+    // (adding 1.5 * 2^23 rounds to a whole number, ties to even, and leaves it
+    // in the low bits; the product is rounded before, as written)
+    const float y = x * inverse;
+    return __builtin_bit_cast(uint32_t, y + 12582912.f);
+}
+
+// scales and codes of a state out, through an LDS tile of [value][key] codes
+struct QuantiseLds {
+    uint32_t tile[kD * kLd];
+    uint32_t top[kD];      // largest magnitude of each row
+    float inverse[kD];
+};
+__device__ __forceinline__ void quantise(const State& v, const Place& p, QuantiseLds& lds, int8_t* codes, float* scale) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        uint32_t m[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[r] = max(m[r], magnitude(v[t][r][e]));
+            m[r] = max32(m[r]);
+        }
+        if (p.l == 0) *reinterpret_cast<uintx4*>(lds.top + p.row(t)) = uintx4{m[0], m[1], m[2], m[3]};
+    }
+    __syncthreads();
+    if (threadIdx.x < kD) {
+        const uint32_t m = lds.top[threadIdx.x];
+        const float top = __builtin_bit_cast(float, m);
+        const bool held = m >= 0x0d800000u;   // 2^-100
+        lds.inverse[threadIdx.x] = held ? 127.f / top : 0.f;
+        // (a row with a NaN or an infinity reads back as NaN)
+        scale[threadIdx.x] = !held ? 0.f : m >= 0x7f800000u ? __builtin_nanf("") : top / 127.f;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const floatx4 inverse = *reinterpret_cast<const floatx4*>(lds.inverse + p.row(t));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = __builtin_amdgcn_perm(code(v[t][1][e], inverse[1]), code(v[t][0][e], inverse[0]), 0x0c0c0400u);
+            const uint32_t hi = __builtin_amdgcn_perm(code(v[t][3][e], inverse[3]), code(v[t][2][e], inverse[2]), 0x04000c0cu);
+            lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)] = lo | hi;
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int piece = threadIdx.x + 256 * s;   // 16 bytes: eight of a value channel
+        const uintx4 x = *reinterpret_cast<const uintx4*>(lds.tile + (piece >> 3) * kLd + 4 * (piece & 7));
+        __builtin_nontemporal_store(x, reinterpret_cast<uintx4*>(codes) + piece);
+    }
+}
+
+// LDS of a state read back: codes, then (with a window) the keys as far as
+// they are decayed, the updates, and what each row is multiplied by
+struct ReadLds {
+    uint32_t tile[kD * kLd];
+    float row[kD];
+};
+struct WindowLds {
+    float k[kMaxWindow][kD];
+    float u[kMaxWindow][kD];
+};
+
+template <typename T>
+__device__ __forceinline__ void read_state(State& v, const Place& p, ReadLds& lds, WindowLds* wl, const int8_t* codes,
+                                           const float* scale, const CacheWindow& w, int64_t at, int n) {
+    uintx4 x[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        x[s] = __builtin_nontemporal_load(reinterpret_cast<const uintx4*>(codes) + threadIdx.x + 256 * s);
+    const int i = threadIdx.x & (kD - 1);
+    if (n > 0) {
+        const int64_t base = at * w.W * kD + i;
+        if (threadIdx.x < kD) {
+            const T* k = static_cast<const T*>(w.k) + base;
+            const T* la = static_cast<const T*>(w.log_alpha) + base;
+            float kt[kMaxWindow], lt[kMaxWindow];
+#pragma unroll
+            for (int t = 0; t < kMaxWindow; ++t) {
+                if (t < n) {
+                    kt[t] = to_f32(k[t * kD]);
+                    lt[t] = to_f32(la[t * kD]);
+                }
+            }
+            float g = 0.f;
+#pragma unroll
+            for (int t = kMaxWindow - 1; t >= 0; --t) {
+                if (t < n) {
+                    wl->k[t][i] = kt[t] * decay(g);
+                    g += lt[t];
+                }
+            }
+            lds.row[i] = scale[i] * decay(g);
+        } else {
+            const T* u = static_cast<const T*>(w.u) + base;
+#pragma unroll
+            for (int t = 0; t < kMaxWindow; ++t)
+                if (t < n) wl->u[t][i] = to_f32(u[t * kD]);
+        }
+    } else if (threadIdx.x < kD) {
+        lds.row[i] = scale[i];
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int piece = threadIdx.x + 256 * s;
+        *reinterpret_cast<uintx4*>(lds.tile + (piece >> 3) * kLd + 4 * (piece & 7)) = x[s];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const floatx4 m = *reinterpret_cast<const floatx4*>(lds.row + p.row(t));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int d = (int)lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[t][r][e] = (float)(int8_t)(d >> (8 * r)) * m[r];
+        }
+    }
+    for (int t = 0; t < n; ++t) {
+        const floatx4 u = *reinterpret_cast<const floatx4*>(&wl->u[t][4 * p.l]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const floatx4 k = *reinterpret_cast<const floatx4*>(&wl->k[t][p.row(b)]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[b][r] += k[r] * u;
+        }
+    }
+}
+
+__device__ __forceinline__ int window_count(const CacheWindow& w, int64_t b) {
+    if (!w.k) return 0;
+    const int n = w.n ? w.n[b] : w.W;
+    return n < 0 ? 0 : (n > w.W ? w.W : n);
+}
+
+__global__ __launch_bounds__(256) void cache_store_kernel(CacheMoveArgs a) {
+    __shared__ __align__(16) QuantiseLds lds;
+    const uint32_t unit = blockIdx.x;
+    const int b = (int)(unit / (uint32_t)a.H), h = (int)(unit % (uint32_t)a.H);
+    const int page = a.page ? a.page[b] : b;
+    if (page < 0 || page >= a.P) return;
+    const Place p;
+    State v;
+    const float* S = a.S + (size_t)unit * kD * kD + 4 * p.l;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            v[t][r] = __builtin_nontemporal_load(reinterpret_cast<const floatx4*>(S + (p.row(t) + r) * kD));
+    if (a.page) {
+        // of several states for one page the last one counts
+        int later = 0;
+        for (int j = b + 1 + (int)threadIdx.x; j < a.B; j += 256) later |= a.page[j] == page;
+        if (__syncthreads_or(later)) return;
+    }
+    const size_t at = (size_t)page * a.H + h;
+    quantise(v, p, lds, a.codes + at * kD * kD, a.scale + at * kD);
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
+    __shared__ __align__(16) ReadLds lds;
+    __shared__ __align__(16) WindowLds wl;
+    const uint32_t unit = blockIdx.x;
+    const int b = (int)(unit / (uint32_t)a.H), h = (int)(unit % (uint32_t)a.H);
+    const int page = a.page ? a.page[b] : b;
+    if (page < 0 || page >= a.P) return;
+    const Place p;
+    State v;
+    const size_t at = (size_t)page * a.H + h;
+    read_state<T>(v, p, lds, &wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, (int64_t)at, window_count(a.win, b));
+    float* S = a.S + (size_t)unit * kD * kD + 4 * p.l;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+            __builtin_nontemporal_store(v[t][r], reinterpret_cast<floatx4*>(S + (p.row(t) + r) * kD));
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void cache_fold_kernel(CacheMoveArgs a) {
+    __shared__ __align__(16) union {
+        ReadLds in;
+        QuantiseLds out;
+    } lds;
+    __shared__ __align__(16) WindowLds wl;
+    const uint32_t unit = blockIdx.x;
+    const int b = (int)(unit / (uint32_t)a.H);
+    const int n = window_count(a.win, b);
+    if (n == 0) return;
+    const Place p;
+    State v;
+    int8_t* codes = a.codes + (size_t)unit * kD * kD;
+    float* scale = a.scale + (size_t)unit * kD;
+    read_state<T>(v, p, lds.in, &wl, codes, scale, a.win, unit, n);
+    __syncthreads();   // (what is read is read)
+    quantise(v, p, lds.out, codes, scale);
+}
+
+}  // namespace
+
+hipError_t launch_cache_store(const CacheMoveArgs& a, hipStream_t stream) {
+    cache_store_kernel<<<dim3((unsigned)((int64_t)a.B * a.H)), dim3(256), 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_load(const CacheMoveArgs& a, int dtype, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
+    if (dtype == 0) cache_load_kernel<float><<<grid, block, 0, stream>>>(a);
+    else cache_load_kernel<bf16><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+hipError_t launch_cache_fold(const CacheMoveArgs& a, int dtype, hipStream_t stream) {
+    const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
+    if (dtype == 0) cache_fold_kernel<float><<<grid, block, 0, stream>>>(a);
+    else cache_fold_kernel<bf16><<<grid, block, 0, stream>>>(a);
+    return hipGetLastError();
+}
+
+}  // namespace kda

@@ -531,6 +531,115 @@ kda_status kda_tree_commit(const void* k, const void* v, const void* log_alpha,
                            const void* xv, void* conv_state,
                            hipStream_t stream);
 
+/*
+ * The state cache in 8 bits.  A cached state is held as codes in -127..127
+ * and one scale per key channel,
+ *
+ *     codes : [.., H, Dv, Dk] int8   (value channel, then key channel)
+ *     scale : [.., H, Dk] fp32       S[i][j] = scale[i] * codes[j][i],
+ *
+ * scale[i] = (largest |S[i][j]| over j) / 127 and codes[j][i] = S[i][j] *
+ * (127 / largest) rounded to the nearest whole number, ties to even, each
+ * operation in fp32: half a scale step off at the most.  A key channel without
+ * a magnitude of 2^-100 or more is held as zeros; one with a NaN or an
+ * infinity reads back as NaN.  The decay Diag(alpha) multiplies key channels,
+ * so the scales take it up and the codes keep their bits.
+ *
+ * Beside the 8-bit state lies a window of up to W tokens whose rank-one
+ * updates are not yet in it: the tokens' keys k_t and log-decays log alpha_t
+ * and their updates u_t = beta_t (v_t - S'^T k_t), S' the state before token
+ * t's write, decayed by it, so that after the window's first n tokens
+ *
+ *     S = Diag(e^(G_0)) Diag(scale) codes^T
+ *         + sum over t < n of (e^(G_(t+1)) k_t) u_t^T,
+ *     G_t = log alpha_t + ... + log alpha_(n-1).
+ *
+ *     win_k, win_log_alpha : [.., H, W, Dk] dt
+ *     win_u                : [.., H, W, Dv] dt
+ *     n_win : int32 device, tokens in each window.  The caller keeps it, one
+ *             for all the layers of a model: kda_cache_decode puts its token
+ *             at place n_win, after which the caller counts one more;
+ *             kda_cache_fold empties a window, after which the caller sets 0.
+ * 1 <= W <= KDA_MAX_WINDOW.  A state is rounded to its codes once per fold and
+ * not once per token.  B * H < 2^24, else KDA_ERR_BAD_SHAPE; B == 0 is allowed
+ * (nothing is launched).  Pointers are 16-byte aligned, n_win and page 4-byte.
+ * No call keeps anything between calls or uses scratch memory.
+ */
+#define KDA_MAX_WINDOW 16
+
+/*
+ * fp32 states (final states of a prefill, prefix snapshots) into the cache.
+ *
+ *   S     : [B, H, Dk, Dv] fp32, read only
+ *   page  : [B] int32 device, the page each state goes to; a state whose page
+ *           lies outside [0, P) is left out, and of several states for one
+ *           page the last one counts.  NULL = state b to page b (B <= P)
+ *   codes : [P, H, Dv, Dk], scale : [P, H, Dk], outputs; pages not named are
+ *           not written
+ * Any overlap of an output with another buffer is KDA_ERR_ALIAS.
+ */
+kda_status kda_cache_store(const float* S, const int32_t* page, int32_t B, int32_t P,
+                           int32_t H, int32_t Dk, int32_t Dv, int8_t* codes,
+                           float* scale, hipStream_t stream);
+
+/*
+ * Pages of the cache back into fp32 states, with their windows' updates.
+ *
+ *   codes, scale : [P, ..]; win_k, win_log_alpha, win_u : [P, H, W, ..] dt,
+ *           all three NULL = no windows (n_win, W and dt are then not looked at)
+ *   page  : [B] int32, the page each state is read from (several may read the
+ *           same one); outside [0, P) the state is not written.  NULL = page b
+ *   n_win : [B] int32, the tokens to apply to each state, clamped to [0, W];
+ *           NULL = W
+ *   S     : [B, H, Dk, Dv] fp32, output
+ * S overlapping another buffer is KDA_ERR_ALIAS.
+ */
+kda_status kda_cache_load(const int8_t* codes, const float* scale, const int32_t* page,
+                          const void* win_k, const void* win_log_alpha,
+                          const void* win_u, const int32_t* n_win, int32_t B,
+                          int32_t P, int32_t H, int32_t W, int32_t Dk, int32_t Dv,
+                          kda_dtype dt, float* S, hipStream_t stream);
+
+/*
+ * One recurrent step for a batch of states in the 8-bit cache: kda_decode_step
+ * with the state read from codes, scale and window, and the token appended to
+ * the window.  With S the state before, S' = Diag(alpha) S:
+ *
+ *     u = beta (v - S'^T k), held in dt,    o = S'^T q + (k . q) u.
+ *
+ *   q, k, log_alpha : [B, H, Dk]  dt;  v : [B, H, Dv] dt;  beta : [B, H] dt
+ *   codes, scale    : [B, ..], read only
+ *   win_k, win_log_alpha, win_u : [B, H, W, ..] dt, places below n_win[b]
+ *                     read, place n_win[b] written
+ *   n_win           : [B] int32, required; a sequence whose n_win lies outside
+ *                     [0, W) is idle: nothing of it is read or written
+ *   o               : [B, H, Dv]  dt
+ * The reads of the state are exact sums of products of the codes with 31-bit
+ * vectors; a NaN or infinity in q makes NaN of the head's outputs, one in k or
+ * log_alpha of its outputs and its update.  Any overlap of o or the window
+ * with another buffer is KDA_ERR_ALIAS.
+ */
+kda_status kda_cache_decode(const void* q, const void* k, const void* v,
+                            const void* log_alpha, const void* beta,
+                            const int8_t* codes, const float* scale, void* win_k,
+                            void* win_log_alpha, void* win_u, const int32_t* n_win,
+                            int32_t B, int32_t H, int32_t W, int32_t Dk, int32_t Dv,
+                            kda_dtype dt, void* o, hipStream_t stream);
+
+/*
+ * The windows' updates into the 8-bit states, in place: what kda_cache_load
+ * gives, rounded to codes and scales anew.
+ *
+ *   n_win : [B] int32, tokens to take in, clamped to [0, W]; NULL = W.  A
+ *           sequence with none keeps its state untouched.
+ * The windows are read only.  codes or scale overlapping another buffer is
+ * KDA_ERR_ALIAS.
+ */
+kda_status kda_cache_fold(int8_t* codes, float* scale, const void* win_k,
+                          const void* win_log_alpha, const void* win_u,
+                          const int32_t* n_win, int32_t B, int32_t H, int32_t W,
+                          int32_t Dk, int32_t Dv, kda_dtype dt, hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* kda_status_str(kda_status s);
 

@@ -1,0 +1,74 @@
+"""CPU oracle for the 8-bit state cache -- TEST INFRASTRUCTURE ONLY (same rule
+as the rest of ``oracle``).
+
+``quantise`` is the rounding of a state to codes and scales, operation by
+operation in float32 as it is defined; everything else goes through the
+window token by token in float64.  Beside each result stands a bound on what
+an evaluation in 32 bits may be off: 2^-24 times the sum of the magnitudes
+that are added up, each with the roundings that its factors have seen.
+"""
+import numpy as np
+
+EPS = 2.0 ** -24          # half a step of fp32, relative
+TINY = np.float32(2.0 ** -100)
+HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}   # half a step of the type (24 and 8 bits), relative
+
+
+def quantise(S):
+    """float32 states [.., 128 (key), 128 (value)] -> codes [.., value, key]
+    int8 and scales [.., key] float32."""
+    S = np.asarray(S, dtype=np.float32)
+    top = np.abs(S).max(-1)
+    held = top >= TINY
+    with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
+        inverse = np.where(held, np.float32(127) / top, np.float32(0)).astype(np.float32)
+        scale = np.where(held, top / np.float32(127), np.float32(0)).astype(np.float32)
+        codes = np.rint((S * inverse[..., None]).astype(np.float32)).astype(np.int8)
+    return np.swapaxes(codes, -1, -2), scale
+
+
+def values(codes, scale):
+    """float64 states [.., key, value] of codes and scales."""
+    return np.swapaxes(np.asarray(codes, np.float64), -1, -2) * np.asarray(scale, np.float64)[..., None]
+
+
+def state(codes, scale, k, la, u, n):
+    """One head's state after the first n tokens of its window (k, la, u [W,
+    128] float64) and the bound of its entries."""
+    S = values(codes, scale)
+    # weights: the roundings that a term has seen, times its magnitude.  A decay over tokens of
+    # log alpha l is off by (their number) * |sum of l| + 4 roundings of its exponential
+    terms = [(S, np.zeros(128), 0)]
+    for t in range(n):
+        terms = [(x * np.exp(la[t])[:, None], g + la[t], m + 1) for x, g, m in terms]
+        terms.append((k[t][:, None] * u[t][None, :], np.zeros(128), 0))
+    total = sum(x for x, _, _ in terms)
+    bound = EPS * sum(np.abs(x) * ((m + 1) * np.abs(g) + n + 8)[:, None] for x, g, m in terms)
+    return total, bound
+
+
+def decode(q, k, v, la, beta, codes, scale, wk, wla, wu, n):
+    """One head's token: the update before it is rounded, its bound; and a
+    function of the update as it is held that gives the output and its bound."""
+    S, off = state(codes, scale, wk, wla, wu, n)
+    d = np.exp(la)[:, None]
+    S, off = d * S, d * (off + EPS * np.abs(S) * ((n + 2) * np.abs(la) + 4)[:, None])
+    c = np.abs(values(codes, np.ones(128, np.float32)))
+    whole = np.exp(np.sum(wla[:n], 0) + la) * np.asarray(scale, np.float64)
+
+    def read(x):
+        # a vector times 128 terms: a sum of as many roundings as its depth, 16 at the most, and the
+        # vector's entries to 2^-30 of its largest
+        fixed = 2.0 ** -30 * np.abs(x * whole).max() * c.sum(0)
+        return x @ S, np.abs(x) @ off + 16 * EPS * (np.abs(x) @ np.abs(S)) + fixed
+
+    sk, bk = read(k)
+    u = beta * (v - sk)
+    bu = np.abs(beta) * (bk + 4 * EPS * (np.abs(v) + np.abs(sk)))
+
+    def output(held):
+        sq, bq = read(q)
+        kq = float(k @ q)
+        return sq + kq * held, bq + EPS * (16 * (np.abs(k) @ np.abs(q)) * np.abs(held) + 4 * np.abs(sq))
+
+    return u, bu, output
