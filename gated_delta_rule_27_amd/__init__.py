@@ -34,6 +34,8 @@ Functions (same names as the C entry points):
 * ``kda_cache_store``, ``kda_cache_load``, ``kda_cache_decode`` and
   ``kda_cache_fold``  serving from a cache that holds states in 8 bits, with
   the last few tokens' updates beside them;
+* ``kda_sample``  the next token from logits by temperature, top-k, top-p,
+  min-p and given random numbers, and the probabilities it is drawn with;
 * ``kda_chunk_fwd_workspace_size``, ``kda_status_str``, ``kda_abi_version``.
 """
 import ctypes
@@ -127,6 +129,10 @@ def lib():
         L.kda_cache_decode.argtypes = [vp] * 11 + [i32] * 5 + [ctypes.c_int, vp, vp]
         L.kda_cache_fold.restype = ctypes.c_int
         L.kda_cache_fold.argtypes = [vp] * 6 + [i32] * 5 + [ctypes.c_int, vp]
+        L.kda_sample_workspace_size.restype = sz
+        L.kda_sample_workspace_size.argtypes = [i32, i32]
+        L.kda_sample.restype = ctypes.c_int
+        L.kda_sample.argtypes = [vp] * 6 + [i32, i32, ctypes.c_int, vp, vp, vp, sz, vp]
         _lib = L
     return _lib
 
@@ -1003,6 +1009,53 @@ def kda_cache_fold(codes, scale, window, n_win=None):
     return codes, scale
 
 
+def kda_sample_workspace_size(R, V):
+    return lib().kda_sample_workspace_size(int(R), int(V))
+
+
+def kda_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=None, *, token=None,
+               probs=None):
+    """The next token of every row of logits, and the probabilities it is drawn
+    with.
+
+    logits: [..., V] bf16 or fp32; u: fp32 [...], random numbers of [0, 1), or
+    None (no tokens, the probabilities alone); temperature, top_p, min_p: fp32
+    [...], top_k: int32 [...], or None (1, off, off, off).  Kept are, in the
+    order of descending logits (equal ones by index), the first top_k tokens,
+    of those the smallest leading set that holds top_p of their probability,
+    and of those the ones at least min_p times as probable as the first;
+    temperature 0 keeps the first alone.  probs: a tensor like logits for the
+    probabilities that are left (what kda_tree_accept takes), True to make one,
+    or None.  Returns (token int32 [...]: the smallest kept index at which the
+    running sum of the kept probabilities passes u, -1 for a row without a
+    finite logit, or None without u; probs or None)."""
+    torch = _torch()
+    if not isinstance(logits, torch.Tensor) or logits.dim() < 1:
+        raise TypeError("logits must be a torch.Tensor [..., V]")
+    shape, dt, gpu, code = _first(logits, "logits", logits.dim())
+    rows = shape[:-1]
+    R, V = rows.numel(), shape[-1]
+    if u is None and token is not None:
+        raise ValueError("token is given with u")
+    f32, i32 = torch.float32, torch.int32
+    x = _one(logits, "logits", shape, dt, gpu)
+    ask = (_one(u, "u", rows, f32, gpu), _one(temperature, "temperature", rows, f32, gpu),
+           _one(top_k, "top_k", rows, i32, gpu), _one(top_p, "top_p", rows, f32, gpu),
+           _one(min_p, "min_p", rows, f32, gpu))
+    if token is None and u is not None:
+        token = torch.empty_like(u, dtype=i32)
+    if probs is True:
+        probs = torch.empty_like(logits)
+    if u is None and probs is None:
+        raise TypeError("u or probs is required")
+    size = lib().kda_sample_workspace_size(R, V)
+    # (of the allocator's, on the stream that the call is on: its own until it has run)
+    work = torch.empty(size, dtype=torch.uint8, device=logits.device)
+    _check(_on_device(gpu, lib().kda_sample, x, *ask, R, V, code, _one(token, "token", rows, i32, gpu),
+                      _one(probs, "probs", shape, dt, gpu), work.data_ptr(), size))
+    return token, probs
+
+
 __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_step",
            "kda_decode_multi", "kda_segment_summary", "kda_segment_scan", "kda_prologue",
            "kda_epilogue", "kda_chunk_bwd", "kda_chunk_bwd_workspace_size",
@@ -1011,4 +1064,5 @@ __all__ = ["kda_chunk_fwd", "kda_chunk_fwd_snap", "snapshot_index", "kda_decode_
            "kda_tree_prologue", "kda_tree_decode", "kda_tree_accept",
            "kda_tree_commit", "MAX_TREE", "MAX_VOCAB",
            "MAX_PATH", "kda_cache_store", "kda_cache_load", "kda_cache_decode",
-           "kda_cache_fold", "MAX_WINDOW", "lib", "LIB_PATH"]
+           "kda_cache_fold", "MAX_WINDOW", "kda_sample", "kda_sample_workspace_size",
+           "lib", "LIB_PATH"]

@@ -21,7 +21,8 @@ SOURCES = ["kda_api.cpp", "kda_chunk.hip", "kda_chunk_ws2.hip", "kda_chunk_ws2_s
            "kda_segment.hip", "kda_layer.hip", "kda_bwd.hip",
            "kda_bwd_ws.hip", "kda_noalloc.hip",
            "kda_tree_api.cpp", "kda_tree_decode.hip", "kda_tree_accept.hip", "kda_tree_commit.hip",
-           "kda_cache_api.cpp", "kda_cache.hip", "kda_cache_decode.hip"]
+           "kda_cache_api.cpp", "kda_cache.hip", "kda_cache_decode.hip",
+           "kda_sample_api.cpp", "kda_sample.hip"]
 ARCH = "gfx950"
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

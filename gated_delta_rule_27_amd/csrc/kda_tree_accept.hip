@@ -28,6 +28,7 @@
 // the device-wide fences of every arrival.
 #include "kda.h"
 #include "kda_device.h"
+#include "kda_scan.h"
 #include "kda_tree_device.h"
 
 namespace kda {
@@ -38,45 +39,6 @@ constexpr int kTile = 1024;          // tokens of a tile: 16 per lane of a wavef
 constexpr int kPer = kTile / 64;
 constexpr int kMaxTiles = KDA_MAX_VOCAB / kTile;
 constexpr int kAcceptWaves = 16;
-
-__device__ __forceinline__ double lane_value(double x, int lane) {
-    union { double d; int w[2]; } v;
-    v.d = x;
-    v.w[0] = __builtin_amdgcn_readlane(v.w[0], lane);
-    v.w[1] = __builtin_amdgcn_readlane(v.w[1], lane);
-    return v.d;
-}
-// x of the lane that the data-parallel move `kCtrl` names, 0 where it names
-// none or the lane's row of 16 is not in kRows
-template <int kCtrl, int kRows>
-__device__ __forceinline__ double moved(double x) {
-    union { double d; int w[2]; } v;
-    v.d = x;
-    v.w[0] = __builtin_amdgcn_update_dpp(0, v.w[0], kCtrl, kRows, 0xf, false);
-    v.w[1] = __builtin_amdgcn_update_dpp(0, v.w[1], kCtrl, kRows, 0xf, false);
-    return v.d;
-}
-// inclusive prefix sum over the lanes: along the rows of 16 (shifts by 1, 2,
-// 4, 8), then lane 15 of rows 0 and 2 to the row after, lane 31 to the upper half
-__device__ __forceinline__ double wave_scan(double x) {
-    x += moved<0x111, 0xf>(x);
-    x += moved<0x112, 0xf>(x);
-    x += moved<0x114, 0xf>(x);
-    x += moved<0x118, 0xf>(x);
-    x += moved<0x142, 0xa>(x);
-    x += moved<0x143, 0xc>(x);
-    return x;
-}
-__device__ __forceinline__ double wave_sum(double x) { return lane_value(wave_scan(x), 63); }
-
-// 16 bytes of probabilities from an address that only its elements align
-// (rows of an odd vocabulary)
-template <typename T>
-__device__ __forceinline__ typename Vec16<T>::type load16(const T* p) {
-    typename Vec16<T>::type x;
-    __builtin_memcpy(&x, p, 16);
-    return x;
-}
 
 // What is left at a node: max(p - c q, 0), or p without the refused tokens
 // (lanes of `gone`).

@@ -640,6 +640,50 @@ kda_status kda_cache_fold(int8_t* codes, float* scale, const void* win_k,
                           const int32_t* n_win, int32_t B, int32_t H, int32_t W,
                           int32_t Dk, int32_t Dv, kda_dtype dt, hipStream_t stream);
 
+/*
+ * Sampling: the next token of every row of logits, and the probabilities it is
+ * drawn with (what kda_tree_accept takes as the target's p and, from a draft
+ * model's logits, as q).  With T the row's temperature and M its largest
+ * logit, a token weighs w_i = e^((l_i - M) / T); -infinity and NaN weigh 0 and
+ * are never kept, and if M is infinite, what equals it weighs 1 and all else 0.
+ * In the order of descending logits, equal ones by ascending index, what is
+ * kept is the shortest of
+ *     top-k : the first k tokens                 (off: k < 1 or k >= V)
+ *     top-p : the smallest leading set whose weights sum to at least p times
+ *             those of the first k               (off: p >= 1 or NaN; one
+ *             token at least)
+ *     min-p : the tokens of w_i >= min(m, 1)     (off: m <= 0 or NaN)
+ * and T = 0 (or less, or NaN) keeps the first token alone.  The probabilities
+ * are the kept tokens' weights over their sum, 0 elsewhere, rounded to dt
+ * once.  The token drawn is the smallest kept i with
+ *     (sum of the kept w over 0..i)  >  u * (sum of the kept w),
+ * -1 where a row has no weight at all (its probabilities are then all 0).
+ * Weights are e^x in 64 bits and sums hold 40 bits or more below the largest
+ * weight, so a token is what 64-bit sums give unless a border lies within
+ * about 1e-11 of them.  Results do not depend on the launch.
+ *
+ *   logits, probs : [R, V] dt;  probs NULL = not wanted
+ *   u             : [R] fp32 in [0, 1) (clamped; NaN counts as 0); NULL = no
+ *                   token is wanted (token is then not looked at, probs is
+ *                   required)
+ *   temperature, top_p, min_p : [R] fp32;  top_k : [R] int32;  NULL = 1, off,
+ *                   off, off for every row
+ *   token         : [R] int32
+ *   workspace     : kda_sample_workspace_size(R, V) bytes, 16-byte aligned,
+ *                   for this call alone until it has run (calls that may run at
+ *                   the same time, captured ones among them, need their own)
+ * 1 <= V <= KDA_MAX_VOCAB, R < 2^22, R * ceil(V / 4096) < 2^24, else
+ * KDA_ERR_BAD_SHAPE; R == 0 is allowed (nothing is launched).  logits and
+ * probs 16-byte aligned (their rows need not be), the arrays 4-byte.  Any overlap of token, probs or
+ * workspace with another buffer is KDA_ERR_ALIAS.
+ */
+size_t kda_sample_workspace_size(int32_t R, int32_t V);
+
+kda_status kda_sample(const void* logits, const float* u, const float* temperature,
+                      const int32_t* top_k, const float* top_p, const float* min_p,
+                      int32_t R, int32_t V, kda_dtype dt, int32_t* token, void* probs,
+                      void* workspace, size_t workspace_bytes, hipStream_t stream);
+
 /* Static, human-readable name of a status code (never NULL). */
 const char* kda_status_str(kda_status s);
 
