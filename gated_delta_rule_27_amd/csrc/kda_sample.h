@@ -25,8 +25,10 @@ struct SampleArgs {
     char* workspace;
 };
 
-// Workspace: per tile its largest logit and the sum of its weights, then what
-// the last pass needs of each row.
+constexpr int kSampleGroups = 16;   // of a tile: 64 tokens each
+
+// Workspace: per tile its largest logit, the largest of each of its groups, and
+// the sum of its weights; then what the last pass needs of each row.
 struct SampleRow {
     double scale;      // log2(e) / temperature
     double per;        // 1 / (sum of the weights that are kept)
@@ -36,15 +38,20 @@ struct SampleRow {
     int32_t pad;
 };
 inline int64_t sample_tiles(int32_t V) { return ((int64_t)V + kSampleTile - 1) / kSampleTile; }
-inline size_t sample_tops_bytes(int32_t R, int32_t V) {
-    return (size_t)(((uint64_t)R * sample_tiles(V) * 4 + 15) / 16 * 16);
+struct SampleSections {
+    uint64_t tops, groups, sums, rows, end;   // bytes
+};
+__host__ __device__ inline SampleSections sample_sections(int32_t R, int64_t tiles) {
+    const uint64_t n = (uint64_t)R * tiles;
+    SampleSections s;
+    s.tops = 0;
+    s.groups = (n * 4 + 15) / 16 * 16;
+    s.sums = s.groups + n * 4 * kSampleGroups;
+    s.rows = s.sums + (n * 8 + 15) / 16 * 16;
+    s.end = s.rows + (uint64_t)R * sizeof(SampleRow);
+    return s;
 }
-inline size_t sample_sums_bytes(int32_t R, int32_t V) {
-    return (size_t)(((uint64_t)R * sample_tiles(V) * 8 + 15) / 16 * 16);
-}
-inline size_t sample_workspace(int32_t R, int32_t V) {
-    return sample_tops_bytes(R, V) + sample_sums_bytes(R, V) + (size_t)R * sizeof(SampleRow);
-}
+inline size_t sample_workspace(int32_t R, int32_t V) { return (size_t)sample_sections(R, sample_tiles(V)).end; }
 // workgroups of the passes over tiles: four tiles each
 inline int64_t sample_groups(int32_t R, int32_t V) { return (int64_t)R * ((sample_tiles(V) + 3) / 4); }
 

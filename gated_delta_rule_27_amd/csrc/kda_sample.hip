@@ -5,20 +5,24 @@
 // place in it is one 54-bit number, the logit's bits made monotone above the
 // index counted down, so that no two are equal and every filter keeps the
 // tokens from some place on.  Three passes, each a launch:
-//   tiles   the largest logit of every 1024-token tile and the sum of its
-//           weights e^((l - largest) / T), the row read once at full width
+//   tiles   the largest logit of every 1024-token tile, and of each of its 16
+//           groups, and the sum of its weights e^((l - largest) / T): the row
+//           read once at full width
 //   rows    one workgroup a row finds the last place that is kept and draws
 //   probs   the probabilities, tiles without a kept token unread
-// The second pass rarely reads the row again as a whole.  The k-th largest tile
-// maximum bounds the k-th largest logit from below, and the smallest tile
-// maximum lies low enough for most of a nucleus: what is at least that large (a
-// few tokens a tile) goes to a list in LDS, and places are found there by
-// histograms of 1024 bins, each level inside one bin of the last.  Where the
-// list overflows, or turns out not to hold the nucleus, the first levels read
-// the row's tiles instead.
-// Weights are taken in 64 bits, the histograms' as whole numbers of 2^-F, whose
-// sums are the same in any order: the drawn token is a whole number, too, which
-// a rounding of a running sum must not move.
+// The second pass rarely reads the row again as a whole.  A group's maximum says
+// whether anything of it can be large enough: the k-th largest of them bounds the
+// k-th largest logit from below, and some hundred of the largest groups hold most
+// nuclei.  Their tokens over such a bound go to a list in LDS, and everything is
+// decided there: a short one by counting, for each token, those before it; a
+// longer one by histograms of 1024 bins, each level inside one bin of the last.
+// Where the list overflows, or turns out not to hold the nucleus, the row's tiles
+// are read twice more: once to count their tokens in bins, from which follows
+// where the last kept one lies, within a few bins; once to collect those bins and
+// to sum each tile's weight above them, which shows that it does.
+// Weights are taken in 64 bits and added up as whole numbers of 2^-F: their sums
+// are the same in any order, and the drawn token is a whole number, too, which a
+// rounding of a running sum must not move.
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_sample.h"
@@ -33,6 +37,8 @@ constexpr int kPer = kTile / 64;
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = kThreads;
 constexpr uint32_t kCap = 2048;        // tokens of the list
+constexpr uint32_t kFew = 192;         // of them, that are counted pair by pair
+constexpr int kGroupTiles = 512;       // most tiles whose groups' maxima are kept (32 KB)
 constexpr int kIndexBits = 22;         // KDA_MAX_VOCAB
 constexpr uint64_t kIndexMask = (1u << kIndexBits) - 1;
 static_assert(KDA_MAX_VOCAB == 1 << kIndexBits, "an index fits its bits");
@@ -49,39 +55,45 @@ __device__ __forceinline__ uint32_t key_of(float x) {
 __device__ __forceinline__ float of_key(uint32_t k) {
     return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
+// the next smaller logit (of zero, whichever: the smallest negative number)
+__device__ __forceinline__ float under(float x) {
+    const uint32_t k = key_of(x);
+    return of_key(k - (k == 0x80000000u ? 2 : 1));
+}
 // a token's place; larger ones come first
 __device__ __forceinline__ uint64_t place(float x, int v) {
     return (uint64_t)key_of(x) << kIndexBits | (kIndexMask - (uint32_t)v);
 }
+__device__ __forceinline__ int index_of(uint64_t place) { return (int)(kIndexMask - (place & kIndexMask)); }
 __device__ __forceinline__ float logit_of(uint64_t place) { return of_key((uint32_t)(place >> kIndexBits)); }
 
 // ---- weights -----------------------------------------------------------------
 
-// 2^y for y <= 0, to an ulp or two (0 below 2^-1020), 1 at 0: 2^n e^r, |r| <= ln 2 / 2, the
-// series to r^12 (the next term: 2^-52)
+// 2^y for -1020 <= y <= 0, relative error 4e-14, 1 at 0: 2^n 2^f, |f| <= 1/2, and
+// 2^f = 1 + f q(f), q of degree 8 through (2^f - 1) / f at the Chebyshev points
 __device__ __forceinline__ double exp2_neg(double y) {
-    const double n = __builtin_rint(y);
-    const double r = (y - n) * 0.693147180559945309417;
-    double p = 1.0 / 479001600;
-    p = __builtin_fma(p, r, 1.0 / 39916800);
-    p = __builtin_fma(p, r, 1.0 / 3628800);
-    p = __builtin_fma(p, r, 1.0 / 362880);
-    p = __builtin_fma(p, r, 1.0 / 40320);
-    p = __builtin_fma(p, r, 1.0 / 5040);
-    p = __builtin_fma(p, r, 1.0 / 720);
-    p = __builtin_fma(p, r, 1.0 / 120);
-    p = __builtin_fma(p, r, 1.0 / 24);
-    p = __builtin_fma(p, r, 1.0 / 6);
-    p = __builtin_fma(p, r, 0.5);
-    p = __builtin_fma(p, r, 1.0);
-    p = __builtin_fma(p, r, 1.0);
-    if (!(y > -1020.0)) return 0.0;
-    const uint64_t b = __builtin_bit_cast(uint64_t, p) + ((uint64_t)(int64_t)(int32_t)n << 52);
-    return __builtin_bit_cast(double, b);
+    const double round = 6755399441055744.0;   // 1.5 * 2^52: a whole number in the low bits
+    const double t = y + round;
+    const double f = y - (t - round);
+    double q = 1.0203121071468306e-07;
+    q = __builtin_fma(q, f, 1.3255224879377917e-06);
+    q = __builtin_fma(q, f, 1.52526868462088e-05);
+    q = __builtin_fma(q, f, 0.000154034558524499);
+    q = __builtin_fma(q, f, 0.001333355817904325);
+    q = __builtin_fma(q, f, 0.009618129159402565);
+    q = __builtin_fma(q, f, 0.055504108664760424);
+    q = __builtin_fma(q, f, 0.2402265069581299);
+    q = __builtin_fma(q, f, 0.6931471805599453);
+    const uint64_t p = __builtin_bit_cast(uint64_t, __builtin_fma(q, f, 1.0));
+    const uint32_t n = (uint32_t)__builtin_bit_cast(uint64_t, t);
+    return __builtin_bit_cast(double, p + ((uint64_t)(n << 20) << 32));
 }
-// e^((x - top) / T), scale = log2(e) / T; top may be infinite (then what equals it weighs 1)
+// e^((x - top) / T), scale = log2(e) / T, 0 below 2^-1020; top may be infinite
+// (then what equals it weighs 1)
 __device__ __forceinline__ double weight(float x, float top, double scale) {
-    return x == top ? 1.0 : exp2_neg(((double)x - (double)top) * scale);
+    const double y = x == top ? 0.0 : ((double)x - (double)top) * scale;
+    const double w = exp2_neg(__builtin_fmax(y, -1020.0));
+    return y > -1020.0 ? w : 0.0;
 }
 
 // what a row is asked for
@@ -103,134 +115,157 @@ struct Ask {
     }
     // whether the sum of all weights takes part
     __device__ __forceinline__ bool sums() const { return !greedy && !by_k && (by_p || !by_m); }
+    // whether the maxima of the tiles' groups do
+    __device__ __forceinline__ bool groups(int tiles) const { return !greedy && (by_k || by_p || by_m) && tiles <= kGroupTiles; }
 };
 
 // ---- tiles -------------------------------------------------------------------
 
-// a tile's logits, the lane's (j, e) being token (j * 64 + lane) * M + e of it;
-// past the row's end, and for NaN, -infinity
+// a tile's logits, the lane's (j, e) being token (j * 64 + lane) * M + e of it
 template <typename T>
 struct Tile {
     static constexpr int M = Vec16<T>::N, J = kPer / M;
-    float x[J][M];
-    __device__ __forceinline__ void load(const T* row, int t, int V, int lane) {
-        typename Vec16<T>::type v[J];
+    typename Vec16<T>::type v[J];
+    __device__ __forceinline__ void load(const T* from, int t, int V, int lane) {
+        typedef const T __attribute__((address_space(1))) * global;   // (also where the compiler cannot see it)
+        const global row = (global)from;
         const int at = t * kTile + lane * M;
         if ((t + 1) * kTile <= V) {
 #pragma unroll
-            for (int j = 0; j < J; ++j) v[j] = load16(row + at + j * 64 * M);
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int e = 0; e < M; ++e) x[j][e] = __builtin_fmaxf(to_f32((T)v[j][e]), minus_inf());
+            for (int j = 0; j < J; ++j) __builtin_memcpy(&v[j], row + at + j * 64 * M, 16);
         } else {
 #pragma unroll
             for (int j = 0; j < J; ++j)
 #pragma unroll
-                for (int e = 0; e < M; ++e) v[j][e] = row[min(at + j * 64 * M + e, V - 1)];
-#pragma unroll
-            for (int j = 0; j < J; ++j)
-#pragma unroll
-                for (int e = 0; e < M; ++e)
-                    x[j][e] = at + j * 64 * M + e < V ? __builtin_fmaxf(to_f32((T)v[j][e]), minus_inf()) : minus_inf();
+                for (int e = 0; e < M; ++e) {
+                    const int i = at + j * 64 * M + e;
+                    const T x = row[min(i, V - 1)];
+                    v[j][e] = i < V ? x : (T)minus_inf();
+                }
         }
     }
-    // f(logit, token)
+    // f(logit, token); past the row's end -infinity
     template <typename F>
     __device__ __forceinline__ void each(int t, int lane, F&& f) const {
 #pragma unroll
         for (int j = 0; j < J; ++j)
 #pragma unroll
-            for (int e = 0; e < M; ++e) f(x[j][e], t * kTile + (j * 64 + lane) * M + e);
+            for (int e = 0; e < M; ++e) f(to_f32((T)v[j][e]), t * kTile + (j * 64 + lane) * M + e);
     }
 };
 
-__device__ __forceinline__ float wave_top(float x) {
+template <int kCtrl>
+__device__ __forceinline__ float top_with(float x) {
+    return __builtin_fmaxf(x, __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, x), kCtrl, 0xf, 0xf, true)));
+}
+// largest of each four lanes, of the wavefront
+__device__ __forceinline__ float quad_top(float x) { return top_with<0x4e>(top_with<0xb1>(x)); }
+__device__ __forceinline__ float wave_top_of_quads(float x) {
+    x = top_with<0x128>(top_with<0x124>(x));   // rotations of a row of 16 by 4 and 8
+    float m = minus_inf();
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) x = __builtin_fmaxf(x, __shfl_xor(x, off, 64));
-    return x;
+    for (int i = 0; i < 4; ++i)
+        m = __builtin_fmaxf(m, __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), 16 * i)));
+    return m;
 }
-
-struct Sections {
-    float* tops;        // [R, tiles]
-    double* sums;       // [R, tiles]
-    SampleRow* rows;    // [R]
-};
-__device__ __forceinline__ Sections sections(const SampleArgs& a, int64_t tiles) {
-    Sections s;
-    const uint64_t n = (uint64_t)a.R * tiles;
-    s.tops = reinterpret_cast<float*>(a.workspace);
-    s.sums = reinterpret_cast<double*>(a.workspace + (n * 4 + 15) / 16 * 16);
-    s.rows = reinterpret_cast<SampleRow*>(a.workspace + (n * 4 + 15) / 16 * 16 + (n * 8 + 15) / 16 * 16);
-    return s;
-}
+__device__ __forceinline__ float wave_top(float x) { return wave_top_of_quads(quad_top(x)); }
 
 template <typename T>
 __global__ __launch_bounds__(256) void sample_tiles_kernel(SampleArgs a) {
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = (a.V + kTile - 1) / kTile;
-    const uint32_t groups = (uint32_t)(tiles + 3) / 4;
-    const uint32_t row = blockIdx.x / groups;
-    const int t = (int)(blockIdx.x % groups) * 4 + wave;
+    const uint32_t per_row = (uint32_t)(tiles + 3) / 4;
+    const uint32_t row = blockIdx.x / per_row;
+    const int t = (int)(blockIdx.x % per_row) * 4 + wave;
     if (t >= tiles) return;
     Tile<T> x;
     x.load(static_cast<const T*>(a.logits) + (size_t)row * a.V, t, a.V, lane);
     const Ask ask(a, row);
+    const SampleSections at = sample_sections(a.R, tiles);
+    const size_t i = (size_t)row * tiles + t;
     float top = minus_inf();
     x.each(t, lane, [&](float l, int) { top = __builtin_fmaxf(top, l); });
-    top = wave_top(top);
-    const Sections s = sections(a, tiles);
-    const size_t at = (size_t)row * tiles + t;
-    if (lane == 0) s.tops[at] = top;
+    top = quad_top(top);
+    if (ask.groups(tiles) && (lane & 3) == 0)
+        reinterpret_cast<float*>(a.workspace + at.groups)[i * kSampleGroups + (lane >> 2)] = top;
+    top = wave_top_of_quads(top);
+    if (lane == 0) reinterpret_cast<float*>(a.workspace + at.tops)[i] = top;
     if (!ask.sums()) return;
     double sum = 0.0;
-    if (top > minus_inf()) x.each(t, lane, [&](float l, int) { sum += weight(l, top, ask.scale); });
+    if (top == __builtin_inff()) {
+        x.each(t, lane, [&](float l, int) { sum += l == top ? 1.0 : 0.0; });
+    } else if (top > minus_inf()) {
+        // (2^-1020 for what weighs less than that: nothing beside the tile's largest)
+        const double d = (double)top;
+        x.each(t, lane, [&](float l, int) { sum += exp2_neg(__builtin_fmax(((double)l - d) * ask.scale, -1020.0)); });
+    }
     sum = wave_sum(sum);
-    if (lane == 0) s.sums[at] = sum;
+    if (lane == 0) reinterpret_cast<double*>(a.workspace + at.sums)[i] = sum;
 }
 
 // ---- rows --------------------------------------------------------------------
 
+struct Entry {
+    uint64_t place, w;
+};
+// One workgroup a row.  Its state lies in LDS, where the functions below, which
+// are called and not inlined (their code is read once by every workgroup, from
+// far away: a short one is a fast one), find it.
 struct RowLds {
-    uint64_t list[kCap];      // places
-    uint64_t w[kCap];         // their weights
+    Entry list[kCap];
     uint64_t bin_w[kBins];
     uint32_t bin_n[kBins];
     uint64_t part_w[kWaves];
     uint32_t part_n[kWaves];
-    double part_d[kWaves];
-    float part_f[kWaves];
-    uint64_t few[64], few_w[64];
+    float part_f[2][kWaves];
+    Entry few[64];
+    float ring[kWaves][128];   // weights to be, on their way
     // what one thread tells the others
-    uint64_t total_w, before_w, key, key_w;
+    uint64_t total_w, before_w, key, key_w, kept_w, above_w;
     uint32_t total_n, before_n, here_n, n, key_n;
     int bin, token;
 };
+constexpr int kRowBytes = (sizeof(RowLds) + 15) / 16 * 16;
+extern __shared__ __align__(16) char row_memory[];
+#define KDA_ROW_LDS RowLds& l = *reinterpret_cast<RowLds*>(row_memory)
+
+__device__ __forceinline__ void add(uint64_t* to, uint64_t w) {
+    atomicAdd(reinterpret_cast<unsigned long long*>(to), (unsigned long long)w);
+}
+__device__ __forceinline__ void clear_bins(RowLds& l) {
+    l.bin_n[threadIdx.x] = 0;
+    l.bin_w[threadIdx.x] = 0;
+    __syncthreads();
+}
+__device__ __forceinline__ void count(RowLds& l, int bin, uint64_t w) {
+    atomicAdd(&l.bin_n[bin], 1u);
+    add(&l.bin_w[bin], w);
+}
 
 // Where sums over the bins, first to last, reach `target`: counts or weights.
 // All threads; the histogram is complete.  Returns the bin, -1 if none; the
-// sums before it, what it counts, and all sums are in `l`.
-__device__ int cross(RowLds& l, bool by_count, uint64_t target) {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// sums before it, what it counts, and all sums are in LDS.
+template <bool kWeights>   // false: counts alone, in bin_n
+__device__ __noinline__ int cross(bool by_count, uint64_t target) {
+    KDA_ROW_LDS;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n = l.bin_n[threadIdx.x];
-    const uint64_t w = l.bin_w[threadIdx.x];
+    const uint64_t w = kWeights ? l.bin_w[threadIdx.x] : 0;
     uint32_t sn = wave_scan_whole(n);
-    uint64_t sw = wave_scan_whole(w);
+    uint64_t sw = kWeights ? wave_scan_whole(w) : 0;
     if (lane == 63) {
         l.part_n[wave] = sn;
-        l.part_w[wave] = sw;
+        if (kWeights) l.part_w[wave] = sw;
     }
     if (threadIdx.x == 0) l.bin = -1;
     __syncthreads();
-    uint32_t bn = 0;
-    uint64_t bw = 0;
-    for (int i = 0; i < wave; ++i) {
-        bn += l.part_n[i];
-        bw += l.part_w[i];
+    const uint32_t pn = wave_scan_whole(lane < kWaves ? l.part_n[lane] : 0u);
+    const uint64_t pw = kWeights ? wave_scan_whole(lane < kWaves ? l.part_w[lane] : (uint64_t)0) : 0;
+    if (wave > 0) {
+        sn += lane_value(pn, wave - 1);
+        if (kWeights) sw += lane_value(pw, wave - 1);
     }
-    sn += bn;
-    sw += bw;
     const uint64_t now = by_count ? (uint64_t)sn : sw, own = by_count ? (uint64_t)n : w;
     if (now >= target && now - own < target) {
         l.bin = (int)threadIdx.x;
@@ -245,36 +280,31 @@ __device__ int cross(RowLds& l, bool by_count, uint64_t target) {
     __syncthreads();
     return l.bin;
 }
-__device__ __forceinline__ void clear_bins(RowLds& l) {
-    l.bin_n[threadIdx.x] = 0;
-    l.bin_w[threadIdx.x] = 0;
-    __syncthreads();
-}
-__device__ __forceinline__ void count(RowLds& l, int bin, uint64_t w) {
-    atomicAdd(&l.bin_n[bin], 1u);
-    atomicAdd(reinterpret_cast<unsigned long long*>(&l.bin_w[bin]), (unsigned long long)w);
-}
 
-// Of the n entries of the list, in descending order of key(i) (distinct; 0: not
-// one of them), keys at most `hi`: the first at which the number of them, or
-// their weights, reach `target` (not 0).  All threads.  False if none; else its
-// key in l.key, and what has been reached in l.key_n and l.key_w.
-template <typename K>
-__device__ bool find(RowLds& l, uint32_t n, K key, uint64_t lo, uint64_t hi, bool by_count, uint64_t target) {
+// Of n entries, in descending order of their keys (distinct), keys between lo and
+// hi: the first at which the number of them, or their weights, reach `target` (not
+// 0).  All threads.  False if none; else its key in l.key, and what has been
+// reached in l.key_n and l.key_w.
+enum Keys { kByPlace, kByIndex };   // the list's entries; those with weight, first index first
+__device__ __noinline__ bool find(Keys keys, uint32_t n, uint64_t lo, uint64_t hi, bool by_count, uint64_t target) {
+    KDA_ROW_LDS;
     uint32_t base_n = 0;
     uint64_t base_w = 0;
+    auto entry = [&](uint32_t i) {
+        const Entry x = l.list[i];
+        return keys == kByPlace ? x : Entry{x.w ? (x.place & kIndexMask) + 1 : 0, x.w};
+    };
     for (;;) {
         // (after the shift at most 1024 bins; the last level's hold one key each)
         const int bits = 64 - __builtin_clzll((hi - lo) | 1);
         const int shift = bits > 10 ? bits - 10 : 0;
         clear_bins(l);
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-            const uint64_t k = key(i);
-            if (k && k >= lo && k <= hi) count(l, (int)((hi - k) >> shift), l.w[i]);
+            const Entry x = entry(i);
+            if (x.place && x.place >= lo && x.place <= hi) count(l, (int)((hi - x.place) >> shift), x.w);
         }
         __syncthreads();
-        const uint64_t base = by_count ? base_n : base_w;
-        const int bin = cross(l, by_count, target - base);
+        const int bin = cross<true>(by_count, target - (by_count ? (uint64_t)base_n : base_w));
         if (bin < 0) return false;
         base_n += l.before_n;
         base_w += l.before_w;
@@ -286,29 +316,24 @@ __device__ bool find(RowLds& l, uint32_t n, K key, uint64_t lo, uint64_t hi, boo
         __syncthreads();
         if (here > 64) continue;
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-            const uint64_t k = key(i);
-            if (k && k >= lo && k <= hi) {
-                const uint32_t at = atomicAdd(&l.n, 1u);
-                l.few[at] = k;
-                l.few_w[at] = l.w[i];
-            }
+            const Entry x = entry(i);
+            if (x.place && x.place >= lo && x.place <= hi) l.few[atomicAdd(&l.n, 1u)] = x;
         }
         __syncthreads();
         if (threadIdx.x < 64) {
-            const int lane = threadIdx.x;
-            const uint64_t k = lane < (int)here ? l.few[lane] : 0, w = lane < (int)here ? l.few_w[lane] : 0;
+            const Entry mine = threadIdx.x < here ? l.few[threadIdx.x] : Entry{0, 0};
             uint64_t sw = base_w;
             uint32_t sn = base_n;
             for (uint32_t j = 0; j < here; ++j) {
-                const uint64_t kj = lane_value(k, j), wj = lane_value(w, j);
-                if (kj >= k) {
-                    sw += wj;
+                const Entry x = l.few[j];
+                if (x.place >= mine.place) {
+                    sw += x.w;
                     ++sn;
                 }
             }
-            const uint64_t now = by_count ? (uint64_t)sn : sw, before = by_count ? now - 1 : now - w;
-            if (k && now >= target && before < target) {
-                l.key = k;
+            const uint64_t now = by_count ? (uint64_t)sn : sw, before = by_count ? now - 1 : now - mine.w;
+            if (mine.place && now >= target && before < target) {
+                l.key = mine.place;
                 l.key_n = sn;
                 l.key_w = sw;
             }
@@ -318,92 +343,373 @@ __device__ bool find(RowLds& l, uint32_t n, K key, uint64_t lo, uint64_t hi, boo
     }
 }
 
-// one workgroup a row
-template <typename T>
-struct Row {
-    RowLds& l;
-    float* tops;         // LDS: [tiles]
-    double* sums;        // LDS: [tiles]
-    const T* logits;
-    int V, tiles;
-    int lane, wave;
-    float top;
-    double scale, unit;  // unit: 2^F
-
-    __device__ __forceinline__ uint64_t whole(double w) const { return (uint64_t)(w * unit + 0.5); }
-    __device__ __forceinline__ double weight_of(float x) const { return weight(x, top, scale); }
-    template <typename F>
-    __device__ __forceinline__ void tiles_from(float least, F&& f) const {
-        for (int t = wave; t < tiles; t += kWaves) {
-            const float m = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, tops[t])));
-            if (!(m >= least) || m == minus_inf()) continue;
-            Tile<T> x;
-            x.load(logits, t, V, lane);
-            f(x, t);
+// For each of n <= kFew entries, over the entries at or before it (by place, or by
+// index): their number in l.bin_n and weights in l.bin_w.  All threads.
+__device__ __noinline__ void count_pairs(uint32_t n, bool by_index) {
+    KDA_ROW_LDS;
+    clear_bins(l);
+    const uint64_t mask = by_index ? kIndexMask : ~(uint64_t)0;
+    const int shared = n <= 64 ? 6 : 32 - __builtin_clz(n - 1);   // 2^shared threads take an entry each
+    const uint32_t e = threadIdx.x & ((1u << shared) - 1), part = threadIdx.x >> shared, parts = kThreads >> shared;
+    const uint32_t per = (n + parts - 1) / parts, j0 = part * per, j1 = min(n, j0 + per);
+    if (e < n && j0 < j1) {
+        const uint64_t mine = l.list[e].place & mask;
+        uint32_t sn = 0;
+        uint64_t sw = 0;
+#pragma unroll 4
+        for (uint32_t j = j0; j < j1; ++j) {
+            const Entry x = l.list[j];
+            const bool yes = (x.place & mask) >= mine;
+            sn += yes;
+            sw += yes ? x.w : 0;
         }
+        atomicAdd(&l.bin_n[e], sn);
+        add(&l.bin_w[e], sw);
     }
-    // tokens of logit >= least that `keep` names, and their weights, to the list;
-    // how many there are (more than kCap: those past it are left out)
-    template <typename F>
-    __device__ uint32_t gather(float least, F&& keep) {
+    __syncthreads();
+}
+
+// Bins of equal width in the logit, from 2^high of the largest weight down to 2^low
+// (any function that never rises with the logit will do).
+struct Bins {
+    float top, slope, start;
+    __device__ __forceinline__ Bins(float top, double scale, double high, double low) : top(top) {
+        const double steps = (kBins - 1) / (high - low);
+        slope = (float)__builtin_fmin(__builtin_fmax(steps * scale, 1e-30), 1e30);
+        start = (float)(high * steps);
+    }
+    __device__ __forceinline__ int operator()(float x) const {
+        const float d = x == top ? 0.f : x - top;
+        return (int)__builtin_fminf(__builtin_fmaxf(__builtin_fmaf(-d, slope, start), 0.f), kBins - 1.f);
+    }
+    // about the logit at which bin b begins
+    __device__ __forceinline__ float edge(float b) const { return top - (b - start) / slope; }
+};
+
+// The nth largest of `count` maxima, of which the largest is `top` and nth ones or
+// more, as a rule, are not below `low`.  All threads; -infinity if there are not as many.
+__device__ __noinline__ float nth_maximum(const __attribute__((address_space(3))) float* maxima, uint32_t count, uint32_t nth,
+                                          float top, float low) {
+    KDA_ROW_LDS;
+    const Bins bin_of(top, 1.0, 0.0, low < top ? (double)low - (double)top : -1.0);
+    uint64_t lo = 1, hi = ~(uint64_t)0 >> (32 - kIndexBits);
+    uint32_t before = 0, here = 65;
+    int bin = -1;
+    while (here > 64) {   // (once, but for many equal maxima, or far ones)
+        l.bin_n[threadIdx.x] = 0;
+        __syncthreads();
+        const int bits = 64 - __builtin_clzll((hi - lo) | 1), shift = bits > 10 ? bits - 10 : 0;
+        for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+            const float m = maxima[i];
+            if (!(m > minus_inf())) continue;
+            const uint64_t k = place(m, i);
+            if (bin < 0) atomicAdd(&l.bin_n[bin_of(m)], 1u);
+            else if (bin_of(m) == bin && k >= lo && k <= hi) atomicAdd(&l.bin_n[(hi - k) >> shift], 1u);
+        }
+        __syncthreads();
+        const int b = cross<false>(true, nth - before);
+        if (b < 0) return minus_inf();
+        before += l.before_n;
+        here = l.here_n;
+        if (bin < 0) {
+            bin = b;
+        } else {
+            hi -= (uint64_t)b << shift;
+            const uint64_t width = ((uint64_t)1 << shift) - 1;
+            lo = hi - lo > width ? hi - width : lo;
+        }
         if (threadIdx.x == 0) l.n = 0;
         __syncthreads();
-        tiles_from(least, [&](const Tile<T>& x, int t) {
-            uint32_t mine = 0;
-            x.each(t, lane, [&](float v, int i) { mine += v >= least && v > minus_inf() && keep(v, i); });
-            const uint32_t incl = wave_scan_whole(mine), all = lane_value(incl, 63);
-            if (all == 0) return;
-            uint32_t at = 0;
-            if (lane == 0) at = atomicAdd(&l.n, all);
-            at = lane_value(at, 0) + incl - mine;
-            if (mine)
-                x.each(t, lane, [&](float v, int i) {
-                    if (v >= least && v > minus_inf() && keep(v, i)) {
-                        if (at < kCap) l.list[at] = place(v, i);
-                        ++at;
-                    }
-                });
+    }
+    for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+        const float m = maxima[i];
+        const uint64_t k = place(m, i);
+        if (m > minus_inf() && bin_of(m) == bin && k >= lo && k <= hi) l.few[atomicAdd(&l.n, 1u)].place = k;
+    }
+    __syncthreads();
+    if (threadIdx.x < here) {
+        const uint64_t mine = l.few[threadIdx.x].place;
+        uint32_t n = before;
+        for (uint32_t j = 0; j < here; ++j) n += l.few[j].place >= mine;
+        if (n == nth) l.key = mine;
+    }
+    __syncthreads();
+    return logit_of(l.key);
+}
+
+template <typename T>
+struct Row {
+    const T* logits;
+    int V, tiles;
+    float top;
+    double scale;
+    double unit;         // 2^F, F <= 50: what sums are counted in is 2^-F
+    int lane, wave;
+
+    __device__ __forceinline__ uint64_t* sums() const {    // [tiles], weights of what is kept
+        return reinterpret_cast<uint64_t*>(row_memory + kRowBytes);
+    }
+    __device__ __forceinline__ float* tops() const { return reinterpret_cast<float*>(sums() + tiles); }   // [tiles]
+    __device__ __forceinline__ float* groups() const { return tops() + tiles; }   // [tiles * 16], if they are kept
+    __device__ __forceinline__ float logit(int i) const {
+        return to_f32(((const T __attribute__((address_space(1)))*)logits)[i]);
+    }
+    // w <= 1 as a whole number: beside 2^(52 - F) its last bit is 2^-F
+    __device__ __forceinline__ uint64_t whole(double w) const {
+        const double c = 4503599627370496.0 / unit;
+        return __builtin_bit_cast(uint64_t, w + c) - __builtin_bit_cast(uint64_t, c);
+    }
+    __device__ __forceinline__ double weight_of(float x) const { return weight(x, top, scale); }
+    // f(tile, its number) for the tiles with a logit > below, the next one's loads in flight
+    template <typename F>
+    __device__ __forceinline__ void tiles_over(float below, F&& f) const {
+        auto next = [&](int t) {
+            for (; t < tiles; t += kWaves) {
+                const float m = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, tops()[t])));
+                if (m > below) break;
+            }
+            return t;
+        };
+        int t = next(wave);
+        if (t >= tiles) return;
+        Tile<T> x;
+        x.load(logits, t, V, lane);
+        for (;;) {
+            const int then = next(t + kWaves);
+            Tile<T> y;
+            if (then < tiles) y.load(logits, then, V, lane);
+            f(x, t);
+            if (then >= tiles) return;
+            x = y;
+            t = then;
+        }
+    }
+    // lanes of `those` before this one
+    static __device__ __forceinline__ uint32_t rank_in(uint64_t those) {
+        return __builtin_amdgcn_mbcnt_hi((uint32_t)(those >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)those, 0));
+    }
+    // the tokens of a tile that `keep` names to the list (past kCap they are only counted)
+    template <typename F>
+    __device__ __forceinline__ void append(const Tile<T>& x, int t, F&& keep) const {
+        KDA_ROW_LDS;
+        uint32_t named = 0;   // of all lanes
+        x.each(t, lane, [&](float v, int) { named += (uint32_t)__builtin_popcountll(__ballot(keep(v))); });
+        if (named == 0) return;
+        uint32_t at = 0;
+        if (lane == 0) at = atomicAdd(&l.n, named);
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        x.each(t, lane, [&](float v, int i) {
+            const uint64_t those = __ballot(keep(v));
+            if (those == 0) return;
+            if (those >> lane & 1) {
+                const uint32_t mine = at + rank_in(those);
+                if (mine < kCap) l.list[mine].w = (uint64_t)i;   // (its place follows)
+            }
+            at += (uint32_t)__builtin_popcountll(those);
         });
+    }
+    __device__ __forceinline__ void start_list() const {
+        KDA_ROW_LDS;
+        __syncthreads();
+        if (threadIdx.x == 0) l.n = 0;
+        __syncthreads();
+    }
+    // after that, the list's places and weights; how many were named
+    __device__ __forceinline__ uint32_t listed() const {
+        KDA_ROW_LDS;
         __syncthreads();
         const uint32_t n = l.n;
-        for (uint32_t i = threadIdx.x; i < min(n, kCap); i += kThreads) l.w[i] = whole(weight_of(logit_of(l.list[i])));
+        for (uint32_t i = threadIdx.x; i < min(n, kCap); i += kThreads) {
+            const int v = (int)l.list[i].w;
+            const float x = logit(v);
+            l.list[i] = Entry{place(x, v), whole(weight_of(x))};
+        }
         __syncthreads();
         return n;
     }
-    // linear bins of 46 T below the largest logit (less than e^-46 of its weight: in the last)
-    __device__ __forceinline__ int bin_of(float x) const {
-        if (x == top) return 0;
-        return (int)__builtin_fmin(((double)top - (double)x) * scale * (kBins / 66.4), kBins - 1.0);
+    // every token of logit > below to the list
+    __device__ __noinline__ uint32_t gather(float below, bool by_group) const {
+        KDA_ROW_LDS;
+        constexpr int M = Tile<T>::M;
+        start_list();
+        if (!by_group) {
+            tiles_over(below, [&](const Tile<T>& x, int t) { append(x, t, [&](float v) { return v > below; }); });
+            return listed();
+        }
+        // a group's 64 tokens, one a lane, four groups in flight
+        const int count = tiles * kSampleGroups, mine = lane / (4 * M) * 64 * M + lane % (4 * M);
+        for (int g0 = wave * 64; g0 < count; g0 += kThreads) {
+            uint64_t todo = __ballot(g0 + lane < count && groups()[min(g0 + lane, count - 1)] > below);
+            while (todo) {
+                float x[4];
+                int i[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int g = g0 + (todo ? __builtin_ctzll(todo) : 0);
+                    i[q] = todo ? g / kSampleGroups * kTile + g % kSampleGroups * 4 * M + mine : V;
+                    todo &= todo - (todo != 0);
+                    x[q] = logit(min(i[q], V - 1));
+                }
+                uint64_t those[4];
+                uint32_t named = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    those[q] = __ballot(i[q] < V && x[q] > below);
+                    named += (uint32_t)__builtin_popcountll(those[q]);
+                }
+                uint32_t at = 0;
+                if (lane == 0) at = atomicAdd(&l.n, named);
+                at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint32_t to = at + rank_in(those[q]);
+                    if ((those[q] >> lane & 1) && to < kCap) l.list[to].w = (uint64_t)i[q];
+                    at += (uint32_t)__builtin_popcountll(those[q]);
+                }
+            }
+        }
+        return listed();
     }
-    // the same as find(), over the row
-    __device__ bool find_row(bool by_count, uint64_t target) {
+
+    // Sums over a tile of the weights of the tokens that `keep` names, through a ring
+    // that packs them: `all`, and `kept`, of those that weigh `least`; in lane 63.
+    template <typename F>
+    __device__ __forceinline__ void weigh(const Tile<T>& x, int t, double least, F&& keep, uint64_t& all, uint64_t& kept,
+                                          uint32_t& passed) const {
+        KDA_ROW_LDS;
+        float* ring = l.ring[wave];
+        uint32_t head = 0, held = 0;   // of all lanes, as is their number, added to `passed`
+        all = kept = 0;
+        auto flush = [&](uint32_t n) {
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            const double w = (uint32_t)lane < n ? weight_of(ring[(head + lane) & 127]) : 0.0;
+            const uint64_t i = whole(w);
+            all += i;
+            kept += w >= least ? i : 0;
+            __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
+            head += 64;
+        };
+        x.each(t, lane, [&](float v, int) {
+            const uint64_t those = __ballot(keep(v));
+            if (those == 0) return;
+            if (those >> lane & 1)
+                ring[(head + held + rank_in(those)) & 127] = v;
+            held += (uint32_t)__builtin_popcountll(those);
+            if (held >= 64) {
+                flush(64);
+                passed += 64;
+                held -= 64;
+            }
+        });
+        if (held) flush(held);
+        passed += held;
+        all = wave_scan_whole(all);
+        kept = wave_scan_whole(kept);
+    }
+
+    // The same as find(), over the row's tokens: `below` < logit < `above`, which
+    // weigh 2^high at most and, where weights are to reach `target`, 2^low at least
+    // (what weighs less cannot be where they do).  `off` is what those from `above` on
+    // weigh.  If it can be found within a few bins, sums then holds each tile's weight
+    // of what is kept if it ends there and weighs `least`, and l.key_w the weights up
+    // to there.  False if not: it may be there all the same.
+    __device__ __noinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+                                           double low, double least) const {
+        KDA_ROW_LDS;
+        const Bins bin_of(top, scale, high, low);
+        const int exact = !by_count && off == 0 ? kBins / 16 : 0;
         clear_bins(l);
-        tiles_from(minus_inf(), [&](const Tile<T>& x, int t) {
+        uint32_t rest = 0;
+        tiles_over(below, [&](const Tile<T>& x, int t) {
             x.each(t, lane, [&](float v, int) {
-                if (v > minus_inf()) count(l, bin_of(v), whole(weight_of(v)));
+                if (v > below && v < above) {
+                    const int b = bin_of(v);
+                    if (b < kBins - 1) atomicAdd(&l.bin_n[b], 1u);
+                    else ++rest;
+                    if (b < exact) add(&l.bin_w[b], whole(weight_of(v)));
+                }
             });
         });
+        if (rest) atomicAdd(&l.bin_n[kBins - 1], rest);
         __syncthreads();
-        const int bin = cross(l, by_count, target);
+        // (what a bin weighs: about its middle, but for the first ones, whose few tokens may be most of it)
+        if (!by_count && (int)threadIdx.x >= exact) {
+            const double y = high - (threadIdx.x + 0.5) * (high - low) / (kBins - 1);
+            l.bin_w[threadIdx.x] = (uint64_t)(l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0)));
+        }
+        const int bin = cross<true>(by_count, target - off);
         if (bin < 0) return false;
-        uint32_t base_n = l.before_n, here = l.here_n;
-        uint64_t base_w = l.before_w, lo = 1, hi = ~(uint64_t)0 >> (32 - kIndexBits);
+        // that bin and as many beside it as fit the list, up to eight: edges and estimated weights are not exact
+        int j0 = bin, j1 = bin;
+        uint32_t here = l.here_n;
+        for (int r = 0; r < 8; ++r) {
+            const uint32_t more = (j0 > 0 ? l.bin_n[j0 - 1] : 0) + (j1 < kBins - 1 ? l.bin_n[j1 + 1] : 0);
+            if (here + more > kCap - 64) break;
+            here += more;
+            if (j0 > 0) --j0;
+            if (j1 < kBins - 1) ++j1;
+        }
+        if (here > kCap) return false;
+        const float over = j0 > 0 ? bin_of.edge((float)j0) : __builtin_inff(), from = j1 < kBins - 1 ? __builtin_fmaxf(bin_of.edge(j1 + 1.f), below) : below;
+        if (!(from < over)) return false;
+        if (threadIdx.x == 0) {
+            l.above_w = 0;
+            l.before_n = 0;
+        }
+        for (int t = threadIdx.x; t < tiles; t += kThreads) sums()[t] = 0;
+        start_list();
+        uint64_t all = 0;
+        uint32_t passed = 0;   // of all lanes
+        // (what is from `above` on is over, wherever bin 0 begins)
+        const float border = __builtin_fminf(over, under(above));
+        tiles_over(from, [&](const Tile<T>& x, int t) {
+            uint64_t w, kept;
+            append(x, t, [&](float v) { return v > from && !(v > border); });
+            weigh(x, t, least, [&](float v) { return v > border; }, w, kept, passed);
+            all += w;
+            if (lane == 63) sums()[t] = kept;
+        });
+        if (lane == 63) {
+            add(&l.above_w, all);
+            atomicAdd(&l.before_n, passed);
+        }
+        const uint32_t n = listed();
+        const uint64_t base = by_count ? (uint64_t)l.before_n : l.above_w;
+        const uint64_t first = border < top ? place(border, 0) : place(top, 0), last = from > minus_inf() ? place(from, 0) : 1;
+        __syncthreads();
+        if (n > kCap || base >= target || !find(kByPlace, n, last, first, by_count, target - base)) return false;
+        const uint64_t cut = l.key;
+        __syncthreads();
+        if (threadIdx.x == 0) l.key_w += l.above_w;
+        for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+            const Entry x = l.list[i];
+            if (x.place >= cut && weight_of(logit_of(x.place)) >= least) add(&sums()[index_of(x.place) / kTile], x.w);
+        }
+        __syncthreads();
+        return true;
+    }
+    // The same wherever it lies, without the sums: a histogram of the weights
+    // themselves, and as many levels inside one bin as it takes (thousands of equal
+    // logits, a distribution that fits no bins).
+    __device__ __noinline__ bool find_far(bool by_count, uint64_t target) const {
+        KDA_ROW_LDS;
+        uint32_t base_n = 0, here = kCap + 1;
+        uint64_t base_w = 0, lo = 1, hi = place(top, 0);
         while (here > kCap) {
-            // (many equal logits: by their places)
             const int bits = 64 - __builtin_clzll((hi - lo) | 1);
             const int shift = bits > 10 ? bits - 10 : 0;
             __syncthreads();
             clear_bins(l);
-            tiles_from(minus_inf(), [&](const Tile<T>& x, int t) {
+            tiles_over(minus_inf(), [&](const Tile<T>& x, int t) {
                 x.each(t, lane, [&](float v, int i) {
-                    if (v > minus_inf() && bin_of(v) == bin) {
+                    if (v > minus_inf()) {
                         const uint64_t k = place(v, i);
                         if (k >= lo && k <= hi) count(l, (int)((hi - k) >> shift), whole(weight_of(v)));
                     }
                 });
             });
             __syncthreads();
-            const int b = cross(l, by_count, target - (by_count ? (uint64_t)base_n : base_w));
+            const int b = cross<true>(by_count, target - (by_count ? (uint64_t)base_n : base_w));
             if (b < 0) return false;
             base_n += l.before_n;
             base_w += l.before_w;
@@ -412,36 +718,60 @@ struct Row {
             const uint64_t width = ((uint64_t)1 << shift) - 1;
             lo = hi - lo > width ? hi - width : lo;
         }
-        __syncthreads();
-        const uint32_t n = gather(minus_inf(), [&](float v, int i) {
-            const uint64_t k = place(v, i);
-            return bin_of(v) == bin && k >= lo && k <= hi;
+        start_list();
+        tiles_over(minus_inf(), [&](const Tile<T>& x, int t) {
+            x.each(t, lane, [&](float v, int i) {
+                if (v > minus_inf()) {
+                    const uint64_t k = place(v, i);
+                    if (k >= lo && k <= hi) {
+                        const uint32_t at = atomicAdd(&l.n, 1u);
+                        if (at < kCap) l.list[at].w = (uint64_t)i;
+                    }
+                }
+            });
         });
-        const bool ok = find(l, n, [&](uint32_t i) { return l.list[i]; }, lo, hi, by_count,
-                             target - (by_count ? (uint64_t)base_n : base_w));
-        if (ok && threadIdx.x == 0) {
-            l.key_n += base_n;
-            l.key_w += base_w;
-        }
+        const uint32_t n = min(listed(), kCap);
+        if (!find(kByPlace, n, lo, hi, by_count, target - (by_count ? (uint64_t)base_n : base_w))) return false;
+        if (threadIdx.x == 0) l.key_w += base_w;
         __syncthreads();
-        return ok;
+        return true;
     }
-    // sum of the tiles' sums; the same in every thread
-    __device__ double total() {
-        double s = 0.0;
-        for (int t0 = 0; t0 < tiles; t0 += 64) s += wave_sum(t0 + lane < tiles ? sums[t0 + lane] : 0.0);
-        return s;
+    // each tile's weight of what is kept
+    __device__ __noinline__ void sum_kept(uint64_t cut, double least) const {
+        for (int t = threadIdx.x; t < tiles; t += kThreads) sums()[t] = 0;
+        __syncthreads();
+        const float from = cut > 1 ? logit_of(cut) : minus_inf(), below = cut > 1 ? under(from) : from;
+        const int border = index_of(cut);
+        tiles_over(below, [&](const Tile<T>& x, int t) {
+            uint64_t all, kept;
+            uint32_t passed = 0;
+            Tile<T> y = x;   // (of logits equal to the cut's, those up to its index)
+            if (cut > 1)
+#pragma unroll
+                for (int j = 0; j < Tile<T>::J; ++j)
+#pragma unroll
+                    for (int e = 0; e < Tile<T>::M; ++e)
+                        if (to_f32((T)y.v[j][e]) == from && t * kTile + (j * 64 + lane) * Tile<T>::M + e > border) y.v[j][e] = (T)minus_inf();
+            weigh(y, t, least, [&](float v) { return v > below; }, all, kept, passed);
+            if (lane == 63) sums()[t] = kept;
+        });
+        __syncthreads();
     }
-    // the first token at which the running sum of weights passes `target`, from
-    // the tiles' sums (in the first wavefront)
-    __device__ int draw(double target, uint64_t cut, double least) {
-        int tile = -1, filled = -1;
-        double base = 0.0, run = 0.0;
+    // Sum of the tiles' sums; the same in every thread.
+    __device__ __forceinline__ uint64_t total() const {
+        uint64_t s = 0;
+        for (int t0 = 0; t0 < tiles; t0 += 64) s += wave_scan_whole(t0 + lane < tiles ? sums()[t0 + lane] : (uint64_t)0);
+        return lane_value(s, 63);
+    }
+    // The first token at which the running sum of the kept weights reaches `target`,
+    // from the tiles' sums.  All threads; the result is l.token's afterwards.
+    __device__ __forceinline__ void draw(uint64_t target, uint64_t cut, double least) const {
+        KDA_ROW_LDS;
+        int tile = -1;
+        uint64_t base = 0, run = 0;
         for (int t0 = 0; t0 < tiles && tile < 0; t0 += 64) {
-            const double s = t0 + lane < tiles ? sums[t0 + lane] : 0.0;
-            const double incl = run + wave_scan(s);
-            const uint64_t hit = __ballot(s > 0.0 && incl > target), any = __ballot(s > 0.0);
-            if (any) filled = t0 + 63 - __builtin_clzll(any);
+            const uint64_t incl = run + wave_scan_whole(t0 + lane < tiles ? sums()[t0 + lane] : (uint64_t)0);
+            const uint64_t hit = __ballot(incl >= target);
             if (hit) {
                 const int i = __builtin_ctzll(hit);
                 tile = t0 + i;
@@ -449,48 +779,43 @@ struct Row {
             }
             run = lane_value(incl, 63);
         }
-        if (tile < 0) {   // (the target rounded past the end: the last token with weight)
-            tile = max(filled, 0);
-            base = -1e300;
-        }
-        const int v0 = tile * kTile + lane * kPer;   // a lane's tokens are consecutive
-        double w[kPer], s = 0.0;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            const float x = v0 + e < V ? __builtin_fmaxf(to_f32(logits[min(v0 + e, V - 1)]), minus_inf()) : minus_inf();
-            w[e] = x > minus_inf() && place(x, min(v0 + e, V - 1)) >= cut ? weight_of(x) : 0.0;
-            if (w[e] < least) w[e] = 0.0;
-            s += w[e];
-        }
-        const double incl = base + wave_scan(s);
-        double sum = __shfl_up(incl, 1, 64);
-        if (lane == 0) sum = base;
-        int first = -1, last = -1;
-#pragma unroll
-        for (int e = 0; e < kPer; ++e) {
-            sum += w[e];
-            if (w[e] > 0.0) {
-                last = v0 + e;
-                if (first < 0 && sum > target) first = v0 + e;
+        tile = max(tile, 0);
+        const int i = tile * kTile + (int)threadIdx.x;
+        uint64_t w = 0;
+        if (i < V) {
+            const float x = logit(i);
+            if (x > minus_inf() && place(x, i) >= cut) {
+                const double y = weight_of(x);
+                w = y >= least ? whole(y) : 0;
             }
         }
-        const uint64_t hit = __ballot(first >= 0), any = __ballot(last >= 0);
-        if (hit) return __builtin_amdgcn_readlane(first, __builtin_ctzll(hit));
-        if (any) return __builtin_amdgcn_readlane(last, 63 - __builtin_clzll(any));
-        return min(tile * kTile, V - 1);
+        uint64_t sum = wave_scan_whole(w);
+        if (lane == 63) l.part_w[wave] = sum;
+        if (threadIdx.x == 0) {
+            l.token = V;
+            l.n = 0;
+        }
+        __syncthreads();
+        const uint64_t parts = wave_scan_whole(lane < kWaves ? l.part_w[lane] : (uint64_t)0);
+        sum += base + (wave > 0 ? lane_value(parts, wave - 1) : 0);
+        const uint64_t hit = __ballot(w != 0 && sum >= target), any = __ballot(w != 0);
+        if (hit && lane == 0) atomicMin(&l.token, i + __builtin_ctzll(hit));
+        if (any && lane == 0) atomicMax(&l.n, (uint32_t)(i + 63 - __builtin_clzll(any)));
+        __syncthreads();
+        // (a tile's sum is rounded once, its tokens' one by one: then it is the last)
+        if (threadIdx.x == 0 && l.token == V) l.token = (int)l.n;
+        __syncthreads();
     }
 };
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
-    extern __shared__ __align__(16) char dynamic[];
-    RowLds& l = *reinterpret_cast<RowLds*>(dynamic);
+    KDA_ROW_LDS;
     const int64_t row = blockIdx.x;
     const int V = a.V, tiles = (V + kTile - 1) / kTile;
-    const Sections sec = sections(a, tiles);
-    Row<T> r{l};
-    r.sums = reinterpret_cast<double*>(dynamic + (sizeof(RowLds) + 15) / 16 * 16);
-    r.tops = reinterpret_cast<float*>(r.sums + tiles);
+    const SampleSections at = sample_sections(a.R, tiles);
+    SampleRow* to = reinterpret_cast<SampleRow*>(a.workspace + at.rows) + row;
+    Row<T> r;
     r.logits = static_cast<const T*>(a.logits) + (size_t)row * V;
     r.V = V;
     r.tiles = tiles;
@@ -503,27 +828,29 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     float top = minus_inf(), low = __builtin_inff();   // largest; smallest of full tiles that are not empty
     const int full = V / kTile;
     for (int t = threadIdx.x; t < tiles; t += kThreads) {
-        const float m = sec.tops[row * tiles + t];
-        r.tops[t] = m;
+        const float m = reinterpret_cast<const float*>(a.workspace + at.tops)[row * tiles + t];
+        r.tops()[t] = m;
         top = __builtin_fmaxf(top, m);
         if (t < full && m > minus_inf()) low = __builtin_fminf(low, m);
+    }
+    if (ask.groups(tiles)) {
+        const float* from = reinterpret_cast<const float*>(a.workspace + at.groups) + row * tiles * kSampleGroups;
+        for (int i = threadIdx.x; i < tiles * kSampleGroups; i += kThreads) r.groups()[i] = from[i];
     }
     top = wave_top(top);
     low = -wave_top(-low);
     if (r.lane == 0) {
-        l.part_f[r.wave] = top;
-        l.part_d[r.wave] = (double)low;
+        l.part_f[0][r.wave] = top;
+        l.part_f[1][r.wave] = low;
     }
     if (threadIdx.x == 0) l.token = V;
     __syncthreads();
-    for (int i = 0; i < kWaves; ++i) {
-        top = __builtin_fmaxf(top, l.part_f[i]);
-        low = __builtin_fminf(low, (float)l.part_d[i]);
-    }
+    top = wave_top(r.lane < kWaves ? l.part_f[0][r.lane] : minus_inf());
+    low = -wave_top(r.lane < kWaves ? -l.part_f[1][r.lane] : minus_inf());
     r.top = top;
     r.scale = ask.scale;
     const int bits = 32 - __builtin_clz((uint32_t)V);   // V < 2^bits
-    r.unit = __builtin_ldexp(1.0, 62 - bits);
+    r.unit = __builtin_ldexp(1.0, min(62 - bits, 50));
 
     SampleRow out;
     out.scale = ask.scale;
@@ -535,12 +862,12 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     if (top == minus_inf()) {   // nothing to draw from
         if (threadIdx.x == 0) {
             if (a.u) a.token[row] = -1;
-            sec.rows[row] = out;
+            *to = out;
         }
         return;
     }
     if (ask.greedy) {
-        r.tiles_from(top, [&](const Tile<T>& x, int t) {
+        r.tiles_over(under(top), [&](const Tile<T>& x, int t) {
             int first = V;
             x.each(t, r.lane, [&](float v, int i) {
                 if (v == top) first = min(first, i);
@@ -551,145 +878,198 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         if (threadIdx.x == 0) {
             if (a.u) a.token[row] = l.token;
             out.cut = place(top, l.token);
-            sec.rows[row] = out;
+            *to = out;
         }
         return;
     }
 
     // the sum of all weights, where it takes part
-    double Z = 0.0;
+    uint64_t all = 0;
     if (ask.sums()) {
         for (int t = threadIdx.x; t < tiles; t += kThreads) {
-            const float m = r.tops[t];
-            r.sums[t] = m > minus_inf() ? sec.sums[row * tiles + t] * r.weight_of(m) : 0.0;
+            const float m = r.tops()[t];
+            r.sums()[t] = m > minus_inf()
+                ? (uint64_t)(reinterpret_cast<const double*>(a.workspace + at.sums)[row * tiles + t] * r.weight_of(m) * r.unit + 0.5) : 0;
         }
         __syncthreads();
-        Z = r.total();
+        all = r.total();
     }
+    uint64_t sum = all, cut = 1;
+    bool drawn = false;
     if (ask.by_k || ask.by_p || ask.by_m) {
-        // what the list holds: everything from `least` on
-        float least = minus_inf();
-        bool listed = true, holds_all = true;   // holds_all: every token that can be kept (and summed for top-p)
-        if (ask.by_k && ask.k <= full && full <= (int)kCap) {
-            for (int t = threadIdx.x; t < full; t += kThreads) {
-                l.list[t] = r.tops[t] > minus_inf() ? place(r.tops[t], t) : 0;
-                l.w[t] = 0;
-            }
-            __syncthreads();
-            if (find(l, full, [&](uint32_t i) { return l.list[i]; }, place(low, V - 1), place(top, 0), true, ask.k))
-                least = logit_of(l.key);
-            __syncthreads();
-        } else if (V > (int)kCap) {
-            holds_all = false;
-            least = low;
-            listed = full <= 320;   // (on the average n (ln n + 0.6) tokens lie above the smallest of n tile maxima)
-        }
+        // no lower than min-p can keep, less a little for its rounding (not where the sum of the first k counts)
+        float floor = minus_inf();
         if (ask.by_m && !(ask.by_k && ask.by_p)) {
-            // (and no lower than min-p can keep, less a little for its rounding)
             const double x = (double)top + (log2(ask.least) - 1e-6) / ask.scale;
-            const float m = !(x > -3e38) ? minus_inf() : top == __builtin_inff() ? top : of_key(key_of((float)x) - 1);
-            if (holds_all) {
-                least = __builtin_fmaxf(least, m);
-            } else if (m >= least || !listed || !ask.by_p) {
-                holds_all = listed = true;
-                least = m;
-            }
+            if (x > -3e38) floor = top == __builtin_inff() ? under(top) : under(under((float)x));
         }
-        uint32_t n = listed ? r.gather(least, [](float, int) { return true; }) : kCap + 1;
-        bool done = n <= kCap;
-        uint64_t cut = 1;
-        auto entry = [&](uint32_t i) { return l.list[i]; };
-        const uint64_t first = place(top, 0), last = least > minus_inf() ? place(least, V - 1) : 1;
-        auto share = [&](double w) {   // the weight that top-p asks for
-            const double x = __builtin_ceil(ask.p * w);
+        const bool by_group = ask.groups(tiles);
+        const auto* maxima = (const __attribute__((address_space(3))) float*)(by_group ? r.groups() : r.tops());
+        const uint32_t count = by_group ? tiles * kSampleGroups : tiles;
+        // The list is to hold every token of logit > below.  Sure: then it holds all that can be kept (and summed for
+        // top-p).  By top-p alone, the 128 largest maxima first, then as many as 1500 tokens or so exceed.
+        float below = minus_inf(), listed_over = top;
+        bool sure = false, done = false;
+        uint32_t n = kCap + 1;
+        uint64_t listed_w = 0;
+        auto share = [&](uint64_t w) {   // the weight that top-p asks for
+            const double x = __builtin_ceil(ask.p * (double)w);
             return x < 1.0 ? (uint64_t)1 : (uint64_t)x;
         };
-        if (done) {
-            uint64_t sum = 0;
+        for (int attempt = 0;; ++attempt) {
+            below = top;   // (none)
+            sure = V <= (int)kCap;
+            if (sure) {
+                below = minus_inf();
+            } else if (ask.by_k ? (uint32_t)ask.k <= count : ask.by_p && attempt < 2) {
+                const uint32_t few = min(128u, (count + 1) / 2), many = (uint32_t)(count * (1.f - __expf(-1500.f / (float)count)));
+                const uint32_t nth = ask.by_k ? (uint32_t)ask.k : attempt == 0 ? few : many;
+                const float bound = attempt == 1 && many <= few ? minus_inf() : nth_maximum(maxima, count, nth, top, low);
+                if (bound > minus_inf()) {
+                    below = under(bound);
+                    sure = ask.by_k;
+                }
+            }
+            if (floor > minus_inf() && (floor >= below || !(below < top))) {
+                below = floor;
+                sure = true;
+            }
+            // (no lower one, or none that could do: this one would have to hold twice what the last did)
+            if (!(below < top) || (attempt > 0 && !sure && listed_w < share(sum) / 2)) break;
+            n = r.gather(below, by_group);
+            listed_over = below;
+            done = n <= kCap;
+            cut = 1;
+            if (!done) break;
+            if (n <= kFew) {
+                count_pairs(n, false);
+                // entry e's number and running weight in the order
+                const uint32_t e = threadIdx.x;
+                const Entry mine = e < n ? l.list[e] : Entry{0, 0};
+                const uint32_t rank = e < n ? l.bin_n[e] : 0;
+                const uint64_t run = e < n ? l.bin_w[e] : 0;
+                if (threadIdx.x == 0) {
+                    l.key = 0;
+                    l.key_w = 0;
+                    l.kept_w = 0;
+                }
+                __syncthreads();
+                if (e < n && rank == (ask.by_k ? min(n, (uint32_t)ask.k) : n)) {
+                    l.total_w = run;
+                    if (ask.by_k && n >= (uint32_t)ask.k) l.key = mine.place;
+                }
+                __syncthreads();
+                listed_w = l.total_w;
+                if (ask.by_k) {
+                    sum = listed_w;
+                    cut = max(cut, l.key);
+                    done = l.key != 0 || sure;
+                }
+                if (done && ask.by_p) {
+                    const uint64_t target = share(sum);
+                    if (e < n && run >= target && run - mine.w < target) l.key_w = mine.place;
+                    __syncthreads();
+                    cut = max(cut, l.key_w);
+                    done = l.key_w != 0 || sure;
+                }
+                if (done) {
+                    const bool kept = e < n && mine.place >= cut && r.weight_of(logit_of(mine.place)) >= ask.least;
+                    if (e < n && !kept) l.list[e].w = 0;
+                    if (kept) atomicMax(reinterpret_cast<unsigned long long*>(&l.kept_w), (unsigned long long)run);
+                    if (a.u) {
+                        count_pairs(n, true);   // (its first barrier is one for what is above, too)
+                        sum = l.kept_w;
+                        const uint64_t target = min((uint64_t)(u * (double)sum) + 1, sum);
+                        if (kept && l.bin_w[e] >= target && l.bin_w[e] - mine.w < target) l.token = index_of(mine.place);
+                    }
+                    __syncthreads();
+                    sum = l.kept_w;
+                    drawn = true;
+                }
+            } else {
+                const uint64_t first = place(top, 0), last = below > minus_inf() ? place(below, 0) : 1;
+                if (ask.by_k) {
+                    const bool ok = find(kByPlace, n, last, first, true, ask.k);
+                    if (ok) cut = l.key;
+                    sum = ok ? l.key_w : l.total_w;
+                    done = ok || sure;
+                    __syncthreads();
+                }
+                if (done && ask.by_p) {
+                    const bool ok = find(kByPlace, n, last, first, false, share(sum));
+                    if (ok) cut = max(cut, l.key);
+                    done = ok || sure;
+                    listed_w = l.total_w;
+                    __syncthreads();
+                }
+                if (done) {
+                    uint64_t s = 0;
+                    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+                        if (l.list[i].place < cut || r.weight_of(logit_of(l.list[i].place)) < ask.least) l.list[i].w = 0;
+                        s += l.list[i].w;
+                    }
+                    s = wave_scan_whole(s);
+                    if (r.lane == 63) l.part_w[r.wave] = s;
+                    __syncthreads();
+                    sum = lane_value(wave_scan_whole(r.lane < kWaves ? l.part_w[r.lane] : (uint64_t)0), kWaves - 1);
+                    __syncthreads();
+                    if (a.u) {
+                        find(kByIndex, n, kIndexMask + 2 - V, kIndexMask + 1, false, min((uint64_t)(u * (double)sum) + 1, sum));
+                        if (threadIdx.x == 0) l.token = index_of(l.key - 1);
+                    }
+                    drawn = true;
+                }
+            }
+            __syncthreads();
+            if (done) break;
+        }
+        if (!done) {
+            // over the row
+            __syncthreads();
+            cut = 1;
+            bool summed = false;
             if (ask.by_k) {
-                const bool ok = find(l, n, entry, last, first, true, ask.k);
-                if (ok) {
-                    cut = l.key;
-                    sum = l.key_w;
-                } else {
-                    sum = l.total_w;
+                summed = r.find_near(true, ask.k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, ask.least);
+                const bool ok = summed || r.find_far(true, ask.k);
+                if (ok) cut = l.key;
+                sum = ok ? l.key_w : l.total_w;
+                __syncthreads();
+                summed = summed && !ask.by_p;
+            }
+            if (ask.by_p) {
+                // the last one kept weighs at least (what lies behind it) / V; where the list holds all above `below`
+                // and did not reach the share, it lies there or below
+                const uint64_t target = share(sum);
+                const double behind = ((double)sum - (double)target) / ((double)V * r.unit);
+                double bottom = behind > 0.0 ? log2(behind) - 0.01 : -66.4;
+                bottom = bottom < -66.4 ? -66.4 : bottom;
+                float above = __builtin_inff();
+                double high = 0.0;
+                uint64_t off = 0;
+                if (!ask.by_k && n <= kCap && listed_w < target) {
+                    above = of_key(key_of(listed_over) + 1);
+                    high = ((double)above - (double)top) * ask.scale;
+                    off = listed_w;
                 }
-                done = ok || holds_all;
+                if (!(high < 0.0)) high = 0.0;
+                if (bottom > high - 0.01) bottom = high - 0.01;
+                const double low_x = (double)top + bottom / ask.scale;
+                const float from = !(low_x > -3e38) || top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
+                summed = r.find_near(false, target, above, off, from, high, bottom, ask.least);
+                if (summed || r.find_far(false, target)) cut = max(cut, l.key);
                 __syncthreads();
             }
-            if (done && ask.by_p) {
-                const bool ok = find(l, n, entry, last, first, false, share(ask.by_k ? (double)sum : Z * r.unit));
-                if (ok) cut = max(cut, l.key);
-                done = ok || holds_all;
-                __syncthreads();
-            }
+            if (!summed) r.sum_kept(cut, ask.least);
+            sum = r.total();
         }
-        if (done) {
-            // draw from the list, by index
-            uint64_t sum = 0;
-            for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-                if (l.list[i] < cut || r.weight_of(logit_of(l.list[i])) < ask.least) l.w[i] = 0;
-                sum += l.w[i];
-            }
-            sum = wave_scan_whole(sum);
-            if (r.lane == 63) l.part_w[r.wave] = sum;
-            __syncthreads();
-            sum = 0;
-            for (int i = 0; i < kWaves; ++i) sum += l.part_w[i];
-            if (a.u) {
-                const double x = u * (double)sum;
-                const uint64_t target = min((uint64_t)x + 1, sum);
-                __syncthreads();
-                find(l, n, [&](uint32_t i) { return l.w[i] ? (l.list[i] & kIndexMask) + 1 : 0; }, kIndexMask + 2 - V, kIndexMask + 1,
-                     false, target);
-                if (threadIdx.x == 0) a.token[row] = (int)(kIndexMask + 1 - l.key);
-            }
-            if (threadIdx.x == 0) {
-                out.per = r.unit / (double)sum;
-                out.cut = cut;
-                out.least = ask.least;
-                sec.rows[row] = out;
-            }
-            return;
-        }
-        // over the row
-        cut = 1;
-        uint64_t sum = 0;
-        if (ask.by_k) {
-            const bool ok = r.find_row(true, ask.k);
-            if (ok) cut = l.key;
-            sum = ok ? l.key_w : l.total_w;
-            __syncthreads();
-        }
-        if (ask.by_p) {
-            if (r.find_row(false, share(ask.by_k ? (double)sum : Z * r.unit))) cut = max(cut, l.key);
-            __syncthreads();
-        }
-        for (int t = threadIdx.x; t < tiles; t += kThreads) r.sums[t] = 0.0;
-        __syncthreads();
-        r.tiles_from(cut > 1 ? logit_of(cut) : minus_inf(), [&](const Tile<T>& x, int t) {
-            double s = 0.0;
-            x.each(t, r.lane, [&](float v, int i) {
-                if (v > minus_inf() && place(v, i) >= cut) {
-                    const double w = r.weight_of(v);
-                    if (w >= ask.least) s += w;
-                }
-            });
-            s = wave_sum(s);
-            if (r.lane == 0) r.sums[t] = s;
-        });
-        __syncthreads();
-        Z = r.total();
         out.cut = cut;
         out.least = ask.least;
     }
-    if (threadIdx.x < 64) {
-        const int token = a.u ? r.draw(u * Z, out.cut, out.least) : 0;
-        if (threadIdx.x == 0) {
-            if (a.u) a.token[row] = token;
-            out.per = 1.0 / Z;
-            sec.rows[row] = out;
-        }
+    if (a.u && !drawn) r.draw(min((uint64_t)(u * (double)sum) + 1, sum), out.cut, out.least);
+    if (threadIdx.x == 0) {
+        if (a.u) a.token[row] = l.token;
+        out.per = r.unit / (double)sum;
+        *to = out;
     }
 }
 
@@ -697,47 +1077,47 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
 
 template <typename T>
 __global__ __launch_bounds__(256) void sample_probs_kernel(SampleArgs a) {
+    constexpr int M = Tile<T>::M;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int tiles = (a.V + kTile - 1) / kTile;
-    const uint32_t groups = (uint32_t)(tiles + 3) / 4;
-    const uint32_t row = blockIdx.x / groups;
-    const int t = (int)(blockIdx.x % groups) * 4 + wave;
+    const uint32_t per_row = (uint32_t)(tiles + 3) / 4;
+    const uint32_t row = blockIdx.x / per_row;
+    const int t = (int)(blockIdx.x % per_row) * 4 + wave;
     if (t >= tiles) return;
-    const Sections s = sections(a, tiles);
-    const SampleRow r = s.rows[row];
-    const float m = s.tops[(size_t)row * tiles + t];
+    const SampleSections at = sample_sections(a.R, tiles);
+    const SampleRow r = reinterpret_cast<const SampleRow*>(a.workspace + at.rows)[row];
+    const float m = reinterpret_cast<const float*>(a.workspace + at.tops)[(size_t)row * tiles + t];
     T* probs = static_cast<T*>(a.probs) + (size_t)row * a.V;
-    Tile<T> x;
+    typename Vec16<T>::type y[Tile<T>::J];
     if (m > minus_inf() && ((uint64_t)key_of(m) << kIndexBits | kIndexMask) >= r.cut && weight(m, r.top, r.scale) >= r.least) {
+        Tile<T> x;
         x.load(static_cast<const T*>(a.logits) + (size_t)row * a.V, t, a.V, lane);
 #pragma unroll
         for (int j = 0; j < Tile<T>::J; ++j)
 #pragma unroll
-            for (int e = 0; e < Tile<T>::M; ++e) {
-                const float l = x.x[j][e];
-                const int v = t * kTile + (j * 64 + lane) * Tile<T>::M + e;
-                const double w = l > minus_inf() && place(l, min(v, a.V - 1)) >= r.cut ? weight(l, r.top, r.scale) : 0.0;
-                x.x[j][e] = w >= r.least ? (float)(w * r.per) : 0.f;
+            for (int e = 0; e < M; ++e) {
+                const float l = __builtin_fmaxf(to_f32((T)x.v[j][e]), minus_inf());
+                const int v = t * kTile + (j * 64 + lane) * M + e;
+                double w = 0.0;
+                if (l > minus_inf() && place(l, min(v, a.V - 1)) >= r.cut) w = weight(l, r.top, r.scale);
+                y[j][e] = from_f32<T>(w >= r.least ? (float)(w * r.per) : 0.f);
             }
     } else {
 #pragma unroll
         for (int j = 0; j < Tile<T>::J; ++j)
 #pragma unroll
-            for (int e = 0; e < Tile<T>::M; ++e) x.x[j][e] = 0.f;
+            for (int e = 0; e < M; ++e) y[j][e] = (T)0.f;
     }
 #pragma unroll
     for (int j = 0; j < Tile<T>::J; ++j) {
-        const int v = t * kTile + (j * 64 + lane) * Tile<T>::M;
-        typename Vec16<T>::type y;
-#pragma unroll
-        for (int e = 0; e < Tile<T>::M; ++e) y[e] = from_f32<T>(x.x[j][e]);
-        if (v + Tile<T>::M <= a.V) {
-            __builtin_memcpy(probs + v, &y, 16);
+        const int v = t * kTile + (j * 64 + lane) * M;
+        if (v + M <= a.V) {
+            __builtin_memcpy(probs + v, &y[j], 16);
         } else {
 #pragma unroll
-            for (int e = 0; e < Tile<T>::M; ++e)
-                if (v + e < a.V) probs[v + e] = y[e];
+            for (int e = 0; e < M; ++e)
+                if (v + e < a.V) probs[v + e] = y[j][e];
         }
     }
 }
@@ -746,13 +1126,14 @@ template <typename T>
 hipError_t launch_sample_t(const SampleArgs& a, hipStream_t stream) {
     static std::atomic<uint64_t> done{0};
     const int64_t tiles = sample_tiles(a.V);
-    const int fixed = (int)((sizeof(RowLds) + 15) / 16 * 16);
-    const int most = fixed + (int)sample_tiles(KDA_MAX_VOCAB) * 12;
+    // (and the maxima of the groups of kGroupTiles tiles, which are fewer bytes than those of the most tiles)
+    static_assert(kGroupTiles * (12 + 4 * kSampleGroups) <= KDA_MAX_VOCAB / kTile * 12, "the larger of the two");
+    const int most = kRowBytes + (int)sample_tiles(KDA_MAX_VOCAB) * 12;
     const hipError_t e = raise_lds_limit_once(reinterpret_cast<const void*>(sample_rows_kernel<T>), most, done);
     if (e != hipSuccess) return e;
     const dim3 grid((unsigned)sample_groups(a.R, a.V)), block(256);
     sample_tiles_kernel<T><<<grid, block, 0, stream>>>(a);
-    sample_rows_kernel<T><<<dim3((unsigned)a.R), dim3(kThreads), fixed + (size_t)tiles * 12, stream>>>(a);
+    sample_rows_kernel<T><<<dim3((unsigned)a.R), dim3(kThreads), kRowBytes + (size_t)tiles * (tiles <= kGroupTiles ? 12 + 4 * kSampleGroups : 12), stream>>>(a);
     if (a.probs) sample_probs_kernel<T><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }

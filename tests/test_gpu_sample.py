@@ -199,6 +199,33 @@ def test_far_logits_weigh_nothing_and_near_ones_are_told_apart():
     check(kda, y, [0.1, 0.9, 0.5, 0.7], [0.01, 0.1, 1.0, 0.05], [5, 500, 4000, 4999], [0.5, 0.9, 0.99, 0.8])
 
 
+@pytest.mark.parametrize("V", [70, 3000, 40000])
+def test_zeros_of_both_signs(V):
+    """Log-probabilities, whose largest may be 0; both zeros are one value, where
+    they are the largest, where a filter ends and where a tile holds nothing else."""
+    kda = need_gpu()
+    case(f"zeros V={V}")
+    x = -rows(6, V, "f32", 40).abs()
+    x[0, ::7] = 0.0
+    x[0, ::14] = -0.0
+    x[1] = -0.0
+    x[1, 1::2] = 0.0
+    x[2, V // 2] = -0.0
+    x[3] = torch.round(rows(1, V, "f32", 41)[0])
+    x[4] = 0.0
+    x[4, V - 1] = 1e-45
+    x[5] = -1e-45
+    x[5, 3] = -0.0
+    u = uniform(6, 42)
+    for T in ([0.0] * 6, [1.0] * 6):
+        check(kda, x, u, T)
+    check(kda, x, u, None, [3, 5, 1, V // 3, 2, 2])
+    check(kda, x, u, None, [V // 2] * 6)
+    check(kda, x, u, None, None, [0.7, 0.3, 0.9, 0.8, 0.3, 0.6])
+    check(kda, x, u, None, None, None, [1.0] * 6)
+    check(kda, x.bfloat16(), u, [1.0] * 6, [V // 3] * 6, [0.9] * 6, [0.5] * 6)
+
+
 def test_leading_dimensions_and_given_outputs():
     kda = need_gpu()
     case("[B, N, V] logits, as the verification of drafts has its probabilities")
