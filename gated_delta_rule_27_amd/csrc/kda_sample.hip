@@ -170,6 +170,9 @@ __device__ __forceinline__ float wave_top_of_quads(float x) {
 }
 __device__ __forceinline__ float wave_top(float x) { return wave_top_of_quads(quad_top(x)); }
 
+// (One tile a wavefront: two to eight, one after the other with the next one's
+// loads in flight, took 256 x 160,000 fp32 from 35 to 41 us with sums and not from
+// 33 without.)
 template <typename T>
 __global__ __launch_bounds__(256) void sample_tiles_kernel(SampleArgs a) {
     const int lane = threadIdx.x & 63;
@@ -218,7 +221,7 @@ struct RowLds {
     uint32_t bin_n[kBins];
     uint64_t part_w[kWaves];
     uint32_t part_n[kWaves];
-    float part_f[2][kWaves];
+    float part_f[3][kWaves];
     Entry few[64];
     float ring[kWaves][128];   // weights to be, on their way
     // what one thread tells the others
@@ -399,13 +402,17 @@ __device__ __noinline__ float nth_maximum(const __attribute__((address_space(3))
         l.bin_n[threadIdx.x] = 0;
         __syncthreads();
         const int bits = 64 - __builtin_clzll((hi - lo) | 1), shift = bits > 10 ? bits - 10 : 0;
+        uint32_t rest = 0;   // of the last bin: most of them, as a rule
         for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
             const float m = maxima[i];
             if (!(m > minus_inf())) continue;
             const uint64_t k = place(m, i);
-            if (bin < 0) atomicAdd(&l.bin_n[bin_of(m)], 1u);
-            else if (bin_of(m) == bin && k >= lo && k <= hi) atomicAdd(&l.bin_n[(hi - k) >> shift], 1u);
+            const int at = bin < 0 ? bin_of(m) : bin_of(m) == bin && k >= lo && k <= hi ? (int)((hi - k) >> shift) : kBins;
+            if (at < kBins - 1) atomicAdd(&l.bin_n[at], 1u);
+            else rest += at == kBins - 1;
         }
+        rest = wave_scan_whole(rest);
+        if ((threadIdx.x & 63) == 63 && rest) atomicAdd(&l.bin_n[kBins - 1], rest);
         __syncthreads();
         const int b = cross<false>(true, nth - before);
         if (b < 0) return minus_inf();
@@ -437,6 +444,23 @@ __device__ __noinline__ float nth_maximum(const __attribute__((address_space(3))
     return logit_of(l.key);
 }
 
+// Whether the list will hardly hold the tokens of logit > below: of G groups with n
+// such tokens spread over them, G (1 - e^(-n / G)) have one at least.
+__device__ __noinline__ bool overflows(const __attribute__((address_space(3))) float* maxima, uint32_t count, uint32_t tokens,
+                                       float below) {
+    KDA_ROW_LDS;
+    if (threadIdx.x == 0) l.n = 0;
+    __syncthreads();
+    uint32_t over = 0;
+    for (uint32_t i = threadIdx.x; i < count; i += kThreads) over += maxima[i] > below;
+    over = wave_scan_whole(over);
+    if ((threadIdx.x & 63) == 63) atomicAdd(&l.n, over);
+    __syncthreads();
+    const float share = (float)l.n / (float)count;
+    __syncthreads();
+    return -(float)count * __logf(__builtin_fmaxf(1.f - share, 1.f / (float)(4 * count))) > 1.25f * kCap && count * tokens > kCap;
+}
+
 template <typename T>
 struct Row {
     const T* logits;
@@ -460,11 +484,13 @@ struct Row {
         return __builtin_bit_cast(uint64_t, w + c) - __builtin_bit_cast(uint64_t, c);
     }
     __device__ __forceinline__ double weight_of(float x) const { return weight(x, top, scale); }
-    // f(tile, its number) for the tiles with a logit > below, the next one's loads in flight
+    // f(tile, its number) for the tiles with a logit > below (with `step` 2 every other
+    // one of a wavefront's, others than its neighbours'), the next one's loads in flight
     template <typename F>
-    __device__ __forceinline__ void tiles_over(float below, F&& f) const {
+    __device__ __forceinline__ void tiles_over(float below, int step, F&& f) const {
         auto next = [&](int t) {
             for (; t < tiles; t += kWaves) {
+                if (step == 2 && ((t / kWaves + t) & 1)) continue;
                 const float m = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, tops()[t])));
                 if (m > below) break;
             }
@@ -533,27 +559,28 @@ struct Row {
         constexpr int M = Tile<T>::M;
         start_list();
         if (!by_group) {
-            tiles_over(below, [&](const Tile<T>& x, int t) { append(x, t, [&](float v) { return v > below; }); });
+            tiles_over(below, 1, [&](const Tile<T>& x, int t) { append(x, t, [&](float v) { return v > below; }); });
             return listed();
         }
-        // a group's 64 tokens, one a lane, four groups in flight
+        // a group's 64 tokens, one a lane, eight groups in flight
+        constexpr int kAhead = 8;
         const int count = tiles * kSampleGroups, mine = lane / (4 * M) * 64 * M + lane % (4 * M);
         for (int g0 = wave * 64; g0 < count; g0 += kThreads) {
             uint64_t todo = __ballot(g0 + lane < count && groups()[min(g0 + lane, count - 1)] > below);
             while (todo) {
-                float x[4];
-                int i[4];
+                float x[kAhead];
+                int i[kAhead];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kAhead; ++q) {
                     const int g = g0 + (todo ? __builtin_ctzll(todo) : 0);
                     i[q] = todo ? g / kSampleGroups * kTile + g % kSampleGroups * 4 * M + mine : V;
                     todo &= todo - (todo != 0);
                     x[q] = logit(min(i[q], V - 1));
                 }
-                uint64_t those[4];
+                uint64_t those[kAhead];
                 uint32_t named = 0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kAhead; ++q) {
                     those[q] = __ballot(i[q] < V && x[q] > below);
                     named += (uint32_t)__builtin_popcountll(those[q]);
                 }
@@ -561,7 +588,7 @@ struct Row {
                 if (lane == 0) at = atomicAdd(&l.n, named);
                 at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kAhead; ++q) {
                     const uint32_t to = at + rank_in(those[q]);
                     if ((those[q] >> lane & 1) && to < kCap) l.list[to].w = (uint64_t)i[q];
                     at += (uint32_t)__builtin_popcountll(those[q]);
@@ -571,14 +598,16 @@ struct Row {
         return listed();
     }
 
-    // Sums over a tile of the weights of the tokens that `keep` names, through a ring
-    // that packs them: `all`, and `kept`, of those that weigh `least`; in lane 63.
-    template <typename F>
-    __device__ __forceinline__ void weigh(const Tile<T>& x, int t, double least, F&& keep, uint64_t& all, uint64_t& kept,
-                                          uint32_t& passed) const {
+    // Sums over a tile of the weights of its tokens over `border`, through a ring that
+    // packs them: `all`, and `kept`, of those that weigh `least`; in lane 63.  Their
+    // number is added to `passed`; those over `from` and not over `border` go to the list.
+    __device__ __forceinline__ void weigh(const Tile<T>& x, int t, float from, float border, double least, uint64_t& all,
+                                          uint64_t& kept, uint32_t& passed) const {
         KDA_ROW_LDS;
         float* ring = l.ring[wave];
-        uint32_t head = 0, held = 0;   // of all lanes, as is their number, added to `passed`
+        uint32_t head = 0, held = 0, named = 0;   // of all lanes
+        uint64_t between[kPer];
+        int slot = 0;
         all = kept = 0;
         auto flush = [&](uint32_t n) {
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
@@ -590,10 +619,11 @@ struct Row {
             head += 64;
         };
         x.each(t, lane, [&](float v, int) {
-            const uint64_t those = __ballot(keep(v));
+            const uint64_t those = __ballot(v > border);
+            between[slot] = __ballot(v > from) & ~those;
+            named += (uint32_t)__builtin_popcountll(between[slot++]);
             if (those == 0) return;
-            if (those >> lane & 1)
-                ring[(head + held + rank_in(those)) & 127] = v;
+            if (v > border) ring[(head + held + rank_in(those)) & 127] = v;
             held += (uint32_t)__builtin_popcountll(those);
             if (held >= 64) {
                 flush(64);
@@ -605,6 +635,18 @@ struct Row {
         passed += held;
         all = wave_scan_whole(all);
         kept = wave_scan_whole(kept);
+        if (named == 0) return;
+        uint32_t at = 0;
+        if (lane == 0) at = atomicAdd(&l.n, named);
+        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
+        slot = 0;
+        x.each(t, lane, [&](float, int i) {
+            const uint64_t those = between[slot++];
+            if (those == 0) return;
+            const uint32_t to = at + rank_in(those);
+            if ((those >> lane & 1) && to < kCap) l.list[to].w = (uint64_t)i;   // (its place follows)
+            at += (uint32_t)__builtin_popcountll(those);
+        });
     }
 
     // The same as find(), over the row's tokens: `below` < logit < `above`, which
@@ -620,17 +662,21 @@ struct Row {
         const int exact = !by_count && off == 0 ? kBins / 16 : 0;
         clear_bins(l);
         uint32_t rest = 0;
-        tiles_over(below, [&](const Tile<T>& x, int t) {
+        // (where there are many tiles, every other one stands for two: thousands of tokens are off by a fraction of a
+        // bin, and several are collected.  Not so for weights, of which a few tokens may be most.)
+        const int step = by_count && tiles >= 64 ? 2 : 1;
+        tiles_over(below, step, [&](const Tile<T>& x, int t) {
             x.each(t, lane, [&](float v, int) {
                 if (v > below && v < above) {
                     const int b = bin_of(v);
-                    if (b < kBins - 1) atomicAdd(&l.bin_n[b], 1u);
-                    else ++rest;
+                    if (b < kBins - 1) atomicAdd(&l.bin_n[b], (uint32_t)step);
+                    else rest += step;
                     if (b < exact) add(&l.bin_w[b], whole(weight_of(v)));
                 }
             });
         });
-        if (rest) atomicAdd(&l.bin_n[kBins - 1], rest);
+        rest = wave_scan_whole(rest);
+        if (lane == 63) atomicAdd(&l.bin_n[kBins - 1], rest);
         __syncthreads();
         // (what a bin weighs: about its middle, but for the first ones, whose few tokens may be most of it)
         if (!by_count && (int)threadIdx.x >= exact) {
@@ -644,7 +690,7 @@ struct Row {
         uint32_t here = l.here_n;
         for (int r = 0; r < 8; ++r) {
             const uint32_t more = (j0 > 0 ? l.bin_n[j0 - 1] : 0) + (j1 < kBins - 1 ? l.bin_n[j1 + 1] : 0);
-            if (here + more > kCap - 64) break;
+            if (here + more > kCap - 256) break;
             here += more;
             if (j0 > 0) --j0;
             if (j1 < kBins - 1) ++j1;
@@ -662,10 +708,9 @@ struct Row {
         uint32_t passed = 0;   // of all lanes
         // (what is from `above` on is over, wherever bin 0 begins)
         const float border = __builtin_fminf(over, under(above));
-        tiles_over(from, [&](const Tile<T>& x, int t) {
+        tiles_over(from, 1, [&](const Tile<T>& x, int t) {
             uint64_t w, kept;
-            append(x, t, [&](float v) { return v > from && !(v > border); });
-            weigh(x, t, least, [&](float v) { return v > border; }, w, kept, passed);
+            weigh(x, t, from, border, least, w, kept, passed);
             all += w;
             if (lane == 63) sums()[t] = kept;
         });
@@ -700,7 +745,7 @@ struct Row {
             const int shift = bits > 10 ? bits - 10 : 0;
             __syncthreads();
             clear_bins(l);
-            tiles_over(minus_inf(), [&](const Tile<T>& x, int t) {
+            tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
                 x.each(t, lane, [&](float v, int i) {
                     if (v > minus_inf()) {
                         const uint64_t k = place(v, i);
@@ -719,7 +764,7 @@ struct Row {
             lo = hi - lo > width ? hi - width : lo;
         }
         start_list();
-        tiles_over(minus_inf(), [&](const Tile<T>& x, int t) {
+        tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
             x.each(t, lane, [&](float v, int i) {
                 if (v > minus_inf()) {
                     const uint64_t k = place(v, i);
@@ -742,7 +787,7 @@ struct Row {
         __syncthreads();
         const float from = cut > 1 ? logit_of(cut) : minus_inf(), below = cut > 1 ? under(from) : from;
         const int border = index_of(cut);
-        tiles_over(below, [&](const Tile<T>& x, int t) {
+        tiles_over(below, 1, [&](const Tile<T>& x, int t) {
             uint64_t all, kept;
             uint32_t passed = 0;
             Tile<T> y = x;   // (of logits equal to the cut's, those up to its index)
@@ -752,7 +797,7 @@ struct Row {
 #pragma unroll
                     for (int e = 0; e < Tile<T>::M; ++e)
                         if (to_f32((T)y.v[j][e]) == from && t * kTile + (j * 64 + lane) * Tile<T>::M + e > border) y.v[j][e] = (T)minus_inf();
-            weigh(y, t, least, [&](float v) { return v > below; }, all, kept, passed);
+            weigh(y, t, below, below, least, all, kept, passed);
             if (lane == 63) sums()[t] = kept;
         });
         __syncthreads();
@@ -825,7 +870,8 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     const float u0 = a.u ? a.u[row] : 0.f;
     const double u = u0 > 0.f ? (u0 < 1.f ? (double)u0 : 1.0) : 0.0;
 
-    float top = minus_inf(), low = __builtin_inff();   // largest; smallest of full tiles that are not empty
+    float top = minus_inf(), low = __builtin_inff();   // largest; smallest of full tiles that are not empty,
+    float least_top = __builtin_inff();                // of groups that are not
     const int full = V / kTile;
     for (int t = threadIdx.x; t < tiles; t += kThreads) {
         const float m = reinterpret_cast<const float*>(a.workspace + at.tops)[row * tiles + t];
@@ -835,18 +881,25 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     }
     if (ask.groups(tiles)) {
         const float* from = reinterpret_cast<const float*>(a.workspace + at.groups) + row * tiles * kSampleGroups;
-        for (int i = threadIdx.x; i < tiles * kSampleGroups; i += kThreads) r.groups()[i] = from[i];
+        for (int i = threadIdx.x; i < tiles * kSampleGroups; i += kThreads) {
+            const float m = from[i];
+            r.groups()[i] = m;
+            if (m > minus_inf()) least_top = __builtin_fminf(least_top, m);
+        }
     }
     top = wave_top(top);
     low = -wave_top(-low);
+    least_top = -wave_top(-least_top);
     if (r.lane == 0) {
         l.part_f[0][r.wave] = top;
         l.part_f[1][r.wave] = low;
+        l.part_f[2][r.wave] = least_top;
     }
     if (threadIdx.x == 0) l.token = V;
     __syncthreads();
     top = wave_top(r.lane < kWaves ? l.part_f[0][r.lane] : minus_inf());
     low = -wave_top(r.lane < kWaves ? -l.part_f[1][r.lane] : minus_inf());
+    least_top = -wave_top(r.lane < kWaves ? -l.part_f[2][r.lane] : minus_inf());
     r.top = top;
     r.scale = ask.scale;
     const int bits = 32 - __builtin_clz((uint32_t)V);   // V < 2^bits
@@ -867,7 +920,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         return;
     }
     if (ask.greedy) {
-        r.tiles_over(under(top), [&](const Tile<T>& x, int t) {
+        r.tiles_over(under(top), 1, [&](const Tile<T>& x, int t) {
             int first = V;
             x.each(t, r.lane, [&](float v, int i) {
                 if (v == top) first = min(first, i);
@@ -924,7 +977,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
             } else if (ask.by_k ? (uint32_t)ask.k <= count : ask.by_p && attempt < 2) {
                 const uint32_t few = min(128u, (count + 1) / 2), many = (uint32_t)(count * (1.f - __expf(-1500.f / (float)count)));
                 const uint32_t nth = ask.by_k ? (uint32_t)ask.k : attempt == 0 ? few : many;
-                const float bound = attempt == 1 && many <= few ? minus_inf() : nth_maximum(maxima, count, nth, top, low);
+                const float bound = attempt == 1 && many <= few ? minus_inf() : nth_maximum(maxima, count, nth, top, nth <= (uint32_t)full ? low : __builtin_fminf(low, least_top));
                 if (bound > minus_inf()) {
                     below = under(bound);
                     sure = ask.by_k;
@@ -934,8 +987,17 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 below = floor;
                 sure = true;
             }
-            // (no lower one, or none that could do: this one would have to hold twice what the last did)
-            if (!(below < top) || (attempt > 0 && !sure && listed_w < share(sum) / 2)) break;
+            // (hardly one that will do, if much of what the last one left out is asked for: then as far as min-p goes)
+            if (attempt > 0 && !sure && (double)(share(sum) - listed_w) > 0.3 * (double)(sum - listed_w)) {
+                below = floor > minus_inf() ? floor : top;
+                sure = true;
+            }
+            if (!(below < top)) break;
+            if (overflows(maxima, count, by_group ? kTile / kSampleGroups : kTile, below)) {
+                n = kCap + 1;
+                done = false;
+                break;
+            }
             n = r.gather(below, by_group);
             listed_over = below;
             done = n <= kCap;
@@ -973,7 +1035,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                     done = l.key_w != 0 || sure;
                 }
                 if (done) {
-                    const bool kept = e < n && mine.place >= cut && r.weight_of(logit_of(mine.place)) >= ask.least;
+                    const bool kept = e < n && mine.place >= cut && (!ask.by_m || r.weight_of(logit_of(mine.place)) >= ask.least);
                     if (e < n && !kept) l.list[e].w = 0;
                     if (kept) atomicMax(reinterpret_cast<unsigned long long*>(&l.kept_w), (unsigned long long)run);
                     if (a.u) {
@@ -1005,7 +1067,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 if (done) {
                     uint64_t s = 0;
                     for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-                        if (l.list[i].place < cut || r.weight_of(logit_of(l.list[i].place)) < ask.least) l.list[i].w = 0;
+                        if (l.list[i].place < cut || (ask.by_m && r.weight_of(logit_of(l.list[i].place)) < ask.least)) l.list[i].w = 0;
                         s += l.list[i].w;
                     }
                     s = wave_scan_whole(s);
