@@ -29,47 +29,49 @@ typedef floatx4 State[4][4];   // [block][row], four columns
 __device__ __forceinline__ float decay(float x) { return exp_f32(x < -120.f ? -120.f : x, 0.f); }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
-// largest of 32 lanes (the magnitudes' bits: a NaN is larger than anything)
+// largest of 16, of 32 lanes (the magnitudes' bits: a NaN is larger than anything)
 template <int kCtrl>
 __device__ __forceinline__ uint32_t max_with(uint32_t x) {
     return max(x, (uint32_t)__builtin_amdgcn_mov_dpp((int)x, kCtrl, 0xf, 0xf, true));
 }
-__device__ __forceinline__ uint32_t max32(uint32_t x) {
+__device__ __forceinline__ uint32_t max16(uint32_t x) {
     x = max_with<0x128>(x);   // rotations of a row of 16 by 8, 4, 2, 1
     x = max_with<0x124>(x);
     x = max_with<0x122>(x);
-    x = max_with<0x121>(x);
+    return max_with<0x121>(x);
+}
+__device__ __forceinline__ uint32_t max32(uint32_t x) {
+    x = max16(x);
     return max(x, (uint32_t)__builtin_amdgcn_ds_swizzle((int)x, 0x401f));   // the other row
 }
 
-// the code of x, in the low byte
+// the code of x, in the low byte: adding 1.5 * 2^23 to the exact product rounds to
+// a whole number, ties to even, and leaves it in the low bits
 __device__ __forceinline__ uint32_t code(float x, float inverse) {
-#pragma clang fp contract(off)
-    // (adding 1.5 * 2^23 rounds to a whole number, ties to even, and leaves it
-    // in the low bits; the product is rounded before, as written)
-    const float y = x * inverse;
-    return __builtin_bit_cast(uint32_t, y + 12582912.f);
+    return __builtin_bit_cast(uint32_t, __builtin_fmaf(x, inverse, 12582912.f));
+}
+// four rows' codes of a column
+__device__ __forceinline__ uint32_t codes_of(floatx4 x, floatx4 inverse) {
+    const uint32_t lo = __builtin_amdgcn_perm(code(x[1], inverse[1]), code(x[0], inverse[0]), 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(code(x[3], inverse[3]), code(x[2], inverse[2]), 0x04000c0cu);
+    return lo | hi;
+}
+// four rows of a column back
+__device__ __forceinline__ floatx4 values_of(uint32_t codes, floatx4 m) {
+    floatx4 x;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) x[r] = (float)(int8_t)(codes >> (8 * r)) * m[r];
+    return x;
 }
 
-// scales and codes of a state out, through an LDS tile of [value][key] codes
+// Scales and codes of a state out, through an LDS tile of [value][key] codes.
 struct QuantiseLds {
     uint32_t tile[kD * kLd];
     uint32_t top[kD];      // largest magnitude of each row
     float inverse[kD];
 };
-__device__ __forceinline__ void quantise(const State& v, const Place& p, QuantiseLds& lds, int8_t* codes, float* scale) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        uint32_t m[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            m[r] = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) m[r] = max(m[r], magnitude(v[t][r][e]));
-            m[r] = max32(m[r]);
-        }
-        if (p.l == 0) *reinterpret_cast<uintx4*>(lds.top + p.row(t)) = uintx4{m[0], m[1], m[2], m[3]};
-    }
+// top -> inverse and scale; all threads, a barrier before and after
+__device__ __forceinline__ void scales(QuantiseLds& lds, float* scale) {
     __syncthreads();
     if (threadIdx.x < kD) {
         const uint32_t m = lds.top[threadIdx.x];
@@ -80,16 +82,8 @@ __device__ __forceinline__ void quantise(const State& v, const Place& p, Quantis
         scale[threadIdx.x] = !held ? 0.f : m >= 0x7f800000u ? __builtin_nanf("") : top / 127.f;
     }
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const floatx4 inverse = *reinterpret_cast<const floatx4*>(lds.inverse + p.row(t));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t lo = __builtin_amdgcn_perm(code(v[t][1][e], inverse[1]), code(v[t][0][e], inverse[0]), 0x0c0c0400u);
-            const uint32_t hi = __builtin_amdgcn_perm(code(v[t][3][e], inverse[3]), code(v[t][2][e], inverse[2]), 0x04000c0cu);
-            lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)] = lo | hi;
-        }
-    }
+}
+__device__ __forceinline__ void codes_out(const QuantiseLds& lds, int8_t* codes) {
     __syncthreads();
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -99,55 +93,63 @@ __device__ __forceinline__ void quantise(const State& v, const Place& p, Quantis
     }
 }
 
-// LDS of a state read back: codes, then (with a window) the keys as far as
-// they are decayed, the updates, and what each row is multiplied by
+// LDS of a state read back: codes; the keys as far as they are decayed after the
+// last token, the updates (rows of zeros up to a multiple of four), and what each
+// key channel's codes are multiplied by
+constexpr int kWinLd = kD + 16;   // (16 floats more: other banks)
 struct ReadLds {
     uint32_t tile[kD * kLd];
     float row[kD];
 };
 struct WindowLds {
-    float k[kMaxWindow][kD];
-    float u[kMaxWindow][kD];
+    float k[kMaxWindow][kWinLd];
+    float u[kMaxWindow][kWinLd];
 };
 
-template <typename T>
-__device__ __forceinline__ void read_state(State& v, const Place& p, ReadLds& lds, WindowLds* wl, const int8_t* codes,
-                                           const float* scale, const CacheWindow& w, int64_t at, int n) {
+// codes, window and scales into LDS; all threads, a barrier at the end
+template <typename T, bool kStream>
+__device__ __forceinline__ void stage(ReadLds& lds, WindowLds& wl, const int8_t* codes, const float* scale, const CacheWindow& w,
+                                      size_t at, int n) {
     uintx4 x[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-        x[s] = __builtin_nontemporal_load(reinterpret_cast<const uintx4*>(codes) + threadIdx.x + 256 * s);
-    const int i = threadIdx.x & (kD - 1);
-    if (n > 0) {
-        const int64_t base = at * w.W * kD + i;
-        if (threadIdx.x < kD) {
-            const T* k = static_cast<const T*>(w.k) + base;
-            const T* la = static_cast<const T*>(w.log_alpha) + base;
-            float kt[kMaxWindow], lt[kMaxWindow];
+    for (int s = 0; s < 4; ++s) {
+        const uintx4* p = reinterpret_cast<const uintx4*>(codes) + threadIdx.x + 256 * s;
+        x[s] = kStream ? __builtin_nontemporal_load(p) : *p;
+    }
+    const int i = threadIdx.x & (kD - 1), most = (n + 3) & ~3;
+    const size_t base = at * w.W * kD + i;
+    if (threadIdx.x < kD) {
+        const T* k = static_cast<const T*>(w.k) + base;
+        const T* la = static_cast<const T*>(w.log_alpha) + base;
+        const float sc = scale[i];
+        T kt[kMaxWindow], lt[kMaxWindow];
 #pragma unroll
-            for (int t = 0; t < kMaxWindow; ++t) {
-                if (t < n) {
-                    kt[t] = to_f32(k[t * kD]);
-                    lt[t] = to_f32(la[t * kD]);
-                }
+        for (int t = 0; t < kMaxWindow; ++t) {
+            if (t < n) {
+                kt[t] = k[t * kD];
+                lt[t] = la[t * kD];
             }
-            float g = 0.f;
-#pragma unroll
-            for (int t = kMaxWindow - 1; t >= 0; --t) {
-                if (t < n) {
-                    wl->k[t][i] = kt[t] * decay(g);
-                    g += lt[t];
-                }
-            }
-            lds.row[i] = scale[i] * decay(g);
-        } else {
-            const T* u = static_cast<const T*>(w.u) + base;
-#pragma unroll
-            for (int t = 0; t < kMaxWindow; ++t)
-                if (t < n) wl->u[t][i] = to_f32(u[t * kD]);
         }
-    } else if (threadIdx.x < kD) {
-        lds.row[i] = scale[i];
+        float g = 0.f;
+#pragma unroll
+        for (int t = kMaxWindow - 1; t >= 0; --t) {
+            if (t < n) {
+                wl.k[t][i] = to_f32(kt[t]) * decay(g);
+                g += to_f32(lt[t]);
+            } else if (t < most) {
+                wl.k[t][i] = 0.f;
+            }
+        }
+        lds.row[i] = sc * decay(g);
+    } else {
+        const T* u = static_cast<const T*>(w.u) + base;
+        T ut[kMaxWindow];
+#pragma unroll
+        for (int t = 0; t < kMaxWindow; ++t)
+            if (t < n) ut[t] = u[t * kD];
+#pragma unroll
+        for (int t = 0; t < kMaxWindow; ++t)
+            if (t < most) wl.u[t][i] = t < n ? to_f32(ut[t]) : 0.f;
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
@@ -155,25 +157,6 @@ __device__ __forceinline__ void read_state(State& v, const Place& p, ReadLds& ld
         *reinterpret_cast<uintx4*>(lds.tile + (piece >> 3) * kLd + 4 * (piece & 7)) = x[s];
     }
     __syncthreads();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-        const floatx4 m = *reinterpret_cast<const floatx4*>(lds.row + p.row(t));
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int d = (int)lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[t][r][e] = (float)(int8_t)(d >> (8 * r)) * m[r];
-        }
-    }
-    for (int t = 0; t < n; ++t) {
-        const floatx4 u = *reinterpret_cast<const floatx4*>(&wl->u[t][4 * p.l]);
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const floatx4 k = *reinterpret_cast<const floatx4*>(&wl->k[t][p.row(b)]);
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[b][r] += k[r] * u;
-        }
-    }
 }
 
 __device__ __forceinline__ int window_count(const CacheWindow& w, int64_t b) {
@@ -203,7 +186,27 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheMoveArgs a) {
         if (__syncthreads_or(later)) return;
     }
     const size_t at = (size_t)page * a.H + h;
-    quantise(v, p, lds, a.codes + at * kD * kD, a.scale + at * kD);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        uint32_t m[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) m[r] = max(m[r], magnitude(v[t][r][e]));
+            m[r] = max32(m[r]);
+        }
+        if (p.l == 0) *reinterpret_cast<uintx4*>(lds.top + p.row(t)) = uintx4{m[0], m[1], m[2], m[3]};
+    }
+    scales(lds, a.scale + at * kD);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const floatx4 inverse = *reinterpret_cast<const floatx4*>(lds.inverse + p.row(t));
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)] = codes_of(floatx4{v[t][0][e], v[t][1][e], v[t][2][e], v[t][3][e]}, inverse);
+    }
+    codes_out(lds, a.codes + at * kD * kD);
 }
 
 template <typename T>
@@ -217,7 +220,28 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
     const Place p;
     State v;
     const size_t at = (size_t)page * a.H + h;
-    read_state<T>(v, p, lds, &wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, (int64_t)at, window_count(a.win, b));
+    const int n = window_count(a.win, b);
+    // (several requests may read one page: no streaming loads, 281 us for 192 x 96 states against 297)
+    stage<T, false>(lds, wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, at, n);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+        const floatx4 m = *reinterpret_cast<const floatx4*>(lds.row + p.row(t));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const floatx4 x = values_of(lds.tile[(4 * p.l + e) * kLd + (p.row(t) >> 2)], m);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[t][r][e] = x[r];
+        }
+    }
+    for (int t = 0; t < n; ++t) {
+        const floatx4 u = *reinterpret_cast<const floatx4*>(&wl.u[t][4 * p.l]);
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const floatx4 k = *reinterpret_cast<const floatx4*>(&wl.k[t][p.row(b)]);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) v[b][r] += k[r] * u;
+        }
+    }
     float* S = a.S + (size_t)unit * kD * kD + 4 * p.l;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -226,6 +250,10 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
             __builtin_nontemporal_store(v[t][r], reinterpret_cast<floatx4*>(S + (p.row(t) + r) * kD));
 }
 
+// A fold holds its state as matrix tiles: wavefront w rows 32 w + 16 R + 4 g + 0..3
+// of column 16 T + l, so that the window's updates are products of 16 x 4 and 4 x 16
+// (exact fp32 factors), a row's largest magnitude lies in 16 lanes, and four rows'
+// codes of a column are one dword here, too.
 template <typename T>
 __global__ __launch_bounds__(256) void cache_fold_kernel(CacheMoveArgs a) {
     __shared__ __align__(16) union {
@@ -234,16 +262,49 @@ __global__ __launch_bounds__(256) void cache_fold_kernel(CacheMoveArgs a) {
     } lds;
     __shared__ __align__(16) WindowLds wl;
     const uint32_t unit = blockIdx.x;
-    const int b = (int)(unit / (uint32_t)a.H);
-    const int n = window_count(a.win, b);
+    const int n = window_count(a.win, (int)(unit / (uint32_t)a.H));
     if (n == 0) return;
-    const Place p;
-    State v;
     int8_t* codes = a.codes + (size_t)unit * kD * kD;
     float* scale = a.scale + (size_t)unit * kD;
-    read_state<T>(v, p, lds.in, &wl, codes, scale, a.win, unit, n);
+    stage<T, true>(lds.in, wl, codes, scale, a.win, unit, n);
+    const int l = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, row = threadIdx.x >> 6 << 5;
+    floatx4 v[2][8];
+#pragma unroll
+    for (int R = 0; R < 2; ++R) {
+        const floatx4 m = *reinterpret_cast<const floatx4*>(lds.in.row + row + 16 * R + 4 * g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) v[R][c] = values_of(lds.in.tile[(16 * c + l) * kLd + (row >> 2) + 4 * R + g], m);
+    }
+    for (int t = 0; t < n; t += 4) {
+        const float k0 = wl.k[t + g][row + l], k1 = wl.k[t + g][row + 16 + l];
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            const float u = wl.u[t + g][16 * c + l];
+            v[0][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(k0, u, v[0][c], 0, 0, 0);
+            v[1][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(k1, u, v[1][c], 0, 0, 0);
+        }
+    }
     __syncthreads();   // (what is read is read)
-    quantise(v, p, lds.out, codes, scale);
+#pragma unroll
+    for (int R = 0; R < 2; ++R) {
+        uint32_t m[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            m[r] = 0;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) m[r] = max(m[r], magnitude(v[R][c][r]));
+            m[r] = max16(m[r]);
+        }
+        if (l == 0) *reinterpret_cast<uintx4*>(lds.out.top + row + 16 * R + 4 * g) = uintx4{m[0], m[1], m[2], m[3]};
+    }
+    scales(lds.out, scale);
+#pragma unroll
+    for (int R = 0; R < 2; ++R) {
+        const floatx4 inverse = *reinterpret_cast<const floatx4*>(lds.out.inverse + row + 16 * R + 4 * g);
+#pragma unroll
+        for (int c = 0; c < 8; ++c) lds.out.tile[(16 * c + l) * kLd + (row >> 2) + 4 * R + g] = codes_of(v[R][c], inverse);
+    }
+    codes_out(lds.out, codes);
 }
 
 }  // namespace

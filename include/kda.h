@@ -538,9 +538,9 @@ kda_status kda_tree_commit(const void* k, const void* v, const void* log_alpha,
  *     codes : [.., H, Dv, Dk] int8   (value channel, then key channel)
  *     scale : [.., H, Dk] fp32       S[i][j] = scale[i] * codes[j][i],
  *
- * scale[i] = (largest |S[i][j]| over j) / 127 and codes[j][i] = S[i][j] *
- * (127 / largest) rounded to the nearest whole number, ties to even, each
- * operation in fp32: half a scale step off at the most.  A key channel without
+ * scale[i] = (largest |S[i][j]| over j) / 127 in fp32 and codes[j][i] = S[i][j]
+ * times (127 / largest, in fp32), the exact product rounded to the nearest whole
+ * number, ties to even: half a scale step off at the most.  A key channel without
  * a magnitude of 2^-100 or more is held as zeros; one with a NaN or an
  * infinity reads back as NaN.  The decay Diag(alpha) multiplies key channels,
  * so the scales take it up and the codes keep their bits.

@@ -16,14 +16,15 @@ HALF = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}   # half a step of the type (24 an
 
 def quantise(S):
     """float32 states [.., 128 (key), 128 (value)] -> codes [.., value, key]
-    int8 and scales [.., key] float32."""
+    int8 and scales [.., key] float32.  (The product of two 24-bit numbers is
+    exact in float64.)"""
     S = np.asarray(S, dtype=np.float32)
     top = np.abs(S).max(-1)
     held = top >= TINY
     with np.errstate(divide="ignore", over="ignore", invalid="ignore"):
         inverse = np.where(held, np.float32(127) / top, np.float32(0)).astype(np.float32)
         scale = np.where(held, top / np.float32(127), np.float32(0)).astype(np.float32)
-        codes = np.rint((S * inverse[..., None]).astype(np.float32)).astype(np.int8)
+        codes = np.rint(S.astype(np.float64) * inverse[..., None]).astype(np.int8)
     return np.swapaxes(codes, -1, -2), scale
 
 
