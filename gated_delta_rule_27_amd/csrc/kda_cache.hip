@@ -93,68 +93,81 @@ __device__ __forceinline__ void codes_out(const QuantiseLds& lds, int8_t* codes)
     }
 }
 
-// LDS of a state read back: codes; the keys as far as they are decayed after the
-// last token, the updates (rows of zeros up to a multiple of four), and what each
-// key channel's codes are multiplied by
-constexpr int kWinLd = kD + 16;   // (16 floats more: other banks)
+// LDS of a state read back: codes, and what each key channel's codes are multiplied
+// by; the window as it is in memory (rows of zeros up to a multiple of four tokens),
+// and its keys as far as they are decayed after the last token.  kMost: the longest
+// window of an instance.
 struct ReadLds {
     uint32_t tile[kD * kLd];
     float row[kD];
 };
+constexpr int kWinLd = kD + 16;   // (16 elements more: other banks)
+template <typename T, int kMost>
 struct WindowLds {
-    float k[kMaxWindow][kWinLd];
-    float u[kMaxWindow][kWinLd];
+    T raw[3][kMost][kWinLd];   // k, log alpha, u
+    float wide[sizeof(T) == 4 ? 1 : kMost][kWinLd];
+    // (of fp32 keys the decayed ones take the place)
+    __device__ __forceinline__ float* k(int t) { return sizeof(T) == 4 ? reinterpret_cast<float*>(raw[0][t]) : wide[t]; }
 };
 
 // codes, window and scales into LDS; all threads, a barrier at the end
-template <typename T, bool kStream>
-__device__ __forceinline__ void stage(ReadLds& lds, WindowLds& wl, const int8_t* codes, const float* scale, const CacheWindow& w,
-                                      size_t at, int n) {
-    uintx4 x[4];
+template <typename T, int kMost, bool kStream>
+__device__ __forceinline__ void stage(ReadLds& lds, WindowLds<T, kMost>& wl, const int8_t* codes, const float* scale,
+                                      const CacheWindow& w, size_t at, int n) {
+    constexpr int kRow = kD * sizeof(T) / 16;                     // pieces of 16 bytes of a row
+    constexpr int kPieces = (3 * kMost * kRow + 255) / 256;       // that a thread takes
+    const int most = (n + 3) & ~3, i = threadIdx.x & (kD - 1);
+    uintx4 x[4], y[kPieces];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const uintx4* p = reinterpret_cast<const uintx4*>(codes) + threadIdx.x + 256 * s;
         x[s] = kStream ? __builtin_nontemporal_load(p) : *p;
     }
-    const int i = threadIdx.x & (kD - 1), most = (n + 3) & ~3;
-    const size_t base = at * w.W * kD + i;
-    if (threadIdx.x < kD) {
-        const T* k = static_cast<const T*>(w.k) + base;
-        const T* la = static_cast<const T*>(w.log_alpha) + base;
-        const float sc = scale[i];
-        T kt[kMaxWindow], lt[kMaxWindow];
+    const float sc = scale[i];
+    // (token by token, its three rows one after the other)
+    auto piece = [&](int s, int& t, int& array, int& q) {
+        const int p = (int)threadIdx.x + 256 * s;
+        t = p / (3 * kRow);
+        array = p / kRow % 3;
+        q = p % kRow;
+    };
 #pragma unroll
-        for (int t = 0; t < kMaxWindow; ++t) {
-            if (t < n) {
-                kt[t] = k[t * kD];
-                lt[t] = la[t * kD];
-            }
+    for (int s = 0; s < kPieces; ++s) {
+        int t, array, q;
+        piece(s, t, array, q);
+        y[s] = uintx4{0, 0, 0, 0};
+        if (t < n) {
+            const void* p = array == 0 ? w.k : array == 1 ? w.log_alpha : w.u;
+            y[s] = reinterpret_cast<const uintx4*>(p)[(at * w.W + t) * kRow + q];
         }
-        float g = 0.f;
+    }
 #pragma unroll
-        for (int t = kMaxWindow - 1; t >= 0; --t) {
-            if (t < n) {
-                wl.k[t][i] = to_f32(kt[t]) * decay(g);
-                g += to_f32(lt[t]);
-            } else if (t < most) {
-                wl.k[t][i] = 0.f;
-            }
-        }
-        lds.row[i] = sc * decay(g);
-    } else {
-        const T* u = static_cast<const T*>(w.u) + base;
-        T ut[kMaxWindow];
-#pragma unroll
-        for (int t = 0; t < kMaxWindow; ++t)
-            if (t < n) ut[t] = u[t * kD];
-#pragma unroll
-        for (int t = 0; t < kMaxWindow; ++t)
-            if (t < most) wl.u[t][i] = t < n ? to_f32(ut[t]) : 0.f;
+    for (int s = 0; s < kPieces; ++s) {
+        int t, array, q;
+        piece(s, t, array, q);
+        if (t < most) *reinterpret_cast<uintx4*>(&wl.raw[array][t][q * (16 / sizeof(T))]) = y[s];
     }
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
-        const int piece = threadIdx.x + 256 * s;
-        *reinterpret_cast<uintx4*>(lds.tile + (piece >> 3) * kLd + 4 * (piece & 7)) = x[s];
+        const int q = threadIdx.x + 256 * s;
+        *reinterpret_cast<uintx4*>(lds.tile + (q >> 3) * kLd + 4 * (q & 7)) = x[s];
+    }
+    __syncthreads();
+    // a key channel's later tokens in one thread, its earlier ones in another
+    const int half = most / 2;
+    float g = 0.f;
+    if (threadIdx.x < kD) {
+        for (int t = most - 1; t >= half; --t) {
+            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
+            g += to_f32(wl.raw[1][t][i]);
+        }
+    } else {
+        for (int t = most - 1; t >= half; --t) g += to_f32(wl.raw[1][t][i]);
+        for (int t = half - 1; t >= 0; --t) {
+            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
+            g += to_f32(wl.raw[1][t][i]);
+        }
+        lds.row[i] = sc * decay(g);
     }
     __syncthreads();
 }
@@ -209,10 +222,10 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheMoveArgs a) {
     codes_out(lds, a.codes + at * kD * kD);
 }
 
-template <typename T>
+template <typename T, int kMost>
 __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
     __shared__ __align__(16) ReadLds lds;
-    __shared__ __align__(16) WindowLds wl;
+    __shared__ __align__(16) WindowLds<T, kMost> wl;
     const uint32_t unit = blockIdx.x;
     const int b = (int)(unit / (uint32_t)a.H), h = (int)(unit % (uint32_t)a.H);
     const int page = a.page ? a.page[b] : b;
@@ -222,7 +235,7 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
     const size_t at = (size_t)page * a.H + h;
     const int n = window_count(a.win, b);
     // (several requests may read one page: no streaming loads, 281 us for 192 x 96 states against 297)
-    stage<T, false>(lds, wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, at, n);
+    stage<T, kMost, false>(lds, wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, at, n);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const floatx4 m = *reinterpret_cast<const floatx4*>(lds.row + p.row(t));
@@ -234,10 +247,12 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
         }
     }
     for (int t = 0; t < n; ++t) {
-        const floatx4 u = *reinterpret_cast<const floatx4*>(&wl.u[t][4 * p.l]);
+        floatx4 u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[e] = to_f32(wl.raw[2][t][4 * p.l + e]);
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
-            const floatx4 k = *reinterpret_cast<const floatx4*>(&wl.k[t][p.row(b)]);
+            const floatx4 k = *reinterpret_cast<const floatx4*>(wl.k(t) + p.row(b));
 #pragma unroll
             for (int r = 0; r < 4; ++r) v[b][r] += k[r] * u;
         }
@@ -254,19 +269,19 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
 // of column 16 T + l, so that the window's updates are products of 16 x 4 and 4 x 16
 // (exact fp32 factors), a row's largest magnitude lies in 16 lanes, and four rows'
 // codes of a column are one dword here, too.
-template <typename T>
-__global__ __launch_bounds__(256) void cache_fold_kernel(CacheMoveArgs a) {
+template <typename T, int kMost>
+__global__ __launch_bounds__(256, sizeof(T) * kMost <= 16 ? 5 : sizeof(T) * kMost <= 32 ? 4 : 2) void cache_fold_kernel(CacheMoveArgs a) {
     __shared__ __align__(16) union {
         ReadLds in;
         QuantiseLds out;
     } lds;
-    __shared__ __align__(16) WindowLds wl;
+    __shared__ __align__(16) WindowLds<T, kMost> wl;
     const uint32_t unit = blockIdx.x;
     const int n = window_count(a.win, (int)(unit / (uint32_t)a.H));
     if (n == 0) return;
     int8_t* codes = a.codes + (size_t)unit * kD * kD;
     float* scale = a.scale + (size_t)unit * kD;
-    stage<T, true>(lds.in, wl, codes, scale, a.win, unit, n);
+    stage<T, kMost, true>(lds.in, wl, codes, scale, a.win, unit, n);
     const int l = threadIdx.x & 15, g = threadIdx.x >> 4 & 3, row = threadIdx.x >> 6 << 5;
     floatx4 v[2][8];
 #pragma unroll
@@ -276,10 +291,10 @@ __global__ __launch_bounds__(256) void cache_fold_kernel(CacheMoveArgs a) {
         for (int c = 0; c < 8; ++c) v[R][c] = values_of(lds.in.tile[(16 * c + l) * kLd + (row >> 2) + 4 * R + g], m);
     }
     for (int t = 0; t < n; t += 4) {
-        const float k0 = wl.k[t + g][row + l], k1 = wl.k[t + g][row + 16 + l];
+        const float k0 = wl.k(t + g)[row + l], k1 = wl.k(t + g)[row + 16 + l];
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
-            const float u = wl.u[t + g][16 * c + l];
+            const float u = to_f32(wl.raw[2][t + g][16 * c + l]);
             v[0][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(k0, u, v[0][c], 0, 0, 0);
             v[1][c] = __builtin_amdgcn_mfma_f32_16x16x4f32(k1, u, v[1][c], 0, 0, 0);
         }
@@ -316,15 +331,26 @@ hipError_t launch_cache_store(const CacheMoveArgs& a, hipStream_t stream) {
 
 hipError_t launch_cache_load(const CacheMoveArgs& a, int dtype, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
-    if (dtype == 0) cache_load_kernel<float><<<grid, block, 0, stream>>>(a);
-    else cache_load_kernel<bf16><<<grid, block, 0, stream>>>(a);
+    const bool few = !a.win.k || a.win.W <= 8;
+    if (dtype == 0) {
+        if (few) cache_load_kernel<float, 8><<<grid, block, 0, stream>>>(a);
+        else cache_load_kernel<float, kMaxWindow><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (few) cache_load_kernel<bf16, 8><<<grid, block, 0, stream>>>(a);
+        else cache_load_kernel<bf16, kMaxWindow><<<grid, block, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_cache_fold(const CacheMoveArgs& a, int dtype, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
-    if (dtype == 0) cache_fold_kernel<float><<<grid, block, 0, stream>>>(a);
-    else cache_fold_kernel<bf16><<<grid, block, 0, stream>>>(a);
+    if (dtype == 0) {
+        if (a.win.W <= 8) cache_fold_kernel<float, 8><<<grid, block, 0, stream>>>(a);
+        else cache_fold_kernel<float, kMaxWindow><<<grid, block, 0, stream>>>(a);
+    } else {
+        if (a.win.W <= 8) cache_fold_kernel<bf16, 8><<<grid, block, 0, stream>>>(a);
+        else cache_fold_kernel<bf16, kMaxWindow><<<grid, block, 0, stream>>>(a);
+    }
     return hipGetLastError();
 }
 

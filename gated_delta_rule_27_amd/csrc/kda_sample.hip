@@ -224,6 +224,11 @@ struct RowLds {
     float part_f[3][kWaves];
     Entry few[64];
     float ring[kWaves][128];   // weights to be, on their way
+    // the row
+    const void* logits;
+    double scale, unit;
+    float top;
+    int V;
     // what one thread tells the others
     uint64_t total_w, before_w, key, key_w, kept_w, above_w;
     uint32_t total_n, before_n, here_n, n, key_n;
@@ -461,6 +466,16 @@ __device__ __noinline__ bool overflows(const __attribute__((address_space(3))) f
     return -(float)count * __logf(__builtin_fmaxf(1.f - share, 1.f / (float)(4 * count))) > 1.25f * kCap && count * tokens > kCap;
 }
 
+template <typename V>
+__device__ __forceinline__ V uniform(V x) {
+    uint32_t w[sizeof(V) / 4];
+    __builtin_memcpy(w, &x, sizeof(V));
+#pragma unroll
+    for (uint32_t& y : w) y = (uint32_t)__builtin_amdgcn_readfirstlane((int)y);
+    __builtin_memcpy(&x, w, sizeof(V));
+    return x;
+}
+
 template <typename T>
 struct Row {
     const T* logits;
@@ -469,6 +484,21 @@ struct Row {
     double scale;
     double unit;         // 2^F, F <= 50: what sums are counted in is 2^-F
     int lane, wave;
+
+    // the row of this workgroup, from LDS
+    static __device__ __forceinline__ Row here() {
+        KDA_ROW_LDS;
+        Row r;
+        r.logits = static_cast<const T*>(uniform(l.logits));
+        r.V = uniform(l.V);
+        r.tiles = (r.V + kTile - 1) / kTile;
+        r.top = uniform(l.top);
+        r.scale = uniform(l.scale);
+        r.unit = uniform(l.unit);
+        r.lane = threadIdx.x & 63;
+        r.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+        return r;
+    }
 
     __device__ __forceinline__ uint64_t* sums() const {    // [tiles], weights of what is kept
         return reinterpret_cast<uint64_t*>(row_memory + kRowBytes);
@@ -554,7 +584,7 @@ struct Row {
         return n;
     }
     // every token of logit > below to the list
-    __device__ __noinline__ uint32_t gather(float below, bool by_group) const {
+    __device__ __forceinline__ uint32_t gather(float below, bool by_group) const {
         KDA_ROW_LDS;
         constexpr int M = Tile<T>::M;
         start_list();
@@ -655,7 +685,7 @@ struct Row {
     // weigh.  If it can be found within a few bins, sums then holds each tile's weight
     // of what is kept if it ends there and weighs `least`, and l.key_w the weights up
     // to there.  False if not: it may be there all the same.
-    __device__ __noinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+    __device__ __forceinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
                                            double low, double least) const {
         KDA_ROW_LDS;
         const Bins bin_of(top, scale, high, low);
@@ -736,7 +766,7 @@ struct Row {
     // The same wherever it lies, without the sums: a histogram of the weights
     // themselves, and as many levels inside one bin as it takes (thousands of equal
     // logits, a distribution that fits no bins).
-    __device__ __noinline__ bool find_far(bool by_count, uint64_t target) const {
+    __device__ __forceinline__ bool find_far(bool by_count, uint64_t target) const {
         KDA_ROW_LDS;
         uint32_t base_n = 0, here = kCap + 1;
         uint64_t base_w = 0, lo = 1, hi = place(top, 0);
@@ -782,7 +812,7 @@ struct Row {
         return true;
     }
     // each tile's weight of what is kept
-    __device__ __noinline__ void sum_kept(uint64_t cut, double least) const {
+    __device__ __forceinline__ void sum_kept(uint64_t cut, double least) const {
         for (int t = threadIdx.x; t < tiles; t += kThreads) sums()[t] = 0;
         __syncthreads();
         const float from = cut > 1 ? logit_of(cut) : minus_inf(), below = cut > 1 ? under(from) : from;
@@ -854,6 +884,70 @@ struct Row {
 };
 
 template <typename T>
+__device__ __noinline__ uint32_t gather(float below, bool by_group) { return Row<T>::here().gather(below, by_group); }
+template <typename T>
+__device__ __noinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+                                       double low, double least) {
+    return Row<T>::here().find_near(by_count, target, above, off, below, high, low, least);
+}
+template <typename T>
+__device__ __noinline__ bool find_far(bool by_count, uint64_t target) { return Row<T>::here().find_far(by_count, target); }
+
+// the weight that top-p asks for, of that of what it is taken from
+__device__ __forceinline__ uint64_t share_of(double p, uint64_t w) {
+    const double x = __builtin_ceil(p * (double)w);
+    return x < 1.0 ? (uint64_t)1 : (uint64_t)x;
+}
+
+// What is kept where no list holds it, from the row's tiles: the last place, and the
+// sum, with each tile's in sums.  `all`: the weights of all tokens; `listed_w`, not 0:
+// of those of logit > listed_over, which are less than top-p asks for.
+struct Kept {
+    uint64_t cut, sum;
+};
+template <typename T>
+__device__ __noinline__ Kept over_row(int k, bool by_p, double p, double least, uint64_t all, float listed_over, uint64_t listed_w) {
+    KDA_ROW_LDS;
+    const Row<T> r = Row<T>::here();
+    __syncthreads();
+    uint64_t cut = 1, sum = all;
+    bool summed = false;
+    if (k) {
+        summed = find_near<T>(true, (uint64_t)k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, least);
+        const bool ok = summed || find_far<T>(true, (uint64_t)k);
+        if (ok) cut = l.key;
+        sum = ok ? l.key_w : l.total_w;
+        __syncthreads();
+        summed = summed && !by_p;
+    }
+    if (by_p) {
+        // the last one kept weighs at least (what lies behind it) / V; where the list did not reach the share, it
+        // lies below
+        const uint64_t target = share_of(p, sum);
+        const double behind = ((double)sum - (double)target) / ((double)r.V * r.unit);
+        double bottom = behind > 0.0 ? log2(behind) - 0.01 : -66.4;
+        bottom = bottom < -66.4 ? -66.4 : bottom;
+        float above = __builtin_inff();
+        double high = 0.0;
+        if (listed_w && listed_w < target) {
+            above = of_key(key_of(listed_over) + 1);
+            high = ((double)above - (double)r.top) * r.scale;
+        } else {
+            listed_w = 0;
+        }
+        if (!(high < 0.0)) high = 0.0;
+        if (bottom > high - 0.01) bottom = high - 0.01;
+        const double low_x = (double)r.top + bottom / r.scale;
+        const float from = !(low_x > -3e38) || r.top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
+        summed = find_near<T>(false, target, above, listed_w, from, high, bottom, least);
+        if (summed || find_far<T>(false, target)) cut = max(cut, l.key);
+        __syncthreads();
+    }
+    if (!summed) r.sum_kept(cut, least);
+    return Kept{cut, r.total()};
+}
+
+template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     KDA_ROW_LDS;
     const int64_t row = blockIdx.x;
@@ -904,6 +998,14 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     r.scale = ask.scale;
     const int bits = 32 - __builtin_clz((uint32_t)V);   // V < 2^bits
     r.unit = __builtin_ldexp(1.0, min(62 - bits, 50));
+    if (threadIdx.x == 0) {
+        l.logits = r.logits;
+        l.scale = r.scale;
+        l.unit = r.unit;
+        l.top = top;
+        l.V = V;
+    }
+    __syncthreads();
 
     SampleRow out;
     out.scale = ask.scale;
@@ -965,10 +1067,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         bool sure = false, done = false;
         uint32_t n = kCap + 1;
         uint64_t listed_w = 0;
-        auto share = [&](uint64_t w) {   // the weight that top-p asks for
-            const double x = __builtin_ceil(ask.p * (double)w);
-            return x < 1.0 ? (uint64_t)1 : (uint64_t)x;
-        };
+        auto share = [&](uint64_t w) { return share_of(ask.p, w); };
         for (int attempt = 0;; ++attempt) {
             below = top;   // (none)
             sure = V <= (int)kCap;
@@ -998,7 +1097,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 done = false;
                 break;
             }
-            n = r.gather(below, by_group);
+            n = gather<T>(below, by_group);
             listed_over = below;
             done = n <= kCap;
             cut = 1;
@@ -1086,43 +1185,10 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
             if (done) break;
         }
         if (!done) {
-            // over the row
-            __syncthreads();
-            cut = 1;
-            bool summed = false;
-            if (ask.by_k) {
-                summed = r.find_near(true, ask.k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, ask.least);
-                const bool ok = summed || r.find_far(true, ask.k);
-                if (ok) cut = l.key;
-                sum = ok ? l.key_w : l.total_w;
-                __syncthreads();
-                summed = summed && !ask.by_p;
-            }
-            if (ask.by_p) {
-                // the last one kept weighs at least (what lies behind it) / V; where the list holds all above `below`
-                // and did not reach the share, it lies there or below
-                const uint64_t target = share(sum);
-                const double behind = ((double)sum - (double)target) / ((double)V * r.unit);
-                double bottom = behind > 0.0 ? log2(behind) - 0.01 : -66.4;
-                bottom = bottom < -66.4 ? -66.4 : bottom;
-                float above = __builtin_inff();
-                double high = 0.0;
-                uint64_t off = 0;
-                if (!ask.by_k && n <= kCap && listed_w < target) {
-                    above = of_key(key_of(listed_over) + 1);
-                    high = ((double)above - (double)top) * ask.scale;
-                    off = listed_w;
-                }
-                if (!(high < 0.0)) high = 0.0;
-                if (bottom > high - 0.01) bottom = high - 0.01;
-                const double low_x = (double)top + bottom / ask.scale;
-                const float from = !(low_x > -3e38) || top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
-                summed = r.find_near(false, target, above, off, from, high, bottom, ask.least);
-                if (summed || r.find_far(false, target)) cut = max(cut, l.key);
-                __syncthreads();
-            }
-            if (!summed) r.sum_kept(cut, ask.least);
-            sum = r.total();
+            const Kept found = over_row<T>(ask.by_k ? ask.k : 0, ask.by_p, ask.p, ask.least, all, listed_over,
+                                           n <= kCap && !ask.by_k ? listed_w : 0);
+            cut = found.cut;
+            sum = found.sum;
         }
         out.cut = cut;
         out.least = ask.least;
