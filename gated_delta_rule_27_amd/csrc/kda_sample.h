@@ -31,8 +31,8 @@ constexpr int kSampleGroups = 16;   // of a tile: 64 tokens each
 // the sum of its weights; then what the last pass needs of each row.
 struct SampleRow {
     double scale;      // log2(e) / temperature
-    double per;        // 1 / (sum of the weights that are kept)
-    double least;      // smallest weight that is kept
+    double sum;        // log2 of the sum of the weights that are kept
+    double least;      // smallest weight that is kept, where the cut is not all
     uint64_t cut;      // last place in the order that is kept
     float top;         // largest logit; -infinity: nothing is kept
     int32_t pad;
@@ -52,8 +52,10 @@ __host__ __device__ inline SampleSections sample_sections(int32_t R, int64_t til
     return s;
 }
 inline size_t sample_workspace(int32_t R, int32_t V) { return (size_t)sample_sections(R, sample_tiles(V)).end; }
-// workgroups of the passes over tiles: four tiles each
-inline int64_t sample_groups(int32_t R, int32_t V) { return (int64_t)R * ((sample_tiles(V) + 3) / 4); }
+// workgroups a row of the last pass, and the most of a pass: four tiles each, the
+// last pass's up to 7 tokens ahead of the row
+__host__ __device__ inline int64_t sample_row_groups(int32_t V) { return ((int64_t)V + 7 + 4 * kSampleTile - 1) / (4 * kSampleTile); }
+inline int64_t sample_groups(int32_t R, int32_t V) { return R * sample_row_groups(V); }
 
 // dtype: 0 = fp32, 1 = bf16 (kda_dtype values)
 hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream);

@@ -96,6 +96,15 @@ __device__ __forceinline__ double weight(float x, float top, double scale) {
     return y > -1020.0 ? w : 0.0;
 }
 
+// 2^y for y <= 0 in fp32, of a y in 64 bits: its whole part is exact, and 2^f, |f| <=
+// 1/2, the hardware's (an ulp off at most)
+__device__ __forceinline__ float exp2_f32(double y) {
+    const double round = 6755399441055744.0;
+    y = __builtin_fmax(y, -1020.0);
+    const double t = y + round;
+    return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(y - (t - round))), (int)__builtin_bit_cast(uint64_t, t));
+}
+
 // what a row is asked for
 struct Ask {
     double scale, p, least;
@@ -1009,7 +1018,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
 
     SampleRow out;
     out.scale = ask.scale;
-    out.per = 1.0;
+    out.sum = 0.0;
     out.least = 0.0;
     out.cut = 1;
     out.top = top;
@@ -1113,6 +1122,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                     l.key = 0;
                     l.key_w = 0;
                     l.kept_w = 0;
+                    l.above_w = ~(uint64_t)0;   // the last place that is kept
                 }
                 __syncthreads();
                 if (e < n && rank == (ask.by_k ? min(n, (uint32_t)ask.k) : n)) {
@@ -1136,7 +1146,10 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 if (done) {
                     const bool kept = e < n && mine.place >= cut && (!ask.by_m || r.weight_of(logit_of(mine.place)) >= ask.least);
                     if (e < n && !kept) l.list[e].w = 0;
-                    if (kept) atomicMax(reinterpret_cast<unsigned long long*>(&l.kept_w), (unsigned long long)run);
+                    if (kept) {
+                        atomicMax(reinterpret_cast<unsigned long long*>(&l.kept_w), (unsigned long long)run);
+                        if (ask.by_m) atomicMin(reinterpret_cast<unsigned long long*>(&l.above_w), (unsigned long long)mine.place);
+                    }
                     if (a.u) {
                         count_pairs(n, true);   // (its first barrier is one for what is above, too)
                         sum = l.kept_w;
@@ -1145,6 +1158,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                     }
                     __syncthreads();
                     sum = l.kept_w;
+                    if (ask.by_m) cut = l.above_w;
                     drawn = true;
                 }
             } else {
@@ -1164,15 +1178,24 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                     __syncthreads();
                 }
                 if (done) {
-                    uint64_t s = 0;
+                    uint64_t s = 0, end = ~(uint64_t)0;   // the last place that is kept
+                    if (threadIdx.x == 0) l.above_w = end;
+                    __syncthreads();
                     for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
-                        if (l.list[i].place < cut || (ask.by_m && r.weight_of(logit_of(l.list[i].place)) < ask.least)) l.list[i].w = 0;
-                        s += l.list[i].w;
+                        const Entry x = l.list[i];
+                        if (x.place < cut || (ask.by_m && r.weight_of(logit_of(x.place)) < ask.least)) {
+                            l.list[i].w = 0;
+                        } else {
+                            s += x.w;
+                            end = min(end, x.place);
+                        }
                     }
+                    if (ask.by_m) atomicMin(reinterpret_cast<unsigned long long*>(&l.above_w), (unsigned long long)end);
                     s = wave_scan_whole(s);
                     if (r.lane == 63) l.part_w[r.wave] = s;
                     __syncthreads();
                     sum = lane_value(wave_scan_whole(r.lane < kWaves ? l.part_w[r.lane] : (uint64_t)0), kWaves - 1);
+                    if (ask.by_m) cut = l.above_w;
                     __syncthreads();
                     if (a.u) {
                         find(kByIndex, n, kIndexMask + 2 - V, kIndexMask + 1, false, min((uint64_t)(u * (double)sum) + 1, sum));
@@ -1191,61 +1214,76 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
             sum = found.sum;
         }
         out.cut = cut;
-        out.least = ask.least;
+        if (!drawn) out.least = ask.least;   // (else the cut has it)
     }
     if (a.u && !drawn) r.draw(min((uint64_t)(u * (double)sum) + 1, sum), out.cut, out.least);
     if (threadIdx.x == 0) {
         if (a.u) a.token[row] = l.token;
-        out.per = r.unit / (double)sum;
+        if (a.probs) out.sum = log2((double)sum / r.unit);
         *to = out;
     }
 }
 
 // ---- probabilities -----------------------------------------------------------
 
+// Tiles that begin at a multiple of 16 bytes, whichever token that is: a row of an odd
+// vocabulary is written (and read) by whole pieces but for its ends (192 x 50,021 bf16:
+// 13 us at the tokens' own places).
 template <typename T>
 __global__ __launch_bounds__(256) void sample_probs_kernel(SampleArgs a) {
-    constexpr int M = Tile<T>::M;
+    constexpr int M = Tile<T>::M, J = Tile<T>::J;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int tiles = (a.V + kTile - 1) / kTile;
-    const uint32_t per_row = (uint32_t)(tiles + 3) / 4;
+    const uint32_t per_row = (uint32_t)sample_row_groups(a.V);
     const uint32_t row = blockIdx.x / per_row;
-    const int t = (int)(blockIdx.x % per_row) * 4 + wave;
-    if (t >= tiles) return;
+    const int tiles = (a.V + kTile - 1) / kTile, t = (int)(blockIdx.x % per_row) * 4 + wave;
+    const size_t begin = (size_t)row * a.V;
+    const int ahead = (int)(begin % M), v0 = t * kTile - ahead;   // tokens before the row in its first piece
+    if (v0 >= a.V) return;
     const SampleSections at = sample_sections(a.R, tiles);
     const SampleRow r = reinterpret_cast<const SampleRow*>(a.workspace + at.rows)[row];
-    const float m = reinterpret_cast<const float*>(a.workspace + at.tops)[(size_t)row * tiles + t];
-    T* probs = static_cast<T*>(a.probs) + (size_t)row * a.V;
-    typename Vec16<T>::type y[Tile<T>::J];
-    if (m > minus_inf() && ((uint64_t)key_of(m) << kIndexBits | kIndexMask) >= r.cut && weight(m, r.top, r.scale) >= r.least) {
-        Tile<T> x;
-        x.load(static_cast<const T*>(a.logits) + (size_t)row * a.V, t, a.V, lane);
+    const float* tops = reinterpret_cast<const float*>(a.workspace + at.tops) + (size_t)row * tiles;
+    const float m = __builtin_fmaxf(tops[max(t - 1, 0)], tops[min(t, tiles - 1)]);
+    const T* logits = static_cast<const T*>(a.logits) + begin;
+    T* probs = static_cast<T*>(a.probs) + begin;
+    typedef typename Vec16<T>::type vec;
+    const bool some = m > minus_inf() && ((uint64_t)key_of(m) << kIndexBits | kIndexMask) >= r.cut && weight(m, r.top, r.scale) >= r.least;
+    const bool inner = v0 >= 0 && v0 + kTile <= a.V;
+    vec x[J];
+    if (some) {
 #pragma unroll
-        for (int j = 0; j < Tile<T>::J; ++j)
+        for (int j = 0; j < J; ++j) {
+            const int v = v0 + (j * 64 + lane) * M;
+            if (inner) {
+                x[j] = *reinterpret_cast<const vec*>(logits + v);
+            } else {
 #pragma unroll
-            for (int e = 0; e < M; ++e) {
-                const float l = __builtin_fmaxf(to_f32((T)x.v[j][e]), minus_inf());
-                const int v = t * kTile + (j * 64 + lane) * M + e;
-                double w = 0.0;
-                if (l > minus_inf() && place(l, min(v, a.V - 1)) >= r.cut) w = weight(l, r.top, r.scale);
-                y[j][e] = from_f32<T>(w >= r.least ? (float)(w * r.per) : 0.f);
+                for (int e = 0; e < M; ++e) x[j][e] = logits[min(max(v + e, 0), a.V - 1)];
             }
-    } else {
-#pragma unroll
-        for (int j = 0; j < Tile<T>::J; ++j)
-#pragma unroll
-            for (int e = 0; e < M; ++e) y[j][e] = (T)0.f;
+        }
     }
 #pragma unroll
-    for (int j = 0; j < Tile<T>::J; ++j) {
-        const int v = t * kTile + (j * 64 + lane) * M;
-        if (v + M <= a.V) {
-            __builtin_memcpy(probs + v, &y[j], 16);
+    for (int j = 0; j < J; ++j) {
+        const int v = v0 + (j * 64 + lane) * M;
+        vec y;
+#pragma unroll
+        for (int e = 0; e < M; ++e) {
+            y[e] = (T)0.f;
+            if (some) {
+                const float l = to_f32((T)x[j][e]);
+                bool kept = l > minus_inf() && place(l, min(max(v + e, 0), a.V - 1)) >= r.cut;
+                if (r.least > 0.0) kept = kept && weight(l, r.top, r.scale) >= r.least;
+                // (one power of two for the weight over the sum)
+                const double y0 = l == r.top ? 0.0 : ((double)l - (double)r.top) * r.scale;
+                y[e] = from_f32<T>(kept ? exp2_f32(y0 - r.sum) : 0.f);
+            }
+        }
+        if (inner) {
+            *reinterpret_cast<vec*>(probs + v) = y;
         } else {
 #pragma unroll
             for (int e = 0; e < M; ++e)
-                if (v + e < a.V) probs[v + e] = y[j][e];
+                if (v + e >= 0 && v + e < a.V) probs[v + e] = y[e];
         }
     }
 }
@@ -1259,10 +1297,11 @@ hipError_t launch_sample_t(const SampleArgs& a, hipStream_t stream) {
     const int most = kRowBytes + (int)sample_tiles(KDA_MAX_VOCAB) * 12;
     const hipError_t e = raise_lds_limit_once(reinterpret_cast<const void*>(sample_rows_kernel<T>), most, done);
     if (e != hipSuccess) return e;
-    const dim3 grid((unsigned)sample_groups(a.R, a.V)), block(256);
+    const dim3 grid((unsigned)(a.R * ((tiles + 3) / 4))), block(256);
     sample_tiles_kernel<T><<<grid, block, 0, stream>>>(a);
     sample_rows_kernel<T><<<dim3((unsigned)a.R), dim3(kThreads), kRowBytes + (size_t)tiles * (tiles <= kGroupTiles ? 12 + 4 * kSampleGroups : 12), stream>>>(a);
-    if (a.probs) sample_probs_kernel<T><<<grid, block, 0, stream>>>(a);
+    if (a.probs)
+        sample_probs_kernel<T><<<dim3((unsigned)(a.R * sample_row_groups(a.V))), block, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -57,7 +57,7 @@ def test_workspace_size(L):
 
 def test_the_largest_calls_get_past_the_shapes(L):
     assert call(L.kda_sample, SAMPLE, dict(R=(1 << 22) - 1, V=1, token=P(1))) == ALIAS
-    assert call(L.kda_sample, SAMPLE, dict(R=(1 << 14) - 1, V=1 << 22, token=P(1))) == ALIAS
+    assert call(L.kda_sample, SAMPLE, dict(R=((1 << 24) - 1) // 1025, V=1 << 22, token=P(1))) == ALIAS
 
 
 def test_binding_refuses():
