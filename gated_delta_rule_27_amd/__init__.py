@@ -883,16 +883,16 @@ def _pages(codes):
     return codes.shape[0], codes.shape[1], gpu
 
 
-def _window(window, P, H, gpu, dt=None):
-    """Addresses, length and dtype of a window (k, log_alpha, u)."""
-    if len(window) != 3:
+_WINDOW = ("window[0]", "window[1]", "window[2]")
+
+
+def _window(window, P, H, gpu):
+    """Addresses, length and dtype code of a window (k, log_alpha, u)."""
+    if len(window) != 3 or window[0] is None or window[1] is None or window[2] is None:
         raise ValueError("window must be (k, log_alpha, u)")
-    if window[0] is None or window[1] is None or window[2] is None:
-        raise ValueError("window must be (k, log_alpha, u)")
-    shape, own, _, code = _first(window[0], "window", 4)
+    shape, dt, _, code = _first(window[0], "window[0]", 4)
     W = shape[2]
-    dt = own if dt is None else dt
-    return _need(("window",) * 3, window, (P, H, W, HEAD_DIM), dt, gpu), W, code
+    return _need(_WINDOW, window, (P, H, W, HEAD_DIM), dt, gpu), W, code
 
 
 def kda_cache_store(S, codes=None, scale=None, page=None):
@@ -930,7 +930,7 @@ def kda_cache_load(codes, scale, page=None, window=None, n_win=None, *, S=None):
     every page or as many as S has); window: (k, log_alpha, u), each [P, H, W, 128]
     bf16 or fp32, or None; n_win: int32 [B], the window's tokens to apply to
     each state (clamped to [0, W]), or None (W each).  Returns S [B, H, 128,
-    128] fp32."""
+    128] fp32 (where it is made here, states without a page are zeros)."""
     torch = _torch()
     P, H, gpu = _pages(codes)
     _required(scale=scale)
@@ -980,7 +980,10 @@ def kda_cache_decode(q, k, v, log_alpha, beta, codes, scale, window, n_win, *, o
     b = _one(beta, "beta", (B, H), dt, gpu)
     c = _one(codes, "codes", (B, H, D, D), torch.int8, gpu)
     sc = _one(scale, "scale", (B, H, D), torch.float32, gpu)
-    win, W, _ = _window(window, B, H, gpu, dt)
+    if len(window) != 3 or not isinstance(window[0], torch.Tensor) or window[0].dim() != 4:
+        raise ValueError("window must be (k, log_alpha, u), each [B, H, W, 128]")
+    W = window[0].shape[2]
+    win = _need(_WINDOW, window, (B, H, W, D), dt, gpu)
     count = _one(n_win, "n_win", (B,), torch.int32, gpu)
     if o is None:
         o = torch.empty_like(q)

@@ -458,10 +458,9 @@ __device__ __noinline__ float nth_maximum(const __attribute__((address_space(3))
     return logit_of(l.key);
 }
 
-// Whether the list will hardly hold the tokens of logit > below: of G groups with n
-// such tokens spread over them, G (1 - e^(-n / G)) have one at least.
-__device__ __noinline__ bool overflows(const __attribute__((address_space(3))) float* maxima, uint32_t count, uint32_t tokens,
-                                       float below) {
+// About how many tokens of logit > below there are: of G groups with n such tokens
+// spread over them, G (1 - e^(-n / G)) have one at least.
+__device__ __noinline__ float expected(const __attribute__((address_space(3))) float* maxima, uint32_t count, float below) {
     KDA_ROW_LDS;
     if (threadIdx.x == 0) l.n = 0;
     __syncthreads();
@@ -472,7 +471,7 @@ __device__ __noinline__ bool overflows(const __attribute__((address_space(3))) f
     __syncthreads();
     const float share = (float)l.n / (float)count;
     __syncthreads();
-    return -(float)count * __logf(__builtin_fmaxf(1.f - share, 1.f / (float)(4 * count))) > 1.25f * kCap && count * tokens > kCap;
+    return -(float)count * __logf(__builtin_fmaxf(1.f - share, 1.f / (float)(4 * count)));
 }
 
 template <typename V>
@@ -579,15 +578,16 @@ struct Row {
         if (threadIdx.x == 0) l.n = 0;
         __syncthreads();
     }
-    // after that, the list's places and weights; how many were named
-    __device__ __forceinline__ uint32_t listed() const {
+    // after that, the list's weights, and its places from indices where they are not
+    // there yet; how many were named
+    __device__ __forceinline__ uint32_t listed(bool placed = false) const {
         KDA_ROW_LDS;
         __syncthreads();
         const uint32_t n = l.n;
         for (uint32_t i = threadIdx.x; i < min(n, kCap); i += kThreads) {
-            const int v = (int)l.list[i].w;
-            const float x = logit(v);
-            l.list[i] = Entry{place(x, v), whole(weight_of(x))};
+            uint64_t at = l.list[i].place;
+            if (!placed) at = place(logit((int)l.list[i].w), (int)l.list[i].w);
+            l.list[i] = Entry{at, whole(weight_of(logit_of(at)))};
         }
         __syncthreads();
         return n;
@@ -629,12 +629,12 @@ struct Row {
 #pragma unroll
                 for (int q = 0; q < kAhead; ++q) {
                     const uint32_t to = at + rank_in(those[q]);
-                    if ((those[q] >> lane & 1) && to < kCap) l.list[to].w = (uint64_t)i[q];
+                    if ((those[q] >> lane & 1) && to < kCap) l.list[to].place = place(x[q], i[q]);
                     at += (uint32_t)__builtin_popcountll(those[q]);
                 }
             }
         }
-        return listed();
+        return listed(true);
     }
 
     // Sums over a tile of the weights of its tokens over `border`, through a ring that
@@ -1091,7 +1091,8 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                     sure = ask.by_k;
                 }
             }
-            if (floor > minus_inf() && (floor >= below || !(below < top))) {
+            // (min-p's bound where it comes first, or leaves a list about as short)
+            if (floor > minus_inf() && (floor >= below || !(below < top) || (attempt == 0 && !sure && expected(maxima, count, floor) < 600.f))) {
                 below = floor;
                 sure = true;
             }
@@ -1101,7 +1102,8 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 sure = true;
             }
             if (!(below < top)) break;
-            if (overflows(maxima, count, by_group ? kTile / kSampleGroups : kTile, below)) {
+            // (a fifth more than the list holds, if they are spread evenly: not even tried)
+            if (below == floor && V > (int)kCap && expected(maxima, count, below) > 1.2f * kCap) {
                 n = kCap + 1;
                 done = false;
                 break;

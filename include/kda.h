@@ -658,9 +658,10 @@ kda_status kda_cache_fold(int8_t* codes, float* scale, const void* win_k,
  * once.  The token drawn is the smallest kept i with
  *     (sum of the kept w over 0..i)  >  u * (sum of the kept w),
  * -1 where a row has no weight at all (its probabilities are then all 0).
- * Weights are e^x in 64 bits and sums hold 40 bits or more below the largest
- * weight, so a token is what 64-bit sums give unless a border lies within
- * about 1e-11 of them.  Results do not depend on the launch.
+ * Weights are e^x in 64 bits, added up as whole numbers of 2^-39 of the largest
+ * or less, so a token is what 64-bit sums give unless a border lies within about
+ * 1e-11 of them (for vocabularies of 160,000; 1e-9 for millions).  Results do not
+ * depend on the launch.
  *
  *   logits, probs : [R, V] dt;  probs NULL = not wanted
  *   u             : [R] fp32 in [0, 1) (clamped; NaN counts as 0); NULL = no

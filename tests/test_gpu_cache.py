@@ -359,3 +359,52 @@ def test_far_fp32_states_store_and_load():
     kda.kda_cache_load(codes, scale, S=S)
     torch.cuda.synchronize()
     assert torch.equal(S[B - 1], kda.kda_cache_load(*kda.kda_cache_store(part))[0]) and (S[0] == 0).all()
+
+
+def test_no_states_at_all():
+    kda = need_gpu()
+    case("B = 0")
+    H, W = 3, 4
+    codes, scale = kda.kda_cache_store(torch.zeros((0, H, D, D), device="cuda"))
+    win = tuple(torch.zeros((0, H, W, D), device="cuda") for _ in range(3))
+    n = torch.zeros(0, dtype=torch.int32, device="cuda")
+    x = torch.zeros((0, H, D), device="cuda")
+    assert kda.kda_cache_decode(x, x, x, x, torch.zeros((0, H), device="cuda"), codes, scale, win, n).shape == (0, H, D)
+    assert kda.kda_cache_load(codes, scale, None, win, n).shape == (0, H, D, D)
+    kda.kda_cache_fold(codes, scale, win, n)
+    full = kda.kda_cache_store(states(2, H, 1))
+    assert kda.kda_cache_load(*full, i32([])).shape == (0, H, D, D)
+    kda.kda_cache_store(torch.zeros((0, H, D, D), device="cuda"), *full, i32([]))
+    torch.cuda.synchronize()
+
+
+def test_the_binding_refuses_what_does_not_fit():
+    kda = need_gpu()
+    case("refusals with GPU tensors")
+    B, H, W = 2, 3, 4
+    codes, scale = kda.kda_cache_store(states(B, H, 1))
+    win = window(B, H, W, "bf16", 2)
+    q, k, v, la, beta = token(B, H, "bf16", 3)
+    n = i32([0, 1])
+    call = lambda **kw: kda.kda_cache_decode(**dict(dict(  # noqa: E731
+        q=q, k=k, v=v, log_alpha=la, beta=beta, codes=codes, scale=scale, window=win, n_win=n), **kw))
+    for kw, what in ((dict(k=k.float()), TypeError), (dict(codes=codes[:1]), ValueError), (dict(scale=scale.double()), TypeError),
+                     (dict(window=win[:2]), ValueError), (dict(window=(win[0], win[1], win[2].float())), TypeError),
+                     (dict(window=tuple(x.transpose(0, 1) for x in win)), ValueError), (dict(n_win=n.long()), TypeError),
+                     (dict(n_win=n.cpu()), ValueError), (dict(q=q.transpose(0, 1)), ValueError),
+                     (dict(codes=codes.transpose(2, 3)), ValueError), (dict(o=q), kda.KDAError),
+                     (dict(window=(win[0], win[0], win[2])), kda.KDAError)):
+        with pytest.raises(what):
+            call(**kw)
+    big = tuple(torch.zeros((B, H, 17, D), dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    with pytest.raises(kda.KDAError):
+        call(window=big)
+    with pytest.raises(ValueError):
+        kda.kda_cache_load(codes, scale, None, None, n)
+    with pytest.raises(TypeError):
+        kda.kda_cache_store(states(1, H, 1), codes)
+    with pytest.raises(TypeError):
+        kda.kda_cache_store(states(1, H, 1).bfloat16())
+    with pytest.raises(kda.KDAError):
+        kda.kda_cache_store(states(3, H, 1), codes, scale)      # (three states, two pages)
+    torch.cuda.synchronize()

@@ -1,11 +1,14 @@
 """Sampling on the GPU against a sorted row in extended precision.
 
-Tokens are equal wherever the oracle's nearest border lies further than 1e-11
-from the random number (weights hold 40 bits or more below the largest, so a sum
-of n of them is off by at most n / 2 of 2^-(62 - bits(V)) of it: 2^-40 for a
-whole row); the inputs here are checked to be such.  Probabilities are within
-4 * 2^-24 of themselves and half a step of their type (the weight's double, its
-quotient, one rounding to fp32, one to bf16)."""
+Tokens are equal wherever the oracle's nearest border lies further than `slack`
+from the random number.  Weights are rounded to 2^-F of the largest, F = 62 minus
+the vocabulary's bits (50 at most): a sum of V of them, each off by a random half
+of that at most, is off by some sqrt(V / 12) 2^-F, 7e-12 at 160,000 tokens and 1e-9
+at four million; the inputs here are checked to lie further away.  Probabilities
+are within 4.5 * 2^-24 of themselves and half a step of their type (2^f by the
+hardware, an ulp or 2 * 2^-24; its argument's rounding, 0.35 * 2^-24; one rounding to
+the type, beside fp32's for bf16).
+"""
 import numpy as np
 import pytest
 import torch
@@ -45,7 +48,7 @@ def check(kda, logits, u, T=None, k=None, p=None, m=None, slack=1e-11):
         assert tok[r] == t, f"row {r}: token {tok[r]}, {t} expected (border {margin:.1e} away)"
         off = np.abs(got[r] - pr)
         # (below the smallest normal number of the type a step is absolute)
-        ok = off <= (4 * 2.0 ** -24 + half) * pr + 2.0 ** -126
+        ok = off <= (4.5 * 2.0 ** -24 + half) * pr + 2.0 ** -126
         assert ok.all(), f"row {r}: probability {got[r][~ok][:3]} at {np.nonzero(~ok)[0][:3]}, {pr[~ok][:3]} expected"
         assert ((got[r] > 0) <= (pr > 0)).all()
     return tok
@@ -103,6 +106,20 @@ def test_large_vocabularies(V, dtype, kind):
     check(kda, x, u, T, [0, 200, 0, 20000, 0, 17], [0.9, 1.0, 0.95, 0.99, 0.8, 1.0], [0.1, 0.01, 1e-4, 1e-7, 0.02, 0.9])
     check(kda, x, u, T, None, None, [0.1, 0.01, 1e-4, 1e-7, 0.02, 0.9])
     check(kda, x, u, T, [5000] * R, None, [0.1, 0.01, 1e-4, 1e-7, 0.02, 0.9])
+
+
+@pytest.mark.parametrize("V,dtype,kind", [(524288, "bf16", "normal"), (524289, "f32", "peaked"), (1 << 22, "bf16", "normal")])
+def test_the_largest_vocabularies(V, dtype, kind):
+    """Around the most tiles whose groups' maxima are kept, and the most tokens."""
+    kda = need_gpu()
+    R = 2
+    case(f"sample V={V} {dtype} {kind}")
+    x, u = rows(R, V, dtype, 50, kind), uniform(R, 51)
+    T = [0.7, 1.2]
+    check(kda, x, u, T, slack=1e-8)
+    check(kda, x, u, T, [3000, 40], [0.9, 0.8], slack=1e-8)
+    check(kda, x, u, T, None, [0.9, 0.4], slack=1e-8)
+    check(kda, x, u, T, [0, V // 3], [0.6, 1.0], [0.01, 1e-5], slack=1e-8)
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
