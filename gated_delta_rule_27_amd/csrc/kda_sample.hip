@@ -16,10 +16,10 @@
 // nuclei.  Their tokens over such a bound go to a list in LDS, and everything is
 // decided there: a short one by counting, for each token, those before it; a
 // longer one by histograms of 1024 bins, each level inside one bin of the last.
-// Where the list overflows, or turns out not to hold the nucleus, the row's tiles
-// are read twice more: once to count their tokens in bins, from which follows
-// where the last kept one lies, within a few bins; once to collect those bins and
-// to sum each tile's weight above them, which shows that it does.
+// Where the list overflows, or turns out not to hold the nucleus, some or all of the
+// row's tiles are read to count their tokens in bins, from which follows where the
+// last kept one lies, within some bins; and all of them once more to collect those
+// bins and to sum each tile's weight above them, which shows that it does.
 // Weights are taken in 64 bits and added up as whole numbers of 2^-F: their sums
 // are the same in any order, and the drawn token is a whole number, too, which a
 // rounding of a running sum must not move.
@@ -37,6 +37,8 @@ constexpr int kPer = kTile / 64;
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = kThreads;
 constexpr uint32_t kCap = 2048;        // tokens of the list
+constexpr uint32_t kDense = 96;        // tokens of a piece's 256 (512) that are weighed in place
+constexpr uint32_t kRing = 256;
 constexpr uint32_t kFew = 192;         // of them, that are counted pair by pair
 constexpr int kGroupTiles = 512;       // most tiles whose groups' maxima are kept (32 KB)
 constexpr int kIndexBits = 22;         // KDA_MAX_VOCAB
@@ -161,6 +163,32 @@ struct Tile {
 #pragma unroll
             for (int e = 0; e < M; ++e) f(to_f32((T)v[j][e]), t * kTile + (j * 64 + lane) * M + e);
     }
+    // waits for the loads (or a loop over the pieces waits for those of the next tile, too)
+    __device__ __forceinline__ void arrived() {
+#pragma unroll
+        for (int j = 0; j < J; ++j) asm volatile("" : "+v"(v[j]));
+    }
+    // the same piece by piece, f(logits, first token), in a loop: a quarter (a half) of the code
+    template <typename F>
+    __device__ __forceinline__ void pieces(int t, int lane, F&& f) const {
+        Tile x = *this;
+#pragma unroll 1
+        for (int j = 0; j < J; ++j) {
+            float l[M];
+#pragma unroll
+            for (int e = 0; e < M; ++e) l[e] = to_f32((T)x.v[0][e]);
+            f(l, t * kTile + (j * 64 + lane) * M);
+#pragma unroll
+            for (int q = 0; q + 1 < J; ++q) x.v[q] = x.v[q + 1];
+        }
+    }
+    template <typename F>
+    __device__ __forceinline__ void each_in_turn(int t, int lane, F&& f) const {
+        pieces(t, lane, [&](const float* l, int i) {
+#pragma unroll
+            for (int e = 0; e < M; ++e) f(l[e], i + e);
+        });
+    }
 };
 
 template <int kCtrl>
@@ -232,7 +260,7 @@ struct RowLds {
     uint32_t part_n[kWaves];
     float part_f[3][kWaves];
     Entry few[64];
-    float ring[kWaves][128];   // weights to be, on their way
+    float ring[kWaves][kRing];   // logits to be weighed, on their way
     // the row
     const void* logits;
     double scale, unit;
@@ -403,6 +431,24 @@ struct Bins {
     __device__ __forceinline__ float edge(float b) const { return top - (b - start) / slope; }
 };
 
+// What those of `count` maxima weigh that are > below.
+__device__ __noinline__ uint64_t weigh_maxima(const __attribute__((address_space(3))) float* maxima, uint32_t count, float below) {
+    KDA_ROW_LDS;
+    if (threadIdx.x == 0) l.above_w = 0;
+    __syncthreads();
+    float w = 0.f;
+    for (uint32_t i = threadIdx.x; i < count; i += kThreads) {
+        const float m = maxima[i];
+        if (m > below) w += __builtin_amdgcn_exp2f((m - l.top) * (float)l.scale);
+    }
+    const double all = wave_sum((double)w);
+    if ((threadIdx.x & 63) == 0 && all > 0.0) add(&l.above_w, (uint64_t)(all * l.unit));
+    __syncthreads();
+    const uint64_t sum = l.above_w;
+    __syncthreads();
+    return sum;
+}
+
 // The nth largest of `count` maxima, of which the largest is `top` and nth ones or
 // more, as a rule, are not below `low`.  All threads; -infinity if there are not as many.
 __device__ __noinline__ float nth_maximum(const __attribute__((address_space(3))) float* maxima, uint32_t count, uint32_t nth,
@@ -484,6 +530,9 @@ __device__ __forceinline__ V uniform(V x) {
     return x;
 }
 
+enum Found { kNot, kMissed, kFound };
+constexpr int kSome = 4;   // tiles that one stands for
+
 template <typename T>
 struct Row {
     const T* logits;
@@ -522,13 +571,16 @@ struct Row {
         return __builtin_bit_cast(uint64_t, w + c) - __builtin_bit_cast(uint64_t, c);
     }
     __device__ __forceinline__ double weight_of(float x) const { return weight(x, top, scale); }
-    // f(tile, its number) for the tiles with a logit > below (with `step` 2 every other
-    // one of a wavefront's, others than its neighbours'), the next one's loads in flight
+    // whether tile t is one that stands for `step`, a power of two: each step-th of a
+    // wavefront's, others than its neighbours'
+    static __device__ __forceinline__ bool taken(int t, int step) { return ((t / kWaves + t) & (step - 1)) == 0; }
+    // f(tile, its number) for the tiles with a logit > below (with a `step`, those that
+    // stand for it), the next one's loads in flight
     template <typename F>
     __device__ __forceinline__ void tiles_over(float below, int step, F&& f) const {
         auto next = [&](int t) {
             for (; t < tiles; t += kWaves) {
-                if (step == 2 && ((t / kWaves + t) & 1)) continue;
+                if (!taken(t, step)) continue;
                 const float m = __builtin_bit_cast(float, __builtin_amdgcn_readfirstlane(__builtin_bit_cast(int, tops()[t])));
                 if (m > below) break;
             }
@@ -541,6 +593,7 @@ struct Row {
         for (;;) {
             const int then = next(t + kWaves);
             Tile<T> y;
+            x.arrived();
             if (then < tiles) y.load(logits, then, V, lane);
             f(x, t);
             if (then >= tiles) return;
@@ -552,25 +605,20 @@ struct Row {
     static __device__ __forceinline__ uint32_t rank_in(uint64_t those) {
         return __builtin_amdgcn_mbcnt_hi((uint32_t)(those >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)those, 0));
     }
-    // the tokens of a tile that `keep` names to the list (past kCap they are only counted)
-    template <typename F>
-    __device__ __forceinline__ void append(const Tile<T>& x, int t, F&& keep) const {
+    // the tokens of a tile that the lanes' bits name, the first one's the highest, to the
+    // list (past kCap they are only counted)
+    __device__ __forceinline__ void append(int t, uint32_t bits) const {
         KDA_ROW_LDS;
-        uint32_t named = 0;   // of all lanes
-        x.each(t, lane, [&](float v, int) { named += (uint32_t)__builtin_popcountll(__ballot(keep(v))); });
-        if (named == 0) return;
+        constexpr int M = Tile<T>::M;
+        if (__ballot(bits != 0) == 0) return;
+        const uint32_t mine = (uint32_t)__builtin_popcount(bits), upto = wave_scan_whole(mine);
         uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&l.n, named);
-        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-        x.each(t, lane, [&](float v, int i) {
-            const uint64_t those = __ballot(keep(v));
-            if (those == 0) return;
-            if (those >> lane & 1) {
-                const uint32_t mine = at + rank_in(those);
-                if (mine < kCap) l.list[mine].w = (uint64_t)i;   // (its place follows)
-            }
-            at += (uint32_t)__builtin_popcountll(those);
-        });
+        if (lane == 63) at = atomicAdd(&l.n, upto);
+        at = (uint32_t)__builtin_amdgcn_readlane((int)at, 63) + upto - mine;
+        for (; bits; bits &= bits - 1, ++at) {
+            const int slot = kPer - 1 - __builtin_ctz(bits);
+            if (at < kCap) l.list[at].w = (uint64_t)(t * kTile + (slot / M * 64 + lane) * M + slot % M);   // (its place follows)
+        }
     }
     __device__ __forceinline__ void start_list() const {
         KDA_ROW_LDS;
@@ -598,7 +646,11 @@ struct Row {
         constexpr int M = Tile<T>::M;
         start_list();
         if (!by_group) {
-            tiles_over(below, 1, [&](const Tile<T>& x, int t) { append(x, t, [&](float v) { return v > below; }); });
+            tiles_over(below, 1, [&](const Tile<T>& x, int t) {
+                uint32_t bits = 0;
+                x.each_in_turn(t, lane, [&](float v, int) { bits = 2 * bits + (v > below); });
+                append(t, bits);
+            });
             return listed();
         }
         // a group's 64 tokens, one a lane, eight groups in flight
@@ -637,131 +689,189 @@ struct Row {
         return listed(true);
     }
 
-    // Sums over a tile of the weights of its tokens over `border`, through a ring that
-    // packs them: `all`, and `kept`, of those that weigh `least`; in lane 63.  Their
-    // number is added to `passed`; those over `from` and not over `border` go to the list.
+    // Sums over a tile of the weights of its tokens over `border`: `all`, the lane's part,
+    // and `kept`, of those that weigh `least`, in lane 63.  Their number is added to
+    // `passed`; those over `from` and not over `border` go to the list.  A piece with many
+    // of them is weighed in place, few are packed by a ring first (256 x 160,000 fp32, normal
+    // logits: by min-p 1e-4 114 us with the ring alone, 93 so; by top-p 0.99 127 and 129;
+    // everything in place 158, the share that weighs anything being small).
     __device__ __forceinline__ void weigh(const Tile<T>& x, int t, float from, float border, double least, uint64_t& all,
                                           uint64_t& kept, uint32_t& passed) const {
+        constexpr int M = Tile<T>::M;
+        const double c = 4503599627370496.0 / unit;   // (as in whole())
+        const bool infinite = top == __builtin_inff();
         KDA_ROW_LDS;
         float* ring = l.ring[wave];
-        uint32_t head = 0, held = 0, named = 0;   // of all lanes
-        uint64_t between[kPer];
-        int slot = 0;
+        uint32_t bits = 0, summed = 0, head = 0, held = 0;   // of all lanes
         all = kept = 0;
+        auto take = [&](float v, bool counts) {
+            const double y = __builtin_fmax(((double)v - (double)top) * scale, -1020.0);
+            double w = exp2_neg(y);
+            if (infinite) w = v == top ? 1.0 : 0.0;
+            w = counts && (infinite || y > -1020.0) ? w : 0.0;
+            all += __builtin_bit_cast(uint64_t, w + c);
+            if (least > 0.0) kept += __builtin_bit_cast(uint64_t, (w >= least ? w : 0.0) + c);
+            ++summed;
+        };
         auto flush = [&](uint32_t n) {
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-            const double w = (uint32_t)lane < n ? weight_of(ring[(head + lane) & 127]) : 0.0;
-            const uint64_t i = whole(w);
-            all += i;
-            kept += w >= least ? i : 0;
+            take(ring[(head + lane) % kRing], (uint32_t)lane < n);
             __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront");
-            head += 64;
+            head += n;
+            held -= n;
         };
-        x.each(t, lane, [&](float v, int) {
-            const uint64_t those = __ballot(v > border);
-            between[slot] = __ballot(v > from) & ~those;
-            named += (uint32_t)__builtin_popcountll(between[slot++]);
-            if (those == 0) return;
-            if (v > border) ring[(head + held + rank_in(those)) & 127] = v;
-            held += (uint32_t)__builtin_popcountll(those);
-            if (held >= 64) {
-                flush(64);
-                passed += 64;
-                held -= 64;
+        x.pieces(t, lane, [&](const float* v, int) {
+            uint64_t those[M];
+            uint32_t n = 0;
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                those[e] = __ballot(v[e] > border);
+                n += (uint32_t)__builtin_popcountll(those[e]);
+                bits = 2 * bits + (v[e] > from && !(v[e] > border));
             }
+            if (n == 0) return;
+            passed += n;
+            if (n >= kDense) {
+#pragma unroll
+                for (int e = 0; e < M; ++e) take(v[e], v[e] > border);
+                return;
+            }
+#pragma unroll
+            for (int e = 0; e < M; ++e) {
+                if (v[e] > border) ring[(head + held + rank_in(those[e])) % kRing] = v[e];
+                held += (uint32_t)__builtin_popcountll(those[e]);
+            }
+            while (held >= 64) flush(64);
         });
         if (held) flush(held);
-        passed += held;
-        all = wave_scan_whole(all);
-        kept = wave_scan_whole(kept);
-        if (named == 0) return;
-        uint32_t at = 0;
-        if (lane == 0) at = atomicAdd(&l.n, named);
-        at = (uint32_t)__builtin_amdgcn_readfirstlane((int)at);
-        slot = 0;
-        x.each(t, lane, [&](float, int i) {
-            const uint64_t those = between[slot++];
-            if (those == 0) return;
-            const uint32_t to = at + rank_in(those);
-            if ((those >> lane & 1) && to < kCap) l.list[to].w = (uint64_t)i;   // (its place follows)
-            at += (uint32_t)__builtin_popcountll(those);
-        });
+        all -= summed * __builtin_bit_cast(uint64_t, c);
+        kept = wave_scan_whole(least > 0.0 ? kept - summed * __builtin_bit_cast(uint64_t, c) : all);
+        append(t, bits);
     }
 
     // The same as find(), over the row's tokens: `below` < logit < `above`, which
     // weigh 2^high at most and, where weights are to reach `target`, 2^low at least
     // (what weighs less cannot be where they do).  `off` is what those from `above` on
-    // weigh.  If it can be found within a few bins, sums then holds each tile's weight
+    // weigh.  If it can be found within some bins, sums then holds each tile's weight
     // of what is kept if it ends there and weighs `least`, and l.key_w the weights up
-    // to there.  False if not: it may be there all the same.
-    __device__ __forceinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
-                                           double low, double least) const {
+    // to there.  kNot: it may be there all the same, in a bin of too many; kMissed: where
+    // some tiles were taken for all.  `all`, not 0: what all tokens weigh, of which those
+    // behind `target` are to be told from some tiles.
+    __device__ __forceinline__ Found find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+                                               double low, double least, uint64_t all) const {
         KDA_ROW_LDS;
         const Bins bin_of(top, scale, high, low);
         const int exact = !by_count && off == 0 ? kBins / 16 : 0;
+        if (threadIdx.x == 0) {
+            l.above_w = 0;
+            l.before_n = 0;
+        }
         clear_bins(l);
         uint32_t rest = 0;
-        // (where there are many tiles, every other one stands for two: thousands of tokens are off by a fraction of a
-        // bin, and several are collected.  Not so for weights, of which a few tokens may be most.)
-        const int step = by_count && tiles >= 64 ? 2 : 1;
-        tiles_over(below, step, [&](const Tile<T>& x, int t) {
-            x.each(t, lane, [&](float v, int) {
-                if (v > below && v < above) {
+        uint64_t aim = target - off;
+        if (all) {
+            // what the tokens behind weigh
+            uint32_t tokens = 0;   // of the tiles taken
+            if ((int)threadIdx.x < tiles && taken((int)threadIdx.x, kSome)) tokens = (uint32_t)min(kTile, V - (int)threadIdx.x * kTile);
+            float beyond = 0.f;   // (what weighs less than 2^low)
+            tiles_over(minus_inf(), kSome, [&](const Tile<T>& x, int t) {
+                x.each_in_turn(t, lane, [&](float v, int) {
+                    if (!(v < above)) return;
                     const int b = bin_of(v);
-                    if (b < kBins - 1) atomicAdd(&l.bin_n[b], (uint32_t)step);
-                    else rest += step;
-                    if (b < exact) add(&l.bin_w[b], whole(weight_of(v)));
-                }
+                    if (b < kBins - 1) {
+                        atomicAdd(&l.bin_n[b], 1u);
+                    } else {
+                        rest += v > minus_inf();
+                        beyond += __builtin_amdgcn_exp2f((v - top) * (float)scale);
+                    }
+                });
             });
-        });
-        rest = wave_scan_whole(rest);
-        if (lane == 63) atomicAdd(&l.bin_n[kBins - 1], rest);
-        __syncthreads();
-        // (what a bin weighs: about its middle, but for the first ones, whose few tokens may be most of it)
-        if (!by_count && (int)threadIdx.x >= exact) {
+            tokens = wave_scan_whole(tokens);
+            rest = wave_scan_whole(rest);
+            const double beyond_w = wave_sum((double)beyond);
+            if (lane == 63) {
+                atomicAdd(&l.before_n, tokens);
+                atomicAdd(&l.bin_n[kBins - 1], rest);
+                add(&l.above_w, (uint64_t)(beyond_w * unit));
+            }
+            __syncthreads();
+            const double each = (double)V / (double)max(l.before_n, 1u);
             const double y = high - (threadIdx.x + 0.5) * (high - low) / (kBins - 1);
-            l.bin_w[threadIdx.x] = (uint64_t)(l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0)));
+            const double w = threadIdx.x == kBins - 1 ? (double)l.above_w
+                                                      : l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0));
+            const uint64_t here_w = (uint64_t)(w * each);
+            l.bin_w[threadIdx.x] = here_w;
+            l.bin_n[threadIdx.x] = (uint32_t)(l.bin_n[threadIdx.x] * each);
+            __syncthreads();
+            if (threadIdx.x == 0) l.above_w = 0;
+            __syncthreads();
+            const uint64_t sum = wave_scan_whole(here_w);
+            if (lane == 63) add(&l.above_w, sum);
+            __syncthreads();
+            const uint64_t found = l.above_w, behind = all - target;
+            aim = found > behind ? found - behind : 1;
+        } else {
+            // (where there are many tiles, every other one stands for two: thousands of tokens are off by a fraction of a
+            // bin, and several are collected.  Not so for weights, of which a few tokens may be most.)
+            const int step = by_count && tiles >= 64 ? 2 : 1;
+            tiles_over(below, step, [&](const Tile<T>& x, int t) {
+                x.each_in_turn(t, lane, [&](float v, int) {
+                    if (v > below && v < above) {
+                        const int b = bin_of(v);
+                        if (b < kBins - 1) atomicAdd(&l.bin_n[b], (uint32_t)step);
+                        else rest += step;
+                        if (b < exact) add(&l.bin_w[b], whole(weight_of(v)));
+                    }
+                });
+            });
+            rest = wave_scan_whole(rest);
+            if (lane == 63) atomicAdd(&l.bin_n[kBins - 1], rest);
+            __syncthreads();
+            // (what a bin weighs: about its middle, but for the first ones, whose few tokens may be most of it)
+            if (!by_count && (int)threadIdx.x >= exact) {
+                const double y = high - (threadIdx.x + 0.5) * (high - low) / (kBins - 1);
+                l.bin_w[threadIdx.x] = (uint64_t)(l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0)));
+            }
         }
-        const int bin = cross<true>(by_count, target - off);
-        if (bin < 0) return false;
-        // that bin and as many beside it as fit the list, up to eight: edges and estimated weights are not exact
-        int j0 = bin, j1 = bin;
-        uint32_t here = l.here_n;
-        for (int r = 0; r < 8; ++r) {
-            const uint32_t more = (j0 > 0 ? l.bin_n[j0 - 1] : 0) + (j1 < kBins - 1 ? l.bin_n[j1 + 1] : 0);
-            if (here + more > kCap - 256) break;
-            here += more;
-            if (j0 > 0) --j0;
-            if (j1 < kBins - 1) ++j1;
-        }
-        if (here > kCap) return false;
+        const int bin = cross<true>(by_count, aim);
+        if (bin < 0) return kMissed;
+        // that bin and as many beside it as fit the list, up to eight: edges and estimated weights are not exact; 64
+        // where some tiles stand for all
+        const uint32_t here = l.here_n;
+        const int left = bin - 1 - lane, right = bin + 1 + lane;
+        const uint32_t more = (left >= 0 ? l.bin_n[left] : 0) + (right < kBins ? l.bin_n[right] : 0);
+        const bool fit = here + wave_scan_whole(more) <= kCap - 256 && (all || lane < 8);
+        const int beside = __builtin_popcountll(__ballot(fit));
+        const int j0 = max(bin - beside, 0), j1 = min(bin + beside, kBins - 1);
+        if (here > kCap) return kNot;
         const float over = j0 > 0 ? bin_of.edge((float)j0) : __builtin_inff(), from = j1 < kBins - 1 ? __builtin_fmaxf(bin_of.edge(j1 + 1.f), below) : below;
-        if (!(from < over)) return false;
+        if (!(from < over)) return kNot;
         if (threadIdx.x == 0) {
             l.above_w = 0;
             l.before_n = 0;
         }
         for (int t = threadIdx.x; t < tiles; t += kThreads) sums()[t] = 0;
         start_list();
-        uint64_t all = 0;
+        uint64_t over_w = 0;
         uint32_t passed = 0;   // of all lanes
         // (what is from `above` on is over, wherever bin 0 begins)
         const float border = __builtin_fminf(over, under(above));
         tiles_over(from, 1, [&](const Tile<T>& x, int t) {
             uint64_t w, kept;
             weigh(x, t, from, border, least, w, kept, passed);
-            all += w;
+            over_w += w;
             if (lane == 63) sums()[t] = kept;
         });
+        over_w = wave_scan_whole(over_w);
         if (lane == 63) {
-            add(&l.above_w, all);
-            atomicAdd(&l.before_n, passed);
+            add(&l.above_w, over_w);
+            if (by_count) atomicAdd(&l.before_n, passed);
         }
         const uint32_t n = listed();
         const uint64_t base = by_count ? (uint64_t)l.before_n : l.above_w;
         const uint64_t first = border < top ? place(border, 0) : place(top, 0), last = from > minus_inf() ? place(from, 0) : 1;
         __syncthreads();
-        if (n > kCap || base >= target || !find(kByPlace, n, last, first, by_count, target - base)) return false;
+        if (n > kCap || base >= target || !find(kByPlace, n, last, first, by_count, target - base)) return kMissed;
         const uint64_t cut = l.key;
         __syncthreads();
         if (threadIdx.x == 0) l.key_w += l.above_w;
@@ -770,7 +880,7 @@ struct Row {
             if (x.place >= cut && weight_of(logit_of(x.place)) >= least) add(&sums()[index_of(x.place) / kTile], x.w);
         }
         __syncthreads();
-        return true;
+        return kFound;
     }
     // The same wherever it lies, without the sums: a histogram of the weights
     // themselves, and as many levels inside one bin as it takes (thousands of equal
@@ -785,7 +895,7 @@ struct Row {
             __syncthreads();
             clear_bins(l);
             tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
-                x.each(t, lane, [&](float v, int i) {
+                x.each_in_turn(t, lane, [&](float v, int i) {
                     if (v > minus_inf()) {
                         const uint64_t k = place(v, i);
                         if (k >= lo && k <= hi) count(l, (int)((hi - k) >> shift), whole(weight_of(v)));
@@ -804,7 +914,7 @@ struct Row {
         }
         start_list();
         tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
-            x.each(t, lane, [&](float v, int i) {
+            x.each_in_turn(t, lane, [&](float v, int i) {
                 if (v > minus_inf()) {
                     const uint64_t k = place(v, i);
                     if (k >= lo && k <= hi) {
@@ -895,9 +1005,9 @@ struct Row {
 template <typename T>
 __device__ __noinline__ uint32_t gather(float below, bool by_group) { return Row<T>::here().gather(below, by_group); }
 template <typename T>
-__device__ __noinline__ bool find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
-                                       double low, double least) {
-    return Row<T>::here().find_near(by_count, target, above, off, below, high, low, least);
+__device__ __noinline__ Found find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+                                        double low, double least, uint64_t all) {
+    return Row<T>::here().find_near(by_count, target, above, off, below, high, low, least, all);
 }
 template <typename T>
 __device__ __noinline__ bool find_far(bool by_count, uint64_t target) { return Row<T>::here().find_far(by_count, target); }
@@ -922,7 +1032,7 @@ __device__ __noinline__ Kept over_row(int k, bool by_p, double p, double least, 
     uint64_t cut = 1, sum = all;
     bool summed = false;
     if (k) {
-        summed = find_near<T>(true, (uint64_t)k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, least);
+        summed = find_near<T>(true, (uint64_t)k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, least, 0) == kFound;
         const bool ok = summed || find_far<T>(true, (uint64_t)k);
         if (ok) cut = l.key;
         sum = ok ? l.key_w : l.total_w;
@@ -948,7 +1058,16 @@ __device__ __noinline__ Kept over_row(int k, bool by_p, double p, double least, 
         if (bottom > high - 0.01) bottom = high - 0.01;
         const double low_x = (double)r.top + bottom / r.scale;
         const float from = !(low_x > -3e38) || r.top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
-        summed = find_near<T>(false, target, above, listed_w, from, high, bottom, least);
+        Found found = kMissed;
+        // (from a quarter of the tiles the place of the cut is off by some hundred tokens, of over a thousand that are
+        // collected; beyond 256 tiles by too many.  256 x 160,000 fp32 by top-p 0.5, 0.9, 0.99: 155, 143, 157 us from all
+        // tiles, 98, 116, 129 from a quarter, 94, 111, 205 from an eighth.  Fewer than 32 take no longer than the rest.)
+        if (!k && r.tiles >= 32 && r.tiles <= 256) {
+            found = find_near<T>(false, target, above, listed_w, from, high, bottom, least, sum);
+            __syncthreads();
+        }
+        if (found == kMissed) found = find_near<T>(false, target, above, listed_w, from, high, bottom, least, 0);
+        summed = found == kFound;
         if (summed || find_far<T>(false, target)) cut = max(cut, l.key);
         __syncthreads();
     }
@@ -1075,7 +1194,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         float below = minus_inf(), listed_over = top;
         bool sure = false, done = false;
         uint32_t n = kCap + 1;
-        uint64_t listed_w = 0;
+        uint64_t listed_w = 0, about_w = 0;
         auto share = [&](uint64_t w) { return share_of(ask.p, w); };
         for (int attempt = 0;; ++attempt) {
             below = top;   // (none)
@@ -1097,11 +1216,17 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
                 sure = true;
             }
             // (hardly one that will do, if much of what the last one left out is asked for: then as far as min-p goes)
-            if (attempt > 0 && !sure && (double)(share(sum) - listed_w) > 0.3 * (double)(sum - listed_w)) {
+            const double less = (double)max(listed_w, about_w);
+            if (attempt > 0 && !sure && (double)share(sum) - less > 0.3 * ((double)sum - less)) {
                 below = floor > minus_inf() ? floor : top;
                 sure = true;
             }
             if (!(below < top)) break;
+            // (hardly a token over the first bound that is not its group's largest: not listed if those do not make it)
+            if (attempt == 0 && !sure && !ask.by_k) {
+                about_w = weigh_maxima(maxima, count, below);
+                if ((double)about_w * 1.25 < (double)share(sum)) continue;
+            }
             // (a fifth more than the list holds, if they are spread evenly: not even tried)
             if (below == floor && V > (int)kCap && expected(maxima, count, below) > 1.2f * kCap) {
                 n = kCap + 1;

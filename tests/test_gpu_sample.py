@@ -108,6 +108,35 @@ def test_large_vocabularies(V, dtype, kind):
     check(kda, x, u, T, [5000] * R, None, [0.1, 0.01, 1e-4, 1e-7, 0.02, 0.9])
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [32768, 40001, 160000, 262144])
+def test_rows_whose_tiles_are_unlike(V, dtype):
+    """A row's parts say little about its whole: sorted rows, rows whose tiles differ by residue, rows with most tiles
+    masked, two values alone."""
+    kda = need_gpu()
+    R = 12
+    x = rows(R, V, "f32", V + 1)
+    t = torch.arange(V, device="cuda") // 1024
+    some = (t // 16 + t) % 4 == 0
+    x[0], x[1] = torch.sort(x[0]).values, torch.sort(x[1], descending=True).values
+    x[2, some] -= 6
+    x[3, ~some] -= 6
+    x[4, some] = -INF
+    x[5, ~some] = -INF
+    x[6, V // 3:] = -INF
+    x[7, : V - 3 * 1024] = -INF
+    x[8] = torch.where(torch.arange(V, device="cuda") % 3 == 0, 1.5, -0.5)
+    x[9] = torch.where(some, 2.0, 0.0) + x[9] * 1e-3
+    x[10, 17] += 25
+    x[11] *= 0.1
+    x = x.to(DT[dtype])
+    for j, p in enumerate((0.5, 0.9, 0.99, 0.9997)):
+        u = uniform(R, V + j)
+        case(f"sample tiles V={V} {dtype} p={p}")
+        check(kda, x, u, None, None, [p] * R, slack=1e-10)
+    check(kda, x, uniform(R, 3), [1.7] * R, None, [0.93] * R, [1e-5] * R, slack=1e-10)
+
+
 @pytest.mark.parametrize("V,dtype,kind", [(524288, "bf16", "normal"), (524289, "f32", "peaked"), (1 << 22, "bf16", "normal")])
 def test_the_largest_vocabularies(V, dtype, kind):
     """Around the most tiles whose groups' maxima are kept, and the most tokens."""
