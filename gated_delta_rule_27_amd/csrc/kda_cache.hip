@@ -1,5 +1,18 @@
 // kda_cache.hip -- fp32 states into the 8-bit cache, back, and a window's
 // updates taken into the 8-bit state in place.
+//
+// A state S [key i][value j] is scale[i] * codes[j][i], scale[i] = max_j |S[i][j]| / 127.
+// With G the sum of log alpha over a window's n tokens and G_t that up to token t, it
+// is read back as S[i][j] = scale[i] e^G[i] codes[j][i] + sum_t e^(G - G_t)[i] k_t[i] u_t[j]:
+// decay belongs to the key channel, as the scale does, so that it costs the codes
+// nothing, and the n updates are a product of 128 x n by n x 128.
+// All three move memory: a workgroup of 256 threads holds one state in registers (64
+// values a thread) and passes the codes, which lie the other way round, through LDS;
+// every global access is whole lines.  256 x 96 states: stored in 364 us (2.03 GB,
+// 5.6 TB/s), folded with 8 bf16 tokens in 179 us (0.98 GB, 5.5 TB/s; 4 tokens 145 us,
+// 6.3 TB/s); 192 x 96 loaded in 273 us (1.52 GB, 5.6 TB/s).  A large device copy
+// reaches 4.7 TB/s.  One state each of 96 heads: 4.6 us to store, a launch and one trip
+// through the workgroup.
 #include "kda.h"
 #include "kda_cache.h"
 #include "kda_device.h"
@@ -14,7 +27,7 @@ constexpr int kLd = 36;   // dwords of a value channel's 128 codes in LDS, with 
 
 typedef uint32_t uintx4 __attribute__((ext_vector_type(4)));
 
-// The workgroup's four wavefronts hold a state as blocks of four rows and
+// In a store and a load the workgroup's four wavefronts hold a state as blocks of four rows and
 // four columns a lane: block t of wavefront w, lane (half, l) covers rows
 // 32 w + 8 t + 4 half + 0..3 and columns 4 l + 0..3, so that a row's loads and
 // stores are whole lines and four rows' codes of a column are one dword.
@@ -157,12 +170,15 @@ __device__ __forceinline__ void stage(ReadLds& lds, WindowLds<T, kMost>& wl, con
     const int half = most / 2;
     float g = 0.f;
     if (threadIdx.x < kD) {
+#pragma unroll 2
         for (int t = most - 1; t >= half; --t) {
             wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
             g += to_f32(wl.raw[1][t][i]);
         }
     } else {
+#pragma unroll 2
         for (int t = most - 1; t >= half; --t) g += to_f32(wl.raw[1][t][i]);
+#pragma unroll 2
         for (int t = half - 1; t >= 0; --t) {
             wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
             g += to_f32(wl.raw[1][t][i]);
@@ -222,8 +238,12 @@ __global__ __launch_bounds__(256) void cache_store_kernel(CacheMoveArgs a) {
     codes_out(lds, a.codes + at * kD * kD);
 }
 
-template <typename T, int kMost>
-__global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
+// (Codes by streaming loads beside a window only: 192 x 96 states with windows of 4 of 8
+// and 8 of 16 tokens, bf16, take 286 and 296 us so and 288 and 307 by ordinary ones, fp32
+// 283, 345 and 299, 357; without windows 290 and 270, four requests a page 256 and 222.)
+template <typename T, bool kWindow>
+__global__ __launch_bounds__(256, kWindow ? 3 : 5) void cache_load_kernel(CacheMoveArgs a) {
+    constexpr int kMost = kWindow ? kMaxWindow : 4;   // (an instance for short ones gains nothing)
     __shared__ __align__(16) ReadLds lds;
     __shared__ __align__(16) WindowLds<T, kMost> wl;
     const uint32_t unit = blockIdx.x;
@@ -234,8 +254,7 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
     State v;
     const size_t at = (size_t)page * a.H + h;
     const int n = window_count(a.win, b);
-    // (several requests may read one page: no streaming loads, 281 us for 192 x 96 states against 297)
-    stage<T, kMost, false>(lds, wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, at, n);
+    stage<T, kMost, kWindow>(lds, wl, a.codes + at * kD * kD, a.scale + at * kD, a.win, at, n);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
         const floatx4 m = *reinterpret_cast<const floatx4*>(lds.row + p.row(t));
@@ -268,9 +287,13 @@ __global__ __launch_bounds__(256) void cache_load_kernel(CacheMoveArgs a) {
 // A fold holds its state as matrix tiles: wavefront w rows 32 w + 16 R + 4 g + 0..3
 // of column 16 T + l, so that the window's updates are products of 16 x 4 and 4 x 16
 // (exact fp32 factors), a row's largest magnitude lies in 16 lanes, and four rows'
-// codes of a column are one dword here, too.
+// codes of a column are one dword here, too.  (With rank-one updates by the vector unit
+// 256 x 96 states and 8 tokens took 311 us, not 179.)  Two instances by the longest
+// window: the LDS of a short one lets more workgroups in (192 x 96 states, windows of 8,
+// bf16 and fp32: 164 and 150 us, by the instance for 16 189 and 216); the registers are
+// bounded to match it (fp32, 16: 298 us at three workgroups a CU, 351 at two).
 template <typename T, int kMost>
-__global__ __launch_bounds__(256, sizeof(T) * kMost <= 16 ? 5 : sizeof(T) * kMost <= 32 ? 4 : 2) void cache_fold_kernel(CacheMoveArgs a) {
+__global__ __launch_bounds__(256, sizeof(T) * kMost <= 16 ? 5 : kMost <= 8 ? 4 : 3) void cache_fold_kernel(CacheMoveArgs a) {
     __shared__ __align__(16) union {
         ReadLds in;
         QuantiseLds out;
@@ -290,6 +313,7 @@ __global__ __launch_bounds__(256, sizeof(T) * kMost <= 16 ? 5 : sizeof(T) * kMos
 #pragma unroll
         for (int c = 0; c < 8; ++c) v[R][c] = values_of(lds.in.tile[(16 * c + l) * kLd + (row >> 2) + 4 * R + g], m);
     }
+#pragma unroll 1
     for (int t = 0; t < n; t += 4) {
         const float k0 = wl.k(t + g)[row + l], k1 = wl.k(t + g)[row + 16 + l];
 #pragma unroll
@@ -331,14 +355,9 @@ hipError_t launch_cache_store(const CacheMoveArgs& a, hipStream_t stream) {
 
 hipError_t launch_cache_load(const CacheMoveArgs& a, int dtype, hipStream_t stream) {
     const dim3 grid((unsigned)((int64_t)a.B * a.H)), block(256);
-    const bool few = !a.win.k || a.win.W <= 8;
-    if (dtype == 0) {
-        if (few) cache_load_kernel<float, 8><<<grid, block, 0, stream>>>(a);
-        else cache_load_kernel<float, kMaxWindow><<<grid, block, 0, stream>>>(a);
-    } else {
-        if (few) cache_load_kernel<bf16, 8><<<grid, block, 0, stream>>>(a);
-        else cache_load_kernel<bf16, kMaxWindow><<<grid, block, 0, stream>>>(a);
-    }
+    if (!a.win.k) cache_load_kernel<bf16, false><<<grid, block, 0, stream>>>(a);
+    else if (dtype == 0) cache_load_kernel<float, true><<<grid, block, 0, stream>>>(a);
+    else cache_load_kernel<bf16, true><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 

@@ -11,6 +11,12 @@
 // code is converted or multiplied by the vector unit, the sums are exact, and
 // what is rounded is each vector's entry, to 2^-31 of the vector's largest,
 // and the sum of the four digits' results, to 24 bits.
+// Bounded by memory: 256 x 96 states with windows of 4 tokens take 106 us for 0.53 GB,
+// 5.0 TB/s (reads alone, laid out as the codes are, reach 6.1); a step of fp32 states
+// moves 3.2 GB.  The window's three new rows, 19 MB in lines of their own, cost 13 us of
+// it.  One sequence: 5.4 us, a launch and the chain of loads, digits and products.
+// 23 x 31 states with 6 fp32 tokens on average: 11.4 us, the window's tokens one after
+// the other in a wavefront.
 #include "kda.h"
 #include "kda_cache.h"
 #include "kda_device.h"

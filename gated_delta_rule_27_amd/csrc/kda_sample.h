@@ -52,10 +52,8 @@ __host__ __device__ inline SampleSections sample_sections(int32_t R, int64_t til
     return s;
 }
 inline size_t sample_workspace(int32_t R, int32_t V) { return (size_t)sample_sections(R, sample_tiles(V)).end; }
-// workgroups a row of the last pass, and the most of a pass: four tiles each, the
-// last pass's up to 7 tokens ahead of the row
-__host__ __device__ inline int64_t sample_row_groups(int32_t V) { return ((int64_t)V + 7 + 4 * kSampleTile - 1) / (4 * kSampleTile); }
-inline int64_t sample_groups(int32_t R, int32_t V) { return R * sample_row_groups(V); }
+// workgroups of the first pass and of the last: four tiles each
+inline int64_t sample_groups(int32_t R, int32_t V) { return R * ((sample_tiles(V) + 3) / 4); }
 
 // dtype: 0 = fp32, 1 = bf16 (kda_dtype values)
 hipError_t launch_sample(const SampleArgs& a, int dtype, hipStream_t stream);

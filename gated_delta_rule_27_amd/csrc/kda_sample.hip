@@ -23,6 +23,13 @@
 // Weights are taken in 64 bits and added up as whole numbers of 2^-F: their sums
 // are the same in any order, and the drawn token is a whole number, too, which a
 // rounding of a running sum must not move.
+// What bounds it, 256 x 160,000 fp32 (0.16 GB): the first pass HBM, 33 us (4.9 TB/s;
+// 30 without weights); the second the slowest row, which one CU reads: 10 us without a
+// filter, 20 to 30 us where the list holds all that is kept, 80 us where a nucleus has
+// thousands of tokens (0.64 MB through one CU, some 25 fp64 and integer instructions a
+// logit).  The third pass, 192 x 50,021 bf16: 11 us (19 MB written, as much read where
+// something is kept).  One row of 32,000: 18.5 us, three launches' trips to memory and
+// the second one's instructions, fetched as they run.
 #include "kda.h"
 #include "kda_device.h"
 #include "kda_sample.h"
@@ -39,7 +46,9 @@ constexpr int kBins = kThreads;
 constexpr uint32_t kCap = 2048;        // tokens of the list
 constexpr uint32_t kDense = 96;        // tokens of a piece's 256 (512) that are weighed in place
 constexpr uint32_t kRing = 256;
-constexpr uint32_t kFew = 192;         // of them, that are counted pair by pair
+// of them, that are counted pair by pair (one row of 32,000 with top-k some hundred and top-p: 18 us, 21 by histograms;
+// top-k 300 the other way round: 27 by histograms, 50 by pairs)
+constexpr uint32_t kFew = 192;
 constexpr int kGroupTiles = 512;       // most tiles whose groups' maxima are kept (32 KB)
 constexpr int kIndexBits = 22;         // KDA_MAX_VOCAB
 constexpr uint64_t kIndexMask = (1u << kIndexBits) - 1;
@@ -1190,7 +1199,9 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         const auto* maxima = (const __attribute__((address_space(3))) float*)(by_group ? r.groups() : r.tops());
         const uint32_t count = by_group ? tiles * kSampleGroups : tiles;
         // The list is to hold every token of logit > below.  Sure: then it holds all that can be kept (and summed for
-        // top-p).  By top-p alone, the 128 largest maxima first, then as many as 1500 tokens or so exceed.
+        // top-p).  By top-p alone, the 64 largest maxima first, then 256, then as many as 1500 tokens or so
+        // exceed (128 and 1500: 57 instead of 53 us for peaked rows, 256 x 160,000 by top-p 0.9; one row by top-p 0.5, 56
+        // instead of 34).
         float below = minus_inf(), listed_over = top;
         bool sure = false, done = false;
         uint32_t n = kCap + 1;
@@ -1201,17 +1212,17 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
             sure = V <= (int)kCap;
             if (sure) {
                 below = minus_inf();
-            } else if (ask.by_k ? (uint32_t)ask.k <= count : ask.by_p && attempt < 2) {
-                const uint32_t few = min(128u, (count + 1) / 2), many = (uint32_t)(count * (1.f - __expf(-1500.f / (float)count)));
-                const uint32_t nth = ask.by_k ? (uint32_t)ask.k : attempt == 0 ? few : many;
-                const float bound = attempt == 1 && many <= few ? minus_inf() : nth_maximum(maxima, count, nth, top, nth <= (uint32_t)full ? low : __builtin_fminf(low, least_top));
+            } else if (ask.by_k ? (uint32_t)ask.k <= count : ask.by_p && attempt < 3) {
+                const uint32_t few = min(attempt == 0 ? 64u : 256u, (count + 1) / 2), many = (uint32_t)(count * (1.f - __expf(-1500.f / (float)count)));
+                const uint32_t nth = ask.by_k ? (uint32_t)ask.k : attempt < 2 ? few : many;
+                const float bound = attempt == 2 && many <= few ? minus_inf() : nth_maximum(maxima, count, nth, top, nth <= (uint32_t)full ? low : __builtin_fminf(low, least_top));
                 if (bound > minus_inf()) {
                     below = under(bound);
                     sure = ask.by_k;
                 }
             }
-            // (min-p's bound where it comes first, or leaves a list about as short)
-            if (floor > minus_inf() && (floor >= below || !(below < top) || (attempt == 0 && !sure && expected(maxima, count, floor) < 600.f))) {
+            // (min-p's bound where it comes first, or leaves a list that fits: 256 x 32,000 by top-p 0.9 and min-p 0.01 48 -> 45 us)
+            if (floor > minus_inf() && (floor >= below || !(below < top) || (attempt == 0 && !sure && expected(maxima, count, floor) < 0.9f * kCap))) {
                 below = floor;
                 sure = true;
             }
@@ -1223,7 +1234,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
             }
             if (!(below < top)) break;
             // (hardly a token over the first bound that is not its group's largest: not listed if those do not make it)
-            if (attempt == 0 && !sure && !ask.by_k) {
+            if (attempt < 2 && !sure && !ask.by_k) {
                 about_w = weigh_maxima(maxima, count, below);
                 if ((double)about_w * 1.25 < (double)share(sum)) continue;
             }
@@ -1353,64 +1364,48 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
 
 // ---- probabilities -----------------------------------------------------------
 
-// Tiles that begin at a multiple of 16 bytes, whichever token that is: a row of an odd
-// vocabulary is written (and read) by whole pieces but for its ends (192 x 50,021 bf16:
-// 13 us at the tokens' own places).
+// (Rows of an odd vocabulary are read and written at the tokens' own places: in pieces
+// that begin at a multiple of 16 bytes 256 x 160,001 fp32 took 64 us here, not 58.)
 template <typename T>
 __global__ __launch_bounds__(256) void sample_probs_kernel(SampleArgs a) {
     constexpr int M = Tile<T>::M, J = Tile<T>::J;
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const uint32_t per_row = (uint32_t)sample_row_groups(a.V);
+    const int tiles = (a.V + kTile - 1) / kTile;
+    const uint32_t per_row = (uint32_t)(tiles + 3) / 4;
     const uint32_t row = blockIdx.x / per_row;
-    const int tiles = (a.V + kTile - 1) / kTile, t = (int)(blockIdx.x % per_row) * 4 + wave;
-    const size_t begin = (size_t)row * a.V;
-    const int ahead = (int)(begin % M), v0 = t * kTile - ahead;   // tokens before the row in its first piece
-    if (v0 >= a.V) return;
+    const int t = (int)(blockIdx.x % per_row) * 4 + wave;
+    if (t >= tiles) return;
     const SampleSections at = sample_sections(a.R, tiles);
     const SampleRow r = reinterpret_cast<const SampleRow*>(a.workspace + at.rows)[row];
-    const float* tops = reinterpret_cast<const float*>(a.workspace + at.tops) + (size_t)row * tiles;
-    const float m = __builtin_fmaxf(tops[max(t - 1, 0)], tops[min(t, tiles - 1)]);
-    const T* logits = static_cast<const T*>(a.logits) + begin;
-    T* probs = static_cast<T*>(a.probs) + begin;
-    typedef typename Vec16<T>::type vec;
+    const float m = reinterpret_cast<const float*>(a.workspace + at.tops)[(size_t)row * tiles + t];
+    const size_t begin = (size_t)row * a.V;
     const bool some = m > minus_inf() && ((uint64_t)key_of(m) << kIndexBits | kIndexMask) >= r.cut && weight(m, r.top, r.scale) >= r.least;
-    const bool inner = v0 >= 0 && v0 + kTile <= a.V;
-    vec x[J];
-    if (some) {
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-            const int v = v0 + (j * 64 + lane) * M;
-            if (inner) {
-                x[j] = *reinterpret_cast<const vec*>(logits + v);
-            } else {
-#pragma unroll
-                for (int e = 0; e < M; ++e) x[j][e] = logits[min(max(v + e, 0), a.V - 1)];
-            }
-        }
-    }
+    Tile<T> x;
+    if (some) x.load(static_cast<const T*>(a.logits) + begin, t, a.V, lane);
+    T* probs = static_cast<T*>(a.probs) + begin;
 #pragma unroll
     for (int j = 0; j < J; ++j) {
-        const int v = v0 + (j * 64 + lane) * M;
-        vec y;
+        const int v = t * kTile + (j * 64 + lane) * M;
+        typename Vec16<T>::type y;
 #pragma unroll
         for (int e = 0; e < M; ++e) {
             y[e] = (T)0.f;
             if (some) {
-                const float l = to_f32((T)x[j][e]);
-                bool kept = l > minus_inf() && place(l, min(max(v + e, 0), a.V - 1)) >= r.cut;
+                const float l = to_f32((T)x.v[j][e]);
+                bool kept = l > minus_inf() && place(l, v + e) >= r.cut;
                 if (r.least > 0.0) kept = kept && weight(l, r.top, r.scale) >= r.least;
                 // (one power of two for the weight over the sum)
                 const double y0 = l == r.top ? 0.0 : ((double)l - (double)r.top) * r.scale;
                 y[e] = from_f32<T>(kept ? exp2_f32(y0 - r.sum) : 0.f);
             }
         }
-        if (inner) {
-            *reinterpret_cast<vec*>(probs + v) = y;
+        if ((t + 1) * kTile <= a.V) {
+            __builtin_memcpy(probs + v, &y, 16);
         } else {
 #pragma unroll
             for (int e = 0; e < M; ++e)
-                if (v + e >= 0 && v + e < a.V) probs[v + e] = y[e];
+                if (v + e < a.V) probs[v + e] = y[e];
         }
     }
 }
@@ -1428,7 +1423,7 @@ hipError_t launch_sample_t(const SampleArgs& a, hipStream_t stream) {
     sample_tiles_kernel<T><<<grid, block, 0, stream>>>(a);
     sample_rows_kernel<T><<<dim3((unsigned)a.R), dim3(kThreads), kRowBytes + (size_t)tiles * (tiles <= kGroupTiles ? 12 + 4 * kSampleGroups : 12), stream>>>(a);
     if (a.probs)
-        sample_probs_kernel<T><<<dim3((unsigned)(a.R * sample_row_groups(a.V))), block, 0, stream>>>(a);
+        sample_probs_kernel<T><<<grid, block, 0, stream>>>(a);
     return hipGetLastError();
 }
 

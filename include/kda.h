@@ -673,7 +673,7 @@ kda_status kda_cache_fold(int8_t* codes, float* scale, const void* win_k,
  *   workspace     : kda_sample_workspace_size(R, V) bytes, 16-byte aligned,
  *                   for this call alone until it has run (calls that may run at
  *                   the same time, captured ones among them, need their own)
- * 1 <= V <= KDA_MAX_VOCAB, R < 2^22, R * ceil((V + 7) / 4096) < 2^24, else
+ * 1 <= V <= KDA_MAX_VOCAB, R < 2^22, R * ceil(V / 4096) < 2^24, else
  * KDA_ERR_BAD_SHAPE; R == 0 is allowed (nothing is launched).  logits and
  * probs 16-byte aligned (their rows need not be), the arrays 4-byte.  Any overlap of token, probs or
  * workspace with another buffer is KDA_ERR_ALIAS.
