@@ -124,8 +124,7 @@ __global__ __launch_bounds__(256, 4) void cache_decode_kernel(CacheDecodeArgs a)
 
     const size_t vec = (size_t)unit * kD + 2 * lane, row0 = (size_t)unit * W * kD + 2 * lane;
     auto load = [](const void* p, size_t at) { return *reinterpret_cast<const pair*>(static_cast<const T*>(p) + at); };
-    // (256 x 96 states, windows of 8: 100 us with ordinary stores, 96 with streaming
-    // ones; the window's three rows alone, scattered lines of 19 MB, cost 13 us)
+    // (256 x 96 states, windows of 8: 111 us with ordinary stores, 106 with streaming ones)
     auto store = [](void* p, size_t at, pair x) {
         __builtin_nontemporal_store(x, reinterpret_cast<pair*>(static_cast<T*>(p) + at));
     };
