@@ -25,7 +25,7 @@
 // rounding of a running sum must not move.
 // What bounds it, 256 x 160,000 fp32 (0.16 GB): the first pass HBM, 33 us (4.9 TB/s;
 // 30 without weights); the second the slowest row, which one CU reads: 10 us without a
-// filter, 20 to 30 us where the list holds all that is kept, 80 us where a nucleus has
+// filter, 10 to 30 us where the list holds all that is kept, 65 to 90 us where a nucleus has
 // thousands of tokens (0.64 MB through one CU, some 25 fp64 and integer instructions a
 // logit).  The third pass, 192 x 50,021 bf16: 11 us (19 MB written, as much read where
 // something is kept).  One row of 32,000: 18.5 us, three launches' trips to memory and
@@ -116,6 +116,17 @@ __device__ __forceinline__ float exp2_f32(double y) {
     return __builtin_amdgcn_ldexpf(__builtin_amdgcn_exp2f((float)(y - (t - round))), (int)__builtin_bit_cast(uint64_t, t));
 }
 
+// the same in every lane, into scalar registers
+template <typename V>
+__device__ __forceinline__ V uniform(V x) {
+    uint32_t w[sizeof(V) / 4];
+    __builtin_memcpy(w, &x, sizeof(V));
+#pragma unroll
+    for (uint32_t& y : w) y = (uint32_t)__builtin_amdgcn_readfirstlane((int)y);
+    __builtin_memcpy(&x, w, sizeof(V));
+    return x;
+}
+
 // what a row is asked for
 struct Ask {
     double scale, p, least;
@@ -126,12 +137,12 @@ struct Ask {
         const float P = a.top_p ? a.top_p[row] : 1.f, m = a.min_p ? a.min_p[row] : 0.f;
         k = a.top_k ? a.top_k[row] : 0;
         greedy = !(T > 0.f);
-        scale = 1.44269504088896340736 / (greedy ? 1.0 : (double)T);
+        scale = uniform(1.44269504088896340736 / (greedy ? 1.0 : (double)T));
         by_k = k >= 1 && k < a.V;
         by_p = P < 1.f;
         by_m = m > 0.f;
-        p = P > 0.f ? (double)P : 0.0;
-        least = by_m ? (m < 1.f ? (double)m : 1.0) : 0.0;
+        p = uniform(P > 0.f ? (double)P : 0.0);
+        least = uniform(by_m ? (m < 1.f ? (double)m : 1.0) : 0.0);
     }
     // whether the sum of all weights takes part
     __device__ __forceinline__ bool sums() const { return !greedy && !by_k && (by_p || !by_m); }
@@ -177,22 +188,22 @@ struct Tile {
 #pragma unroll
         for (int j = 0; j < J; ++j) asm volatile("" : "+v"(v[j]));
     }
-    // the same piece by piece, f(logits, first token), in a loop: a quarter (a half) of the code
+    // the same piece by piece, f(logits, first token), in a loop: a quarter (a half) of the code;
+    // the tile is gone afterwards
     template <typename F>
-    __device__ __forceinline__ void pieces(int t, int lane, F&& f) const {
-        Tile x = *this;
+    __device__ __forceinline__ void pieces(int t, int lane, F&& f) {
 #pragma unroll 1
         for (int j = 0; j < J; ++j) {
             float l[M];
 #pragma unroll
-            for (int e = 0; e < M; ++e) l[e] = to_f32((T)x.v[0][e]);
+            for (int e = 0; e < M; ++e) l[e] = to_f32((T)v[0][e]);
             f(l, t * kTile + (j * 64 + lane) * M);
 #pragma unroll
-            for (int q = 0; q + 1 < J; ++q) x.v[q] = x.v[q + 1];
+            for (int q = 0; q + 1 < J; ++q) v[q] = v[q + 1];
         }
     }
     template <typename F>
-    __device__ __forceinline__ void each_in_turn(int t, int lane, F&& f) const {
+    __device__ __forceinline__ void each_in_turn(int t, int lane, F&& f) {
         pieces(t, lane, [&](const float* l, int i) {
 #pragma unroll
             for (int e = 0; e < M; ++e) f(l[e], i + e);
@@ -260,7 +271,8 @@ struct Entry {
 };
 // One workgroup a row.  Its state lies in LDS, where the functions below, which
 // are called and not inlined (their code is read once by every workgroup, from
-// far away: a short one is a fast one), find it.
+// far away: a short one is a fast one), find it.  They call nothing themselves, and so
+// need no stack.
 struct RowLds {
     Entry list[kCap];
     uint64_t bin_w[kBins];
@@ -301,7 +313,7 @@ __device__ __forceinline__ void count(RowLds& l, int bin, uint64_t w) {
 // All threads; the histogram is complete.  Returns the bin, -1 if none; the
 // sums before it, what it counts, and all sums are in LDS.
 template <bool kWeights>   // false: counts alone, in bin_n
-__device__ __noinline__ int cross(bool by_count, uint64_t target) {
+__device__ __forceinline__ int cross(bool by_count, uint64_t target) {
     KDA_ROW_LDS;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const uint32_t n = l.bin_n[threadIdx.x];
@@ -529,17 +541,16 @@ __device__ __noinline__ float expected(const __attribute__((address_space(3))) f
     return -(float)count * __logf(__builtin_fmaxf(1.f - share, 1.f / (float)(4 * count)));
 }
 
-template <typename V>
-__device__ __forceinline__ V uniform(V x) {
-    uint32_t w[sizeof(V) / 4];
-    __builtin_memcpy(w, &x, sizeof(V));
-#pragma unroll
-    for (uint32_t& y : w) y = (uint32_t)__builtin_amdgcn_readfirstlane((int)y);
-    __builtin_memcpy(&x, w, sizeof(V));
-    return x;
-}
-
-enum Found { kNot, kMissed, kFound };
+enum Found { kNot, kMissed, kFound };   // kNot: in a bin of too many
+struct Near {
+    Found found;
+    float from, border;   // logit > from, and not > border
+};
+struct Far {
+    uint32_t n;           // of the list; 0: nowhere
+    uint64_t lo, hi;      // places
+    uint64_t before_n, before_w;
+};
 constexpr int kSome = 4;   // tiles that one stands for
 
 template <typename T>
@@ -655,7 +666,7 @@ struct Row {
         constexpr int M = Tile<T>::M;
         start_list();
         if (!by_group) {
-            tiles_over(below, 1, [&](const Tile<T>& x, int t) {
+            tiles_over(below, 1, [&](Tile<T>& x, int t) {
                 uint32_t bits = 0;
                 x.each_in_turn(t, lane, [&](float v, int) { bits = 2 * bits + (v > below); });
                 append(t, bits);
@@ -702,9 +713,8 @@ struct Row {
     // and `kept`, of those that weigh `least`, in lane 63.  Their number is added to
     // `passed`; those over `from` and not over `border` go to the list.  A piece with many
     // of them is weighed in place, few are packed by a ring first (256 x 160,000 fp32, normal
-    // logits: by min-p 1e-4 114 us with the ring alone, 93 so; by top-p 0.99 127 and 129;
-    // everything in place 158, the share that weighs anything being small).
-    __device__ __forceinline__ void weigh(const Tile<T>& x, int t, float from, float border, double least, uint64_t& all,
+    // logits: by min-p 1e-4 110 us with the ring alone, 90 so; by top-p 0.99 121 and 124).
+    __device__ __forceinline__ void weigh(Tile<T>& x, int t, float from, float border, double least, uint64_t& all,
                                           uint64_t& kept, uint32_t& passed) const {
         constexpr int M = Tile<T>::M;
         const double c = 4503599627370496.0 / unit;   // (as in whole())
@@ -758,19 +768,23 @@ struct Row {
         append(t, bits);
     }
 
-    // The same as find(), over the row's tokens: `below` < logit < `above`, which
-    // weigh 2^high at most and, where weights are to reach `target`, 2^low at least
-    // (what weighs less cannot be where they do).  `off` is what those from `above` on
-    // weigh.  If it can be found within some bins, sums then holds each tile's weight
-    // of what is kept if it ends there and weighs `least`, and l.key_w the weights up
-    // to there.  kNot: it may be there all the same, in a bin of too many; kMissed: where
-    // some tiles were taken for all.  `all`, not 0: what all tokens weigh, of which those
-    // behind `target` are to be told from some tiles.
-    __device__ __forceinline__ Found find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
-                                               double low, double least, uint64_t all) const {
+    // what the tokens of this thread's bin weigh, taken at its middle
+    __device__ __forceinline__ double about(double high, double low) const {
+        KDA_ROW_LDS;
+        const float y = (float)high - ((float)threadIdx.x + 0.5f) * ((float)(high - low) * (1.f / (kBins - 1)));
+        return (double)((float)l.bin_n[threadIdx.x] * __builtin_amdgcn_exp2f(__builtin_fminf(y, 0.f))) * unit;
+    }
+    // Between which logits, of a number that fits the list, the row's tokens reach
+    // `target`, as find() has it, as far as can be told from a histogram of them: `below` <
+    // logit < `above`, which weigh 2^high at most and, where weights are to reach it, 2^low at
+    // least (what weighs less cannot be where they do).  `off` is what those from `above`
+    // on weigh.  `all`, not 0: what all tokens weigh, of which those behind `target` are to
+    // be told from some tiles.
+    __device__ __forceinline__ Near near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
+                                         double low, uint64_t all) const {
         KDA_ROW_LDS;
         const Bins bin_of(top, scale, high, low);
-        const int exact = !by_count && off == 0 ? kBins / 16 : 0;
+        const int exact = !by_count && off == 0 ? kBins / 4 : 0;
         if (threadIdx.x == 0) {
             l.above_w = 0;
             l.before_n = 0;
@@ -783,7 +797,7 @@ struct Row {
             uint32_t tokens = 0;   // of the tiles taken
             if ((int)threadIdx.x < tiles && taken((int)threadIdx.x, kSome)) tokens = (uint32_t)min(kTile, V - (int)threadIdx.x * kTile);
             float beyond = 0.f;   // (what weighs less than 2^low)
-            tiles_over(minus_inf(), kSome, [&](const Tile<T>& x, int t) {
+            tiles_over(minus_inf(), kSome, [&](Tile<T>& x, int t) {
                 x.each_in_turn(t, lane, [&](float v, int) {
                     if (!(v < above)) return;
                     const int b = bin_of(v);
@@ -805,9 +819,7 @@ struct Row {
             }
             __syncthreads();
             const double each = (double)V / (double)max(l.before_n, 1u);
-            const double y = high - (threadIdx.x + 0.5) * (high - low) / (kBins - 1);
-            const double w = threadIdx.x == kBins - 1 ? (double)l.above_w
-                                                      : l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0));
+            const double w = threadIdx.x == kBins - 1 ? (double)l.above_w : about(high, low);
             const uint64_t here_w = (uint64_t)(w * each);
             l.bin_w[threadIdx.x] = here_w;
             l.bin_n[threadIdx.x] = (uint32_t)(l.bin_n[threadIdx.x] * each);
@@ -817,13 +829,13 @@ struct Row {
             const uint64_t sum = wave_scan_whole(here_w);
             if (lane == 63) add(&l.above_w, sum);
             __syncthreads();
-            const uint64_t found = l.above_w, behind = all - target;
+            const uint64_t found = uniform(l.above_w), behind = all - target;
             aim = found > behind ? found - behind : 1;
         } else {
             // (where there are many tiles, every other one stands for two: thousands of tokens are off by a fraction of a
             // bin, and several are collected.  Not so for weights, of which a few tokens may be most.)
             const int step = by_count && tiles >= 64 ? 2 : 1;
-            tiles_over(below, step, [&](const Tile<T>& x, int t) {
+            tiles_over(below, step, [&](Tile<T>& x, int t) {
                 x.each_in_turn(t, lane, [&](float v, int) {
                     if (v > below && v < above) {
                         const int b = bin_of(v);
@@ -838,12 +850,11 @@ struct Row {
             __syncthreads();
             // (what a bin weighs: about its middle, but for the first ones, whose few tokens may be most of it)
             if (!by_count && (int)threadIdx.x >= exact) {
-                const double y = high - (threadIdx.x + 0.5) * (high - low) / (kBins - 1);
-                l.bin_w[threadIdx.x] = (uint64_t)(l.bin_n[threadIdx.x] * unit * exp2_neg(__builtin_fmax(__builtin_fmin(y, 0.0), -1020.0)));
+                l.bin_w[threadIdx.x] = (uint64_t)about(high, low);
             }
         }
         const int bin = cross<true>(by_count, aim);
-        if (bin < 0) return kMissed;
+        if (bin < 0) return Near{kMissed, 0.f, 0.f};
         // that bin and as many beside it as fit the list, up to eight: edges and estimated weights are not exact; 64
         // where some tiles stand for all
         const uint32_t here = l.here_n;
@@ -852,9 +863,16 @@ struct Row {
         const bool fit = here + wave_scan_whole(more) <= kCap - 256 && (all || lane < 8);
         const int beside = __builtin_popcountll(__ballot(fit));
         const int j0 = max(bin - beside, 0), j1 = min(bin + beside, kBins - 1);
-        if (here > kCap) return kNot;
+        if (here > kCap) return Near{kNot, 0.f, 0.f};
         const float over = j0 > 0 ? bin_of.edge((float)j0) : __builtin_inff(), from = j1 < kBins - 1 ? __builtin_fmaxf(bin_of.edge(j1 + 1.f), below) : below;
-        if (!(from < over)) return kNot;
+        // (what is from `above` on is over, wherever bin 0 begins)
+        return Near{from < over ? kFound : kNot, from, __builtin_fminf(over, under(above))};
+    }
+    // Those tokens to the list (returned: their number), each tile's weight of those over
+    // them that weigh `least` to sums, of all over them to l.above_w, and their number to
+    // l.before_n.
+    __device__ __forceinline__ uint32_t collect(bool by_count, float from, float border, double least) const {
+        KDA_ROW_LDS;
         if (threadIdx.x == 0) {
             l.above_w = 0;
             l.before_n = 0;
@@ -863,9 +881,7 @@ struct Row {
         start_list();
         uint64_t over_w = 0;
         uint32_t passed = 0;   // of all lanes
-        // (what is from `above` on is over, wherever bin 0 begins)
-        const float border = __builtin_fminf(over, under(above));
-        tiles_over(from, 1, [&](const Tile<T>& x, int t) {
+        tiles_over(from, 1, [&](Tile<T>& x, int t) {
             uint64_t w, kept;
             weigh(x, t, from, border, least, w, kept, passed);
             over_w += w;
@@ -876,25 +892,21 @@ struct Row {
             add(&l.above_w, over_w);
             if (by_count) atomicAdd(&l.before_n, passed);
         }
-        const uint32_t n = listed();
-        const uint64_t base = by_count ? (uint64_t)l.before_n : l.above_w;
-        const uint64_t first = border < top ? place(border, 0) : place(top, 0), last = from > minus_inf() ? place(from, 0) : 1;
-        __syncthreads();
-        if (n > kCap || base >= target || !find(kByPlace, n, last, first, by_count, target - base)) return kMissed;
-        const uint64_t cut = l.key;
-        __syncthreads();
-        if (threadIdx.x == 0) l.key_w += l.above_w;
+        return uniform(listed());
+    }
+    // What of the list is kept to sums: from place `cut` on, and of weight `least`.
+    __device__ __forceinline__ void keep(uint32_t n, uint64_t cut, double least) const {
+        KDA_ROW_LDS;
         for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
             const Entry x = l.list[i];
             if (x.place >= cut && weight_of(logit_of(x.place)) >= least) add(&sums()[index_of(x.place) / kTile], x.w);
         }
         __syncthreads();
-        return kFound;
     }
-    // The same wherever it lies, without the sums: a histogram of the weights
-    // themselves, and as many levels inside one bin as it takes (thousands of equal
-    // logits, a distribution that fits no bins).
-    __device__ __forceinline__ bool find_far(bool by_count, uint64_t target) const {
+    // The same as near() and collect() wherever it lies, without the sums: a histogram of
+    // the weights themselves, and as many levels inside one bin as it takes (thousands of
+    // equal logits, a distribution that fits no bins).
+    __device__ __forceinline__ Far far(bool by_count, uint64_t target) const {
         KDA_ROW_LDS;
         uint32_t base_n = 0, here = kCap + 1;
         uint64_t base_w = 0, lo = 1, hi = place(top, 0);
@@ -903,7 +915,7 @@ struct Row {
             const int shift = bits > 10 ? bits - 10 : 0;
             __syncthreads();
             clear_bins(l);
-            tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
+            tiles_over(minus_inf(), 1, [&](Tile<T>& x, int t) {
                 x.each_in_turn(t, lane, [&](float v, int i) {
                     if (v > minus_inf()) {
                         const uint64_t k = place(v, i);
@@ -913,16 +925,16 @@ struct Row {
             });
             __syncthreads();
             const int b = cross<true>(by_count, target - (by_count ? (uint64_t)base_n : base_w));
-            if (b < 0) return false;
-            base_n += l.before_n;
-            base_w += l.before_w;
-            here = l.here_n;
+            if (b < 0) return Far{0, 0, 0, 0, 0};
+            base_n += uniform(l.before_n);
+            base_w += uniform(l.before_w);
+            here = uniform(l.here_n);
             hi -= (uint64_t)b << shift;
             const uint64_t width = ((uint64_t)1 << shift) - 1;
             lo = hi - lo > width ? hi - width : lo;
         }
         start_list();
-        tiles_over(minus_inf(), 1, [&](const Tile<T>& x, int t) {
+        tiles_over(minus_inf(), 1, [&](Tile<T>& x, int t) {
             x.each_in_turn(t, lane, [&](float v, int i) {
                 if (v > minus_inf()) {
                     const uint64_t k = place(v, i);
@@ -933,11 +945,7 @@ struct Row {
                 }
             });
         });
-        const uint32_t n = min(listed(), kCap);
-        if (!find(kByPlace, n, lo, hi, by_count, target - (by_count ? (uint64_t)base_n : base_w))) return false;
-        if (threadIdx.x == 0) l.key_w += base_w;
-        __syncthreads();
-        return true;
+        return Far{min(listed(), kCap), lo, hi, base_n, base_w};
     }
     // each tile's weight of what is kept
     __device__ __forceinline__ void sum_kept(uint64_t cut, double least) const {
@@ -945,17 +953,16 @@ struct Row {
         __syncthreads();
         const float from = cut > 1 ? logit_of(cut) : minus_inf(), below = cut > 1 ? under(from) : from;
         const int border = index_of(cut);
-        tiles_over(below, 1, [&](const Tile<T>& x, int t) {
+        tiles_over(below, 1, [&](Tile<T>& x, int t) {
             uint64_t all, kept;
             uint32_t passed = 0;
-            Tile<T> y = x;   // (of logits equal to the cut's, those up to its index)
-            if (cut > 1)
+            if (cut > 1)   // (of logits equal to the cut's, those up to its index)
 #pragma unroll
                 for (int j = 0; j < Tile<T>::J; ++j)
 #pragma unroll
                     for (int e = 0; e < Tile<T>::M; ++e)
-                        if (to_f32((T)y.v[j][e]) == from && t * kTile + (j * 64 + lane) * Tile<T>::M + e > border) y.v[j][e] = (T)minus_inf();
-            weigh(y, t, below, below, least, all, kept, passed);
+                        if (to_f32((T)x.v[j][e]) == from && t * kTile + (j * 64 + lane) * Tile<T>::M + e > border) x.v[j][e] = (T)minus_inf();
+            weigh(x, t, below, below, least, all, kept, passed);
             if (lane == 63) sums()[t] = kept;
         });
         __syncthreads();
@@ -1013,13 +1020,36 @@ struct Row {
 
 template <typename T>
 __device__ __noinline__ uint32_t gather(float below, bool by_group) { return Row<T>::here().gather(below, by_group); }
+// The same as find(), over the row's tokens, by near() and collect().  If it is found, sums
+// holds each tile's weight of what is kept if it ends there and weighs `least`, and
+// l.key_w the weights up to there.  kNot, kMissed: it may be there all the same.
 template <typename T>
-__device__ __noinline__ Found find_near(bool by_count, uint64_t target, float above, uint64_t off, float below, double high,
-                                        double low, double least, uint64_t all) {
-    return Row<T>::here().find_near(by_count, target, above, off, below, high, low, least, all);
+__device__ __forceinline__ Found find_near(const Row<T>& r, bool by_count, uint64_t target, float above, uint64_t off, float below,
+                                           double high, double low, double least, uint64_t all) {
+    KDA_ROW_LDS;
+    const Near at = r.near(by_count, target, above, off, below, high, low, all);
+    if (at.found != kFound) return at.found;
+    const uint32_t n = r.collect(by_count, at.from, at.border, least);
+    const uint64_t base = uniform(by_count ? (uint64_t)l.before_n : l.above_w);
+    const uint64_t first = at.border < r.top ? place(at.border, 0) : place(r.top, 0), last = at.from > minus_inf() ? place(at.from, 0) : 1;
+    __syncthreads();
+    if (n > kCap || base >= target || !find(kByPlace, n, last, first, by_count, target - base)) return kMissed;
+    const uint64_t cut = l.key;
+    __syncthreads();
+    if (threadIdx.x == 0) l.key_w += l.above_w;
+    r.keep(n, cut, least);
+    return kFound;
 }
+// The same by far(), without the sums.
 template <typename T>
-__device__ __noinline__ bool find_far(bool by_count, uint64_t target) { return Row<T>::here().find_far(by_count, target); }
+__device__ __forceinline__ bool find_far(const Row<T>& r, bool by_count, uint64_t target) {
+    KDA_ROW_LDS;
+    const Far at = r.far(by_count, target);
+    if (at.n == 0 || !find(kByPlace, at.n, at.lo, at.hi, by_count, target - (by_count ? at.before_n : at.before_w))) return false;
+    if (threadIdx.x == 0) l.key_w += at.before_w;
+    __syncthreads();
+    return true;
+}
 
 // the weight that top-p asks for, of that of what it is taken from
 __device__ __forceinline__ uint64_t share_of(double p, uint64_t w) {
@@ -1034,51 +1064,54 @@ struct Kept {
     uint64_t cut, sum;
 };
 template <typename T>
-__device__ __noinline__ Kept over_row(int k, bool by_p, double p, double least, uint64_t all, float listed_over, uint64_t listed_w) {
+__device__ __forceinline__ Kept over_row(int k, bool by_p, double p, double least, uint64_t all, float listed_over, uint64_t listed_w) {
     KDA_ROW_LDS;
     const Row<T> r = Row<T>::here();
     __syncthreads();
     uint64_t cut = 1, sum = all;
     bool summed = false;
-    if (k) {
-        summed = find_near<T>(true, (uint64_t)k, __builtin_inff(), 0, minus_inf(), 0.0, -66.4, least, 0) == kFound;
-        const bool ok = summed || find_far<T>(true, (uint64_t)k);
-        if (ok) cut = l.key;
-        sum = ok ? l.key_w : l.total_w;
-        __syncthreads();
-        summed = summed && !by_p;
-    }
-    if (by_p) {
-        // the last one kept weighs at least (what lies behind it) / V; where the list did not reach the share, it
-        // lies below
-        const uint64_t target = share_of(p, sum);
-        const double behind = ((double)sum - (double)target) / ((double)r.V * r.unit);
-        double bottom = behind > 0.0 ? log2(behind) - 0.01 : -66.4;
-        bottom = bottom < -66.4 ? -66.4 : bottom;
-        float above = __builtin_inff();
-        double high = 0.0;
-        if (listed_w && listed_w < target) {
-            above = of_key(key_of(listed_over) + 1);
-            high = ((double)above - (double)r.top) * r.scale;
-        } else {
-            listed_w = 0;
-        }
-        if (!(high < 0.0)) high = 0.0;
-        if (bottom > high - 0.01) bottom = high - 0.01;
-        const double low_x = (double)r.top + bottom / r.scale;
-        const float from = !(low_x > -3e38) || r.top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
-        Found found = kMissed;
+    // the first k; the share, from some tiles; from all of them (a loop: each function stands here once)
+#pragma unroll 1
+    for (int step = k ? 0 : 1; step < 3; ++step) {
         // (from a quarter of the tiles the place of the cut is off by some hundred tokens, of over a thousand that are
-        // collected; beyond 256 tiles by too many.  256 x 160,000 fp32 by top-p 0.5, 0.9, 0.99: 155, 143, 157 us from all
-        // tiles, 98, 116, 129 from a quarter, 94, 111, 205 from an eighth.  Fewer than 32 take no longer than the rest.)
-        if (!k && r.tiles >= 32 && r.tiles <= 256) {
-            found = find_near<T>(false, target, above, listed_w, from, high, bottom, least, sum);
-            __syncthreads();
+        // collected; beyond 256 tiles by too many.  256 x 160,000 fp32 by top-p 0.5, 0.9, 0.99: 115, 129, 146 us from all
+        // tiles, 97, 111, 124 from a quarter, 92, 106, 198 from an eighth.  Fewer than 32 take no longer than the rest.)
+        if (step > 0 && !by_p) break;
+        if (step == 1 && (k || r.tiles < 32 || r.tiles > 256)) continue;
+        const bool by_count = step == 0;
+        uint64_t target = (uint64_t)k, off = 0;
+        float above = __builtin_inff(), from = minus_inf();
+        double high = 0.0, bottom = -66.4;
+        if (!by_count) {
+            // the last one kept weighs at least (what lies behind it) / V; where the list did not reach the share, it
+            // lies below
+            target = share_of(p, sum);
+            const double behind = ((double)sum - (double)target) / ((double)r.V * r.unit);
+            if (behind > 0.0) bottom = (double)__builtin_fmaxf(__builtin_amdgcn_logf((float)behind) - 0.01f, -66.4f);   // (to base 2)
+            if (listed_w && listed_w < target) {
+                off = listed_w;
+                above = of_key(key_of(listed_over) + 1);
+                high = ((double)above - (double)r.top) * r.scale;
+            }
+            if (!(high < 0.0)) high = 0.0;
+            if (bottom > high - 0.01) bottom = high - 0.01;
+            const double low_x = (double)r.top + bottom / r.scale;
+            from = !(low_x > -3e38) || r.top == __builtin_inff() ? minus_inf() : under(under(under((float)low_x)));
         }
-        if (found == kMissed) found = find_near<T>(false, target, above, listed_w, from, high, bottom, least, 0);
+        const Found found = find_near<T>(r, by_count, target, above, off, from, high, bottom, least, step == 1 ? sum : 0);
+        if (step == 1 && found == kMissed) {
+            __syncthreads();
+            continue;
+        }
         summed = found == kFound;
-        if (summed || find_far<T>(false, target)) cut = max(cut, l.key);
+        const bool ok = summed || find_far<T>(r, by_count, target);
+        if (ok) cut = max(cut, uniform(l.key));
+        if (by_count) {
+            sum = uniform(ok ? l.key_w : l.total_w);
+            summed = summed && !by_p;
+        }
         __syncthreads();
+        if (!by_count) break;
     }
     if (!summed) r.sum_kept(cut, least);
     return Kept{cut, r.total()};
@@ -1099,7 +1132,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     r.wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const Ask ask(a, row);
     const float u0 = a.u ? a.u[row] : 0.f;
-    const double u = u0 > 0.f ? (u0 < 1.f ? (double)u0 : 1.0) : 0.0;
+    const double u = uniform(u0 > 0.f ? (u0 < 1.f ? (double)u0 : 1.0) : 0.0);
 
     float top = minus_inf(), low = __builtin_inff();   // largest; smallest of full tiles that are not empty,
     float least_top = __builtin_inff();                // of groups that are not
@@ -1128,7 +1161,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
     }
     if (threadIdx.x == 0) l.token = V;
     __syncthreads();
-    top = wave_top(r.lane < kWaves ? l.part_f[0][r.lane] : minus_inf());
+    top = uniform(wave_top(r.lane < kWaves ? l.part_f[0][r.lane] : minus_inf()));
     low = -wave_top(r.lane < kWaves ? -l.part_f[1][r.lane] : minus_inf());
     least_top = -wave_top(r.lane < kWaves ? -l.part_f[2][r.lane] : minus_inf());
     r.top = top;
@@ -1159,7 +1192,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         return;
     }
     if (ask.greedy) {
-        r.tiles_over(under(top), 1, [&](const Tile<T>& x, int t) {
+        r.tiles_over(under(top), 1, [&](Tile<T>& x, int t) {
             int first = V;
             x.each(t, r.lane, [&](float v, int i) {
                 if (v == top) first = min(first, i);

@@ -1,8 +1,6 @@
 """Registers of the 8-bit cache's and of sampling's kernels: the wavefronts per SIMD
 that their notes count on (a workgroup of four wavefronts is one of them on every
-SIMD of a compute unit), no scratch but for a few registers of the fold of long fp32
-windows and the rows of sampling, whose calls keep
-their return addresses and arguments there."""
+SIMD of a compute unit), no scratch."""
 import pytest
 
 from gated_delta_rule_27_amd import build
@@ -15,10 +13,10 @@ WAVES = [
     ("kda_cache.hip", "cache_fold_kernel", "IDF16bLi8E", 5, 0),
     ("kda_cache.hip", "cache_fold_kernel", "IfLi8E", 4, 0),
     ("kda_cache.hip", "cache_fold_kernel", "IDF16bLi16E", 3, 0),
-    ("kda_cache.hip", "cache_fold_kernel", "IfLi16E", 3, 32),
+    ("kda_cache.hip", "cache_fold_kernel", "IfLi16E", 3, 0),
     ("kda_cache_decode.hip", "cache_decode_kernel", "", 4, 0),
     ("kda_sample.hip", "sample_tiles_kernel", "", 8, 0),
-    ("kda_sample.hip", "sample_rows_kernel", "", 4, 256),       # one workgroup of sixteen
+    ("kda_sample.hip", "sample_rows_kernel", "", 4, 0),       # one workgroup of sixteen
     ("kda_sample.hip", "sample_probs_kernel", "", 8, 0),
 ]
 
