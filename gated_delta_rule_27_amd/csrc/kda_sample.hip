@@ -1241,6 +1241,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         uint64_t listed_w = 0, about_w = 0;
         auto share = [&](uint64_t w) { return share_of(ask.p, w); };
         for (int attempt = 0;; ++attempt) {
+            if (attempt == 1 && count <= 128) attempt = 2;   // (the same list again)
             below = top;   // (none)
             sure = V <= (int)kCap;
             if (sure) {
