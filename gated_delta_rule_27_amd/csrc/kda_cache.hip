@@ -9,8 +9,8 @@
 // All three move memory: a workgroup of 256 threads holds one state in registers (64
 // values a thread) and passes the codes, which lie the other way round, through LDS;
 // every global access is whole lines.  256 x 96 states: stored in 364 us (2.03 GB,
-// 5.6 TB/s), folded with 8 bf16 tokens in 179 us (0.98 GB, 5.5 TB/s; 4 tokens 145 us,
-// 6.3 TB/s); 192 x 96 loaded in 273 us (1.52 GB, 5.6 TB/s).  A large device copy
+// 5.6 TB/s), folded with 8 bf16 tokens in 178 us (0.98 GB, 5.5 TB/s; 4 tokens 145 us,
+// 6.3 TB/s); 192 x 96 loaded in 268 us (1.52 GB, 5.7 TB/s).  A large device copy
 // reaches 4.7 TB/s.  One state each of 96 heads: 4.6 us to store, a launch and one trip
 // through the workgroup.
 #include "kda.h"
@@ -288,10 +288,10 @@ __global__ __launch_bounds__(256, kWindow ? 3 : 5) void cache_load_kernel(CacheM
 // of column 16 T + l, so that the window's updates are products of 16 x 4 and 4 x 16
 // (exact fp32 factors), a row's largest magnitude lies in 16 lanes, and four rows'
 // codes of a column are one dword here, too.  (With rank-one updates by the vector unit
-// 256 x 96 states and 8 tokens took 311 us, not 179.)  Two instances by the longest
+// 256 x 96 states and 8 tokens took 311 us, not 178.)  Two instances by the longest
 // window: the LDS of a short one lets more workgroups in (192 x 96 states, windows of 8,
 // bf16 and fp32: 164 and 150 us, by the instance for 16 189 and 216); the registers are
-// bounded to match it (fp32, 16: 298 us at three workgroups a CU, 351 at two).
+// bounded to match it (fp32, 16: 271 us at three workgroups a CU, 351 at two).
 template <typename T, int kMost>
 __global__ __launch_bounds__(256, sizeof(T) * kMost <= 16 ? 5 : kMost <= 8 ? 4 : 3) void cache_fold_kernel(CacheMoveArgs a) {
     __shared__ __align__(16) union {

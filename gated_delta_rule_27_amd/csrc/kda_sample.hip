@@ -23,11 +23,11 @@
 // Weights are taken in 64 bits and added up as whole numbers of 2^-F: their sums
 // are the same in any order, and the drawn token is a whole number, too, which a
 // rounding of a running sum must not move.
-// What bounds it, 256 x 160,000 fp32 (0.16 GB): the first pass HBM, 33 us (4.9 TB/s;
+// What bounds it, 256 x 160,000 fp32 (0.16 GB): the first pass HBM, 35 us (4.6 TB/s;
 // 30 without weights); the second the slowest row, which one CU reads: 10 us without a
 // filter, 10 to 30 us where the list holds all that is kept, 65 to 90 us where a nucleus has
 // thousands of tokens (0.64 MB through one CU, some 25 fp64 and integer instructions a
-// logit).  The third pass, 192 x 50,021 bf16: 11 us (19 MB written, as much read where
+// logit).  The third pass, 192 x 50,021 bf16: 10 us (19 MB written, as much read where
 // something is kept).  One row of 32,000: 18.5 us, three launches' trips to memory and
 // the second one's instructions, fetched as they run.
 #include "kda.h"
@@ -44,11 +44,12 @@ constexpr int kPer = kTile / 64;
 constexpr int kThreads = 1024, kWaves = kThreads / 64;
 constexpr int kBins = kThreads;
 constexpr uint32_t kCap = 2048;        // tokens of the list
-constexpr uint32_t kDense = 96;        // tokens of a piece's 256 (512) that are weighed in place
-constexpr uint32_t kRing = 256;
 // of them, that are counted pair by pair (one row of 32,000 with top-k some hundred and top-p: 18 us, 21 by histograms;
 // top-k 300 the other way round: 27 by histograms, 50 by pairs)
 constexpr uint32_t kFew = 192;
+constexpr uint32_t kDense = 96;        // tokens of a piece's 256 (512) from which on they are weighed in place
+constexpr uint32_t kRing = 256;        // 63 and a piece's fewer ones fit
+static_assert(63 + kDense <= kRing, "the ring's length");
 constexpr int kGroupTiles = 512;       // most tiles whose groups' maxima are kept (32 KB)
 constexpr int kIndexBits = 22;         // KDA_MAX_VOCAB
 constexpr uint64_t kIndexMask = (1u << kIndexBits) - 1;
