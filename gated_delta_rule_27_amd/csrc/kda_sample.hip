@@ -974,47 +974,49 @@ struct Row {
         for (int t0 = 0; t0 < tiles; t0 += 64) s += wave_scan_whole(t0 + lane < tiles ? sums()[t0 + lane] : (uint64_t)0);
         return lane_value(s, 63);
     }
-    // The first token at which the running sum of the kept weights reaches `target`,
-    // from the tiles' sums.  All threads; the result is l.token's afterwards.
-    __device__ __forceinline__ void draw(uint64_t target, uint64_t cut, double least) const {
+    // The first token at which the running sum of the kept weights reaches `target` of
+    // `sum`, from the tiles' sums.  Inside the tile weights are counted in 2^-50 of its own
+    // largest and share the tile's sum in proportion: it may be made up of tokens that
+    // weigh less than half of 2^-F each, and so be nothing one by one (a row of one token
+    // and a tail 34 nats under it).  A tile with a sum has a kept token, its largest, so one
+    // that is kept is drawn whatever u is.  All threads; the result is l.token's afterwards.
+    __device__ __forceinline__ void draw(uint64_t target, uint64_t sum, uint64_t cut, double least) const {
         KDA_ROW_LDS;
         int tile = -1;
-        uint64_t base = 0, run = 0;
+        uint64_t base = 0, run = 0, own = 0;
         for (int t0 = 0; t0 < tiles && tile < 0; t0 += 64) {
-            const uint64_t incl = run + wave_scan_whole(t0 + lane < tiles ? sums()[t0 + lane] : (uint64_t)0);
+            const uint64_t mine = t0 + lane < tiles ? sums()[t0 + lane] : (uint64_t)0;
+            const uint64_t incl = run + wave_scan_whole(mine);
             const uint64_t hit = __ballot(incl >= target);
             if (hit) {
                 const int i = __builtin_ctzll(hit);
                 tile = t0 + i;
-                base = i ? lane_value(incl, i - 1) : run;
+                own = lane_value(mine, i);
+                base = lane_value(incl, i) - own;
             }
             run = lane_value(incl, 63);
         }
         tile = max(tile, 0);
         const int i = tile * kTile + (int)threadIdx.x;
+        const float largest = tops()[tile];
         uint64_t w = 0;
         if (i < V) {
             const float x = logit(i);
-            if (x > minus_inf() && place(x, i) >= cut) {
-                const double y = weight_of(x);
-                w = y >= least ? whole(y) : 0;
-            }
+            if (x > minus_inf() && place(x, i) >= cut && weight_of(x) >= least)
+                w = __builtin_bit_cast(uint64_t, weight(x, largest, scale) + 4.0) - __builtin_bit_cast(uint64_t, 4.0);
         }
-        uint64_t sum = wave_scan_whole(w);
-        if (lane == 63) l.part_w[wave] = sum;
-        if (threadIdx.x == 0) {
-            l.token = V;
-            l.n = 0;
-        }
+        uint64_t upto = wave_scan_whole(w);
+        if (lane == 63) l.part_w[wave] = upto;
+        if (threadIdx.x == 0) l.token = V;
         __syncthreads();
         const uint64_t parts = wave_scan_whole(lane < kWaves ? l.part_w[lane] : (uint64_t)0);
-        sum += base + (wave > 0 ? lane_value(parts, wave - 1) : 0);
-        const uint64_t hit = __ballot(w != 0 && sum >= target), any = __ballot(w != 0);
+        if (wave > 0) upto += lane_value(parts, wave - 1);
+        const uint64_t whole_tile = lane_value(parts, kWaves - 1), before = target - 1 - base;
+        // upto / whole_tile > before / own, in 128 bits; u = 1: the last one
+        const uint64_t a = __umul64hi(upto, own), b = __umul64hi(before, whole_tile);
+        const bool there = target >= sum ? upto == whole_tile : a > b || (a == b && upto * own > before * whole_tile);
+        const uint64_t hit = __ballot(w != 0 && there);
         if (hit && lane == 0) atomicMin(&l.token, i + __builtin_ctzll(hit));
-        if (any && lane == 0) atomicMax(&l.n, (uint32_t)(i + 63 - __builtin_clzll(any)));
-        __syncthreads();
-        // (a tile's sum is rounded once, its tokens' one by one: then it is the last)
-        if (threadIdx.x == 0 && l.token == V) l.token = (int)l.n;
         __syncthreads();
     }
 };
@@ -1389,7 +1391,7 @@ __global__ __launch_bounds__(kThreads) void sample_rows_kernel(SampleArgs a) {
         out.cut = cut;
         if (!drawn) out.least = ask.least;   // (else the cut has it)
     }
-    if (a.u && !drawn) r.draw(min((uint64_t)(u * (double)sum) + 1, sum), out.cut, out.least);
+    if (a.u && !drawn) r.draw(min((uint64_t)(u * (double)sum) + 1, sum), sum, out.cut, out.least);
     if (threadIdx.x == 0) {
         if (a.u) a.token[row] = l.token;
         if (a.probs) out.sum = log2((double)sum / r.unit);

@@ -1,0 +1,109 @@
+"""Draws from rows whose tails weigh next to nothing one token at a time, and something
+together: masked tokens are never drawn, and what is drawn lies at its random number.
+
+Sums are whole numbers of 2^-F of the largest weight, F = 62 minus the vocabulary's bits
+(50 at most).  Token by token each is off by half of one at the most, V 2^-(F + 1) in
+all; the sums' own roundings, 1e-12, come on top."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import case, need_gpu, np_
+from test_gpu_sample import DT, INF, NAN, gpu
+
+pytestmark = pytest.mark.gpu
+
+
+def bound(V):
+    return V * 2.0 ** -(min(62 - V.bit_length(), 50) + 1) + 1e-12
+
+
+def drawn_at(l, token, u, T=1.0, keep=None):
+    """The kept token's share of the row from before it to after it holds u, within the bound."""
+    l = np.asarray(l, np.float64)
+    with np.errstate(invalid="ignore"):
+        w = np.exp((l - l.max()).astype(np.longdouble) / np.longdouble(T))
+    if keep is not None:
+        w = np.where(keep, w, 0)
+    assert w[token] > 0, f"token {token} of logit {l[token]} weighs nothing"
+    cum = np.cumsum(w) / w.sum()
+    before = cum[token - 1] if token else 0
+    off = max(float(before) - u, u - float(cum[token]))
+    assert off <= bound(len(l)), f"token {token} holds {before} to {cum[token]}, u = {u}"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [1025, 32000, 160000])
+@pytest.mark.parametrize("tail", [-31.0, -33.0, -34.0, -36.0, -39.0])
+def test_a_masked_token_is_never_drawn_beside_a_thin_tail(V, dtype, tail):
+    kda = need_gpu()
+    case(f"thin tail V={V} {dtype} {tail}")
+    heads = [(V // 2,), (V - 1,), (1,), (V // 5, V - 7), (V // 3, V // 2)]     # (rows of one token, and of two equal ones)
+    x = torch.full((len(heads), V), tail, device="cuda")
+    for r, at in enumerate(heads):
+        x[r, list(at)] = 0.0
+        x[r, 0] = -INF
+    x = x.to(DT[dtype])
+    l = np_(x)
+    # (whether the tail's part of the first and of the last tile of 1024 is a unit)
+    some = np.exp(tail) * min(1022, (V - 1) % 1024 + 1) * 2.0 ** min(62 - V.bit_length(), 50) >= 1
+    for u in (0.0, NAN, 2.0 ** -24, 0.25, 0.5, 1 - 2.0 ** -24, 1.0):
+        token, probs = kda.kda_sample(x, gpu([u] * len(heads)), probs=True)
+        torch.cuda.synchronize()
+        assert (probs.gather(1, token[:, None].long()) > 0).all(), u
+        for r in range(len(heads)):
+            t, at = int(token[r]), 0.0 if u != u else u
+            drawn_at(l[r], t, at)
+            # (inside a tile weights count in 2^-50 of its largest: beside a 1 a tail of -36 is 0.26 of that, nothing.
+            # So these hold where the tile at that end has no head, or the tail's tokens are more than half of 2^-50)
+            thick = np.exp(tail) * 2.0 ** 50 > 0.5
+            if some and at == 0.0 and (thick or min(heads[r]) >= 1024):
+                assert t == 1, (r, t)       # the first one that is not masked
+            if some and at == 1.0 and (thick or max(heads[r]) // 1024 < (V - 1) // 1024):
+                assert t == V - 1, (r, t)   # the last one
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("u", [0.0, NAN, 1.0])
+def test_masked_tiles_before_and_behind(u, dtype):
+    """A masked first tile, one of a thin tail, and one token of weight far behind; and the other way round."""
+    kda = need_gpu()
+    V = 160000
+    case(f"masked tiles u={u} {dtype}")
+    x = torch.full((4, V), -INF, device="cuda")
+    x[0, 1024:2048], x[0, 5000] = -35.0, 0.0
+    x[1, 1030:1033], x[1, 5000] = -35.0, 0.0           # (less than a unit together: nothing)
+    x[2, 5000], x[2, 150000:150900] = 0.0, -33.0
+    x[3, 0], x[3, 100000:] = 0.0, -34.0
+    x = x.to(DT[dtype])
+    token, probs = kda.kda_sample(x, gpu([u] * 4), probs=True)
+    torch.cuda.synchronize()
+    assert token.tolist() == ([5000, 5000, 150899, V - 1] if u == 1.0 else [1024, 5000, 5000, 0])
+    assert (probs.gather(1, token[:, None].long()) > 0).all()
+
+
+@pytest.mark.parametrize("V", [3000, 32000, 160001])
+def test_thin_tails_behind_every_filter(V):
+    """Kept or not, by each filter: the token is kept and lies at its random number."""
+    kda = need_gpu()
+    case(f"thin tails, filters V={V}")
+    T = [1.0, 0.5, 3.0, 1.0]
+    x = torch.full((4, V), -34.0, device="cuda")
+    x[:, ::2] -= 0.5
+    x[0, V // 2] = 0.0
+    x[1] *= 0.5
+    x[1, [7, V - 9]] = 0.0
+    x[2] *= 3.0
+    x[2, V - 1] = 0.0
+    x[3, 40:80] = -1.0
+    x[:, 0] = -INF
+    l = np_(x)
+    for k, p, m in ((None, None, 1e-17), (None, None, 1e-15), ([V - 1] * 4, None, None), ([V // 2] * 4, None, 1e-16),
+                    ([5] * 4, None, None), (None, [1 - 2.0 ** -24] * 4, None), (None, [0.9] * 4, 1e-15)):
+        m = None if m is None else [m] * 4
+        for u in (0.0, 0.5, 1 - 2.0 ** -24, 1.0):
+            token, probs = kda.kda_sample(x, gpu([u] * 4), gpu(T), gpu(k, torch.int32), gpu(p), gpu(m), probs=True)
+            torch.cuda.synchronize()
+            keep = np_(probs) > 0
+            for r in range(4):
+                drawn_at(l[r], int(token[r]), u, T[r], keep[r])
