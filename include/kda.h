@@ -658,10 +658,15 @@ kda_status kda_cache_fold(int8_t* codes, float* scale, const void* win_k,
  * once.  The token drawn is the smallest kept i with
  *     (sum of the kept w over 0..i)  >  u * (sum of the kept w),
  * -1 where a row has no weight at all (its probabilities are then all 0).
- * Weights are e^x in 64 bits, added up as whole numbers of 2^-39 of the largest
- * or less, so a token is what 64-bit sums give unless a border lies within about
- * 1e-11 of them (for vocabularies of 160,000; 1e-9 for millions).  Results do not
- * depend on the launch.
+ * Weights are e^x in 64 bits, added up as whole numbers of 2^-F of the largest
+ * (F = 62 less the bits of V, 50 at most), so that results do not depend on the
+ * launch or the order.  A token that weighs less than half of 2^-F counts for
+ * nothing in them: the share of a nucleus and the place of u are met within
+ * V * 2^-(F + 1) of the sum of the weights, 1.1e-10 for 32,000 tokens, 4.5e-9 for
+ * 160,000 and 4e-6, which is more than a step of an fp32 u or top_p, for four
+ * million.  Elsewhere tokens are what exact sums give.  Without a filter tiles of
+ * 1024 tokens are counted so, not tokens: within a thousandth of that, and 1e-12.
+ * What is drawn is always kept, and has a probability above 0.
  *
  *   logits, probs : [R, V] dt;  probs NULL = not wanted
  *   u             : [R] fp32 in [0, 1) (clamped; NaN counts as 0); NULL = no

@@ -3,7 +3,7 @@ together: masked tokens are never drawn, and what is drawn lies at its random nu
 
 Sums are whole numbers of 2^-F of the largest weight, F = 62 minus the vocabulary's bits
 (50 at most).  Token by token each is off by half of one at the most, V 2^-(F + 1) in
-all; the sums' own roundings, 1e-12, come on top."""
+all, and by tiles of 1024 each of those; the sums' own roundings, 1e-12, come on top."""
 import numpy as np
 import pytest
 import torch
@@ -15,7 +15,7 @@ pytestmark = pytest.mark.gpu
 
 
 def bound(V):
-    return V * 2.0 ** -(min(62 - V.bit_length(), 50) + 1) + 1e-12
+    return (V + V // 1024 + 1) * 2.0 ** -(min(62 - V.bit_length(), 50) + 1) + 1e-12
 
 
 def drawn_at(l, token, u, T=1.0, keep=None):
@@ -107,3 +107,32 @@ def test_thin_tails_behind_every_filter(V):
             keep = np_(probs) > 0
             for r in range(4):
                 drawn_at(l[r], int(token[r]), u, T[r], keep[r])
+
+
+@pytest.mark.parametrize("V,tail", [(160000, -31.5), (1 << 22, -28.5), (1 << 22, -27.0)])
+def test_borders_hold_within_what_the_sums_leave_out(V, tail):
+    """Tails of tokens that each weigh less than half a unit are left out of the sums by token: a share of top-p, and
+    a random number, are met within V 2^-(F + 1) of the sum, at four million tokens more than a step of either."""
+    kda = need_gpu()
+    case(f"borders V={V} {tail}")
+    x = torch.full((6, V), tail, device="cuda")
+    x[:, [3, V // 2, V - 5]] = torch.tensor([0.0, -0.5, -1.0], device="cuda")
+    l = np_(x[0]).astype(np.float64)
+    w = np.exp((l - l.max()).astype(np.longdouble))
+    w = w / w.sum()
+    order = np.lexsort((np.arange(V), -l))
+    share = np.cumsum(w[order])
+    p = [1 - 2.0 ** -24, 1 - 2.0 ** -23, 1 - 2.0 ** -20, 0.984375, 0.5, 1.0]
+    u = [1 - 2.0 ** -24, 1 - 2.0 ** -22, 1.0, 1 - 2.0 ** -19, 0.0, 0.25]
+    for top_p, min_p in ((p, None), (None, [1e-30] * 6), (p, [1e-30] * 6), (None, None)):
+        token, probs = kda.kda_sample(x, gpu(u), None, None, gpu(top_p), gpu(min_p), probs=True)
+        torch.cuda.synchronize()
+        for r in range(6):
+            keep = np_(probs[r]) > 0
+            n = int(keep.sum())
+            assert keep[order[:n]].all()        # the first n
+            if top_p is not None and p[r] < 1:
+                assert share[n - 1] >= p[r] - bound(V) and (n == 1 or share[n - 2] < p[r] + bound(V)), (r, n)
+            else:
+                assert n == V
+            drawn_at(l, int(token[r]), u[r], 1.0, keep)
