@@ -5,12 +5,14 @@
 // One wavefront per head.  The two reads of the state, S^T k for the update
 // and S^T q for the output, are two vectors against 128 x 128 codes, taken as
 // whole numbers: each vector (times decay and scale, per key channel) becomes
-// a 31-bit fixed-point number under a power of two of its own, split into four
-// signed 8-bit digits, and the digits are rows of the 8-bit matrix
-// instruction, whose other operand is the codes as they lie in memory.  So no
-// code is converted or multiplied by the vector unit, the sums are exact, and
-// what is rounded is each vector's entry, to 2^-31 of the vector's largest,
-// and the sum of the four digits' results, to 24 bits.
+// a 62-bit fixed-point number under a power of two of its own, split into two
+// halves of four signed 8-bit digits, and the sixteen digits are the rows of the
+// 8-bit matrix instruction, whose other operand is the codes as they lie in memory.
+// So no code is converted or multiplied by the vector unit, and the sums are exact;
+// what is rounded is each half's result, to 24 bits.  Entries of less than 2^-38 of
+// their vector's largest have bits beyond the 62 and a second round takes them (rarely:
+// the products alone are done again), so that an output that the largest channels'
+// codes leave alone has all its bits, as fp32 products would give it.
 // Bounded by memory: 256 x 96 states with windows of 4 tokens take 106 us for 0.53 GB,
 // 5.0 TB/s (reads alone, laid out as the codes are, reach 6.1); a step of fp32 states
 // moves 3.2 GB.  The window's three new rows, 19 MB in lines of their own, cost 13 us of
@@ -83,30 +85,36 @@ __device__ __forceinline__ float sum64(float x) {
 }
 
 struct WaveLds {
-    uint8_t digit[8 * kDigitLd];   // rows 0..3: digits of the key's vector, lowest first; 4..7: the query's
-    float read[2][kD];             // what the two vectors read
+    uint8_t digit[16 * kDigitLd];  // four rows of digits, lowest first, of the key's upper half, its lower, the query's two
+    float read[4][kD];             // what they read
 };
 
 __device__ __forceinline__ void fence() { __builtin_amdgcn_fence(__ATOMIC_SEQ_CST, "wavefront"); }
 
-// the two entries of this lane as digits into LDS; the exponent to multiply the
-// result by.  A vector that is not finite makes NaN of `read`, what its result
-// is added to.
-__device__ __forceinline__ int to_digits(floatx2 x, uint8_t* row0, int lane, floatx2& read) {
+// x as multiples of its vector's unit, of which its largest has 2^29 to 2^30; the exponent
+// of the unit.  A vector that is not finite makes NaN of `read`, what its result is added to.
+__device__ __forceinline__ int to_units(floatx2& x, floatx2& read) {
     const uint32_t top = wave_max(max(bits(x[0]) & 0x7fffffffu, bits(x[1]) & 0x7fffffffu));
-    const int up = 29 + 127 - (int)(top >> 23);   // |x| 2^up < 2^30
+    const int up = 29 + 127 - (int)(top >> 23);
+    if (top >= 0x7f800000u) read = floatx2{__builtin_nanf(""), __builtin_nanf("")};
+#pragma unroll
+    for (int e = 0; e < 2; ++e) x[e] = top >= 0x7f800000u ? 0.f : __builtin_amdgcn_ldexpf(x[e], up);
+    return -up;
+}
+// the whole parts of the lane's two entries, |x| <= 2^30, as digits into LDS; x
+// becomes what is left, in units of 2^-31 (exact, as the difference is)
+__device__ __forceinline__ void to_digits(floatx2& x, uint8_t* row0, int lane) {
     uint32_t d[2];
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-        const int v = (int)__builtin_rintf(__builtin_amdgcn_ldexpf(x[e], up));
-        d[e] = ((uint32_t)v + 0x00808080u) ^ 0x00808080u;   // signed digits of 8 bits
+        const float v = __builtin_rintf(x[e]);
+        d[e] = ((uint32_t)(int)v + 0x00808080u) ^ 0x00808080u;   // signed digits of 8 bits
+        x[e] = (x[e] - v) * 2147483648.f;
     }
 #pragma unroll
     for (int r = 0; r < 4; ++r)
         *reinterpret_cast<uint16_t*>(row0 + r * kDigitLd + 2 * lane) =
             (uint16_t)__builtin_amdgcn_perm(d[1], d[0], 0x0c0c0400u + 0x0101u * r);
-    if (top >= 0x7f800000u) read = floatx2{__builtin_nanf(""), __builtin_nanf("")};
-    return -up;
 }
 
 template <typename T>
@@ -168,25 +176,43 @@ __global__ __launch_bounds__(256, 4) void cache_decode_kernel(CacheDecodeArgs a)
         }
     }
     const floatx2 held{scale[0] * decay(gone[0]), scale[1] * decay(gone[1])};
-    const int ek = to_digits(k * held, lds.digit, lane, by_k);
-    const int eq = to_digits(q * held, lds.digit + 4 * kDigitLd, lane, by_q);
-    fence();
-    intx4 d[2];
+    floatx2 xk = k * held, xq = q * held, sk{0.f, 0.f}, sq{0.f, 0.f};
+    const int ek = to_units(xk, by_k), eq = to_units(xq, by_q);
+    float step = 1.f;
+    // (the first round on its own: 256 x 96 states 106.2 us, 107.4 by a loop around it)
+    auto round = [&]() {
+        to_digits(xk, lds.digit, lane);
+        to_digits(xk, lds.digit + 4 * kDigitLd, lane);
+        to_digits(xq, lds.digit + 8 * kDigitLd, lane);
+        to_digits(xq, lds.digit + 12 * kDigitLd, lane);
+        fence();
+        intx4 d[2];
 #pragma unroll
-    for (int s = 0; s < 2; ++s)
-        d[s] = *reinterpret_cast<const intx4*>(lds.digit + (l16 & 7) * kDigitLd + 16 * g + 64 * s);
+        for (int s = 0; s < 2; ++s)
+            d[s] = *reinterpret_cast<const intx4*>(lds.digit + l16 * kDigitLd + 16 * g + 64 * s);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-        intx4 x{0, 0, 0, 0};
-        x = __builtin_amdgcn_mfma_i32_16x16x64_i8(d[0], c[t][0], x, 0, 0, 0);
-        x = __builtin_amdgcn_mfma_i32_16x16x64_i8(d[1], c[t][1], x, 0, 0, 0);
-        // lanes of group 0: the key's four digits at column l16, of group 1 the query's
-        const float y = __builtin_fmaf((float)(x[3] * 256 + x[2]), 65536.f, (float)(x[1] * 256 + x[0]));
-        if (g < 2) lds.read[g][16 * t + l16] = y;
-    }
-    fence();
-    floatx2 sk = *reinterpret_cast<const floatx2*>(&lds.read[0][2 * lane]);
-    floatx2 sq = *reinterpret_cast<const floatx2*>(&lds.read[1][2 * lane]);
+        for (int t = 0; t < 8; ++t) {
+            intx4 x{0, 0, 0, 0};
+            x = __builtin_amdgcn_mfma_i32_16x16x64_i8(d[0], c[t][0], x, 0, 0, 0);
+            x = __builtin_amdgcn_mfma_i32_16x16x64_i8(d[1], c[t][1], x, 0, 0, 0);
+            // lanes of group g: the four digits of half g at column l16
+            const float y = __builtin_fmaf((float)(x[3] * 256 + x[2]), 65536.f, (float)(x[1] * 256 + x[0]));
+            lds.read[g][16 * t + l16] = y;
+        }
+        fence();
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            sk[e] += step * __builtin_fmaf(lds.read[1][2 * lane + e], 0x1p-31f, lds.read[0][2 * lane + e]);
+            sq[e] += step * __builtin_fmaf(lds.read[3][2 * lane + e], 0x1p-31f, lds.read[2][2 * lane + e]);
+        }
+        fence();
+        step *= 0x1p-62f;
+        // (what is left loses 62 bits a round, and fp32 ends at 2^-149)
+        return __ballot(xk[0] != 0.f || xk[1] != 0.f || xq[0] != 0.f || xq[1] != 0.f) != 0;
+    };
+    bool more = round();
+#pragma unroll 1
+    while (__builtin_expect(more, 0)) more = round();
     const float kq = sum64(k[0] * q[0] + k[1] * q[1]);
     pair u, o;
 #pragma unroll

@@ -614,8 +614,10 @@ kda_status kda_cache_load(const int8_t* codes, const float* scale, const int32_t
  *   n_win           : [B] int32, required; a sequence whose n_win lies outside
  *                     [0, W) is idle: nothing of it is read or written
  *   o               : [B, H, Dv]  dt
- * The reads of the state are exact sums of products of the codes with 31-bit
- * vectors; a NaN or infinity in q makes NaN of the head's outputs, one in k or
+ * The reads of the state are sums over the key channels that are off by fp32
+ * roundings of their own terms: k and q, times decay and scale in fp32, meet the codes
+ * as whole numbers, with all their bits however much larger another channel is (down to
+ * 2^-150 of the largest).  A NaN or infinity in q makes NaN of the head's outputs, one in k or
  * log_alpha of its outputs and its update.  Any overlap of o or the window
  * with another buffer is KDA_ERR_ALIAS.
  */

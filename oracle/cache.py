@@ -54,14 +54,10 @@ def decode(q, k, v, la, beta, codes, scale, wk, wla, wu, n):
     S, off = state(codes, scale, wk, wla, wu, n)
     d = np.exp(la)[:, None]
     S, off = d * S, d * (off + EPS * np.abs(S) * ((n + 2) * np.abs(la) + 4)[:, None])
-    c = np.abs(values(codes, np.ones(128, np.float32)))
-    whole = np.exp(np.sum(wla[:n], 0) + la) * np.asarray(scale, np.float64)
 
     def read(x):
-        # a vector times 128 terms: a sum of as many roundings as its depth, 16 at the most, and the
-        # vector's entries to 2^-30 of its largest
-        fixed = 2.0 ** -30 * np.abs(x * whole).max() * c.sum(0)
-        return x @ S, np.abs(x) @ off + 16 * EPS * (np.abs(x) @ np.abs(S)) + fixed
+        # a vector times 128 terms: a sum of as many roundings as its depth, 16 at the most
+        return x @ S, np.abs(x) @ off + 16 * EPS * (np.abs(x) @ np.abs(S))
 
     sk, bk = read(k)
     u = beta * (v - sk)
