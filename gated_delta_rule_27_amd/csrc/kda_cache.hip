@@ -15,8 +15,7 @@
 // through the workgroup.
 #include "kda.h"
 #include "kda_cache.h"
-#include "kda_device.h"
-#include "kda_tree_device.h"
+#include "kda_cache_device.h"
 
 namespace kda {
 
@@ -37,9 +36,6 @@ struct Place {
     __device__ __forceinline__ int row(int t) const { return 32 * wave + 8 * t + 4 * half; }
 };
 typedef floatx4 State[4][4];   // [block][row], four columns
-
-// e^x of a sum of log alpha (exp_f32 takes arguments that are finite)
-__device__ __forceinline__ float decay(float x) { return exp_f32(x < -120.f ? -120.f : x, 0.f); }
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __builtin_bit_cast(uint32_t, x) & 0x7fffffffu; }
 // largest of 16, of 32 lanes (the magnitudes' bits: a NaN is larger than anything)
@@ -168,22 +164,22 @@ __device__ __forceinline__ void stage(ReadLds& lds, WindowLds<T, kMost>& wl, con
     __syncthreads();
     // a key channel's later tokens in one thread, its earlier ones in another
     const int half = most / 2;
-    float g = 0.f;
+    LogDecay g;
     if (threadIdx.x < kD) {
 #pragma unroll 2
         for (int t = most - 1; t >= half; --t) {
-            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
-            g += to_f32(wl.raw[1][t][i]);
+            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * g.decay();
+            g.add(to_f32(wl.raw[1][t][i]));
         }
     } else {
 #pragma unroll 2
-        for (int t = most - 1; t >= half; --t) g += to_f32(wl.raw[1][t][i]);
+        for (int t = most - 1; t >= half; --t) g.add(to_f32(wl.raw[1][t][i]));
 #pragma unroll 2
         for (int t = half - 1; t >= 0; --t) {
-            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * decay(g);
-            g += to_f32(wl.raw[1][t][i]);
+            wl.k(t)[i] = to_f32(wl.raw[0][t][i]) * g.decay();
+            g.add(to_f32(wl.raw[1][t][i]));
         }
-        lds.row[i] = sc * decay(g);
+        lds.row[i] = sc * g.decay();
     }
     __syncthreads();
 }

@@ -21,8 +21,7 @@
 // the other in a wavefront.
 #include "kda.h"
 #include "kda_cache.h"
-#include "kda_device.h"
-#include "kda_tree_device.h"
+#include "kda_cache_device.h"
 
 namespace kda {
 
@@ -63,8 +62,6 @@ __device__ __forceinline__ uint32_t wave_max(uint32_t x) {
     const int c = __builtin_amdgcn_readlane((int)x, 32), d = __builtin_amdgcn_readlane((int)x, 48);
     return max(max((uint32_t)a, (uint32_t)b), max((uint32_t)c, (uint32_t)d));
 }
-// e^x of a sum of log alpha (exp_f32 takes arguments that are finite)
-__device__ __forceinline__ float decay(float x) { return exp_f32(x < -120.f ? -120.f : x, 0.f); }
 __device__ __forceinline__ uint32_t bits(float x) { return __builtin_bit_cast(uint32_t, x); }
 
 template <int kCtrl>
@@ -152,7 +149,10 @@ __global__ __launch_bounds__(256, 4) void cache_decode_kernel(CacheDecodeArgs a)
 
     // the window, newest first, kRound tokens at a time: what its updates add to
     // the two reads
-    floatx2 gone = la, by_k{0.f, 0.f}, by_q{0.f, 0.f};
+    floatx2 by_k{0.f, 0.f}, by_q{0.f, 0.f};
+    LogDecay gone[2];
+    gone[0].add(la[0]);
+    gone[1].add(la[1]);
 #pragma unroll 1
     for (int t0 = (n - 1) / kRound * kRound; n > 0 && t0 >= 0; t0 -= kRound) {
         pair kw[kRound], lw[kRound], uw[kRound];
@@ -168,14 +168,15 @@ __global__ __launch_bounds__(256, 4) void cache_decode_kernel(CacheDecodeArgs a)
         for (int t = kRound - 1; t >= 0; --t) {
             if (t0 + t < n) {
                 const floatx2 kt = widen<T>(kw[t]), lt = widen<T>(lw[t]), ut = widen<T>(uw[t]);
-                const float x0 = kt[0] * decay(gone[0]), x1 = kt[1] * decay(gone[1]);
+                const float x0 = kt[0] * gone[0].decay(), x1 = kt[1] * gone[1].decay();
                 by_k += sum64(x0 * k[0] + x1 * k[1]) * ut;
                 by_q += sum64(x0 * q[0] + x1 * q[1]) * ut;
-                gone += lt;
+                gone[0].add(lt[0]);
+                gone[1].add(lt[1]);
             }
         }
     }
-    const floatx2 held{scale[0] * decay(gone[0]), scale[1] * decay(gone[1])};
+    const floatx2 held{scale[0] * gone[0].decay(), scale[1] * gone[1].decay()};
     floatx2 xk = k * held, xq = q * held, sk{0.f, 0.f}, sq{0.f, 0.f};
     const int ek = to_units(xk, by_k), eq = to_units(xq, by_q);
     float step = 1.f;

@@ -37,14 +37,12 @@ def state(codes, scale, k, la, u, n):
     """One head's state after the first n tokens of its window (k, la, u [W,
     128] float64) and the bound of its entries."""
     S = values(codes, scale)
-    # weights: the roundings that a term has seen, times its magnitude.  A decay over tokens of
-    # log alpha l is off by (their number) * |sum of l| + 4 roundings of its exponential
-    terms = [(S, np.zeros(128), 0)]
+    # a decay's sum of log alpha is exact, its exponential off by two steps at the most (four roundings)
+    terms = [S]
     for t in range(n):
-        terms = [(x * np.exp(la[t])[:, None], g + la[t], m + 1) for x, g, m in terms]
-        terms.append((k[t][:, None] * u[t][None, :], np.zeros(128), 0))
-    total = sum(x for x, _, _ in terms)
-    bound = EPS * sum(np.abs(x) * ((m + 1) * np.abs(g) + n + 8)[:, None] for x, g, m in terms)
+        terms = [x * np.exp(la[t])[:, None] for x in terms] + [k[t][:, None] * u[t][None, :]]
+    total = sum(terms)
+    bound = EPS * (n + 8) * sum(np.abs(x) for x in terms)
     return total, bound
 
 
@@ -53,7 +51,7 @@ def decode(q, k, v, la, beta, codes, scale, wk, wla, wu, n):
     function of the update as it is held that gives the output and its bound."""
     S, off = state(codes, scale, wk, wla, wu, n)
     d = np.exp(la)[:, None]
-    S, off = d * S, d * (off + EPS * np.abs(S) * ((n + 2) * np.abs(la) + 4)[:, None])
+    S, off = d * S, d * (off + 4 * EPS * np.abs(S))
 
     def read(x):
         # a vector times 128 terms: a sum of as many roundings as its depth, 16 at the most
