@@ -617,9 +617,10 @@ kda_status kda_cache_load(const int8_t* codes, const float* scale, const int32_t
  * The reads of the state are sums over the key channels that are off by fp32
  * roundings of their own terms: k and q, times decay and scale in fp32, meet the codes
  * as whole numbers, with all their bits however much larger another channel is (down to
- * 2^-150 of the largest).  A NaN or infinity in q makes NaN of the head's outputs, one in k or
- * log_alpha of its outputs and its update.  Any overlap of o or the window
- * with another buffer is KDA_ERR_ALIAS.
+ * 2^-150 of the largest).  A NaN or infinity in q makes NaN of the head's outputs, one
+ * in k, or a NaN or +infinity in log_alpha, of its outputs and its update; -infinity in
+ * log_alpha, here and in a window, is a decay to 0 and empties the key channel.  Any
+ * overlap of o or the window with another buffer is KDA_ERR_ALIAS.
  */
 kda_status kda_cache_decode(const void* q, const void* k, const void* v,
                             const void* log_alpha, const void* beta,
