@@ -1030,8 +1030,8 @@ def kda_sample(logits, u=None, temperature=None, top_k=None, top_p=None, min_p=N
     temperature 0 keeps the first alone.  probs: a tensor like logits for the
     probabilities that are left (what kda_tree_accept takes), True to make one,
     or None.  Returns (token int32 [...]: the smallest kept index at which the
-    running sum of the kept probabilities passes u, -1 for a row without a
-    finite logit, or None without u; probs or None)."""
+    running sum of the kept probabilities passes u, -1 for a row whose logits
+    are all -infinity or NaN, or None without u; probs or None)."""
     torch = _torch()
     if not isinstance(logits, torch.Tensor) or logits.dim() < 1:
         raise TypeError("logits must be a torch.Tensor [..., V]")

@@ -136,3 +136,25 @@ def test_borders_hold_within_what_the_sums_leave_out(V, tail):
             else:
                 assert n == V
             drawn_at(l, int(token[r]), u[r], 1.0, keep)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("V", [5, 3000, 40000])
+def test_rows_without_a_finite_logit(V, dtype):
+    """-1 and no probabilities where every logit is -infinity or NaN; among +infinities one of those."""
+    kda = need_gpu()
+    case(f"rows without a finite logit V={V} {dtype}")
+    x = torch.full((4, V), -INF, device="cuda")
+    x[1, ::2] = NAN
+    x[2, [V // 2, V - 1]] = INF
+    x[3] = NAN
+    x[3, V // 3] = INF
+    x = x.to(DT[dtype])
+    for ask in ({}, dict(top_k=gpu([2] * 4, torch.int32)), dict(top_p=gpu([0.9] * 4)), dict(min_p=gpu([0.5] * 4)),
+                dict(temperature=gpu([0.0] * 4))):
+        token, probs = kda.kda_sample(x, gpu([0.75] * 4), probs=True, **ask)
+        torch.cuda.synchronize()
+        greedy = "temperature" in ask
+        assert token.tolist() == [-1, -1, V // 2 if greedy else V - 1, V // 3]
+        assert (probs[:2] == 0).all() and (probs.sum(1) == gpu([0.0, 0.0, 1.0, 1.0])).all()
+        assert probs[2, V // 2] == (1.0 if greedy else 0.5) and probs[3, V // 3] == 1.0
