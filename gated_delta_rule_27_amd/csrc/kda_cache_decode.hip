@@ -13,11 +13,11 @@
 // their vector's largest have bits beyond the 62 and a second round takes them (rarely:
 // the products alone are done again), so that an output that the largest channels'
 // codes leave alone has all its bits, as fp32 products would give it.
-// Bounded by memory: 256 x 96 states with windows of 4 tokens take 106 us for 0.53 GB,
-// 5.0 TB/s (reads alone, laid out as the codes are, reach 6.1); a step of fp32 states
+// Bounded by memory: 256 x 96 states with windows of 4 tokens take 105 us for 0.53 GB,
+// 5.1 TB/s (reads alone, laid out as the codes are, reach 6.1); a step of fp32 states
 // moves 3.2 GB.  The window's three new rows, 19 MB in lines of their own, cost 13 us of
-// it.  One sequence: 5.4 us, a launch and the chain of loads, digits and products.
-// 23 x 31 states with 6 fp32 tokens on average: 11.4 us, the window's tokens one after
+// it.  One sequence: 5.6 us, a launch and the chain of loads, digits and products.
+// 23 x 31 states with 6 fp32 tokens on average: 11.0 us, the window's tokens one after
 // the other in a wavefront.
 #include "kda.h"
 #include "kda_cache.h"

@@ -25,9 +25,9 @@
 // rounding of a running sum must not move.
 // What bounds it, 256 x 160,000 fp32 (0.16 GB): the first pass HBM, 35 us (4.6 TB/s;
 // 30 without weights); the second the slowest row, which one CU reads: 10 us without a
-// filter, 10 to 30 us where the list holds all that is kept, 65 to 90 us where a nucleus has
+// filter, 10 to 30 us where the list holds all that is kept, 55 to 115 us where a nucleus has
 // thousands of tokens (0.64 MB through one CU, some 25 fp64 and integer instructions a
-// logit).  The third pass, 192 x 50,021 bf16: 10 us (19 MB written, as much read where
+// logit), 205 where in one of many rows the cut is not where some tiles said it was.  The third pass, 192 x 50,021 bf16: 10 us (19 MB written, as much read where
 // something is kept).  One row of 32,000: 18.5 us, three launches' trips to memory and
 // the second one's instructions, fetched as they run.
 #include "kda.h"
@@ -1078,7 +1078,9 @@ __device__ __forceinline__ Kept over_row(int k, bool by_p, double p, double leas
     for (int step = k ? 0 : 1; step < 3; ++step) {
         // (from a quarter of the tiles the place of the cut is off by some hundred tokens, of over a thousand that are
         // collected; beyond 256 tiles by too many.  256 x 160,000 fp32 by top-p 0.5, 0.9, 0.99: 115, 129, 146 us from all
-        // tiles, 97, 111, 124 from a quarter, 92, 106, 198 from an eighth.  Fewer than 32 take no longer than the rest.)
+        // tiles, 97, 111, 124 from a quarter, 92, 106, 198 from an eighth.  Fewer than 32 take no longer than the rest.  Of
+        // logits of deviation 1 by 0.9 some of 256 rows miss, 245 us where all tiles at once take 178; by 0.5 and 0.99 none
+        // does, 149 and 152 where they take 147 and 198.)
         if (step > 0 && !by_p) break;
         if (step == 1 && (k || r.tiles < 32 || r.tiles > 256)) continue;
         const bool by_count = step == 0;
